@@ -326,6 +326,90 @@ gk_status gk_cascade_suffix(gk_pool* pool, void* stream, int32_t layer, const gk
 gk_status gk_cascade_merge(gk_pool* pool, void* stream, int32_t layer, const gk_batch* batch,
                            const gk_plan* plan);
 
+/* ---- one prompt step ------------------------------------------------------- */
+
+/* The new tokens of every request of a step: whole prompts, turns behind a
+ * cached context, or chunks of prompts, of different lengths.  Request r has
+ * n = new_len[r] new tokens, whose rows of q, k, v, out and lse follow those of
+ * request r - 1 (packed; T = the sum of new_len rows), a HOT prefix of
+ * prefix_len[r] tokens and context_len[r] tokens in COLD.  New token i attends
+ * the whole HOT prefix, the COLD tokens and the new tokens 0 .. i, in that order
+ * of positions; n = 0 is allowed (no rows).  The pages leave the prompt's own
+ * attention to the engine ("Paged KV cache", How it works, step 1 only writes
+ * its K/V; GraniKV Section 3.2 fills the HOT slab from it). */
+typedef struct gk_prompt_batch {
+  int32_t num_requests;           /* B */
+  int32_t max_blocks;             /* row stride of d_block_table */
+  const int32_t* new_len;         /* host [B] */
+  const int64_t* prefix_hot_base; /* host [B]: HOT base, -1 = none; NULL = none for any request */
+  const int32_t* prefix_len;      /* host [B]: 0 when the base is -1; NULL exactly when the base is NULL */
+  const int32_t* context_len;     /* host [B]: earlier tokens of the request in COLD; NULL = 0 for all */
+  const int32_t* d_block_table;   /* device [B][max_blocks]; read where context_len > 0, else may be NULL */
+  const void* d_q;                /* device bf16 [T][Hq][d], 16-byte aligned, like the next three */
+  const void* d_k;                /* device bf16 [T][Hkv][d]: the new tokens' keys (gk_append_kv's input) */
+  const void* d_v;                /* device bf16 [T][Hkv][d] */
+  void* d_out;                    /* device bf16 [T][Hq][d] */
+  float* d_lse;                   /* device fp32 [T][Hq], natural log; may be NULL */
+  int64_t q_stride;               /* elements from one token's row to the next (views of a fused q k v */
+  int64_t k_stride;               /* projection): a multiple of 8, at least heads * d; 0 = packed rows */
+  int64_t v_stride;
+  int64_t out_stride;
+} gk_prompt_batch;
+
+typedef struct gk_prompt_plan gk_prompt_plan;
+
+typedef struct gk_prompt_plan_summary {
+  int64_t tokens;                 /* T */
+  int64_t flops;                  /* 4 * d * Hq * (visible row-key pairs per query head), per layer */
+  int64_t bytes;                  /* per layer: q, k, v, out and lse once, each HOT prefix once, COLD tokens */
+  int32_t items;                  /* work items: two 128-row query tiles x one KV head x a range of key tiles */
+  int32_t ctas;                   /* CTAs that run them */
+  int32_t stacked_requests;       /* requests whose HOT keys are read by items that stack several requests' rows */
+  int32_t partials;               /* partial states the join combines (0: no join launch) */
+  int32_t max_pieces;             /* most items over one block of rows' keys */
+  int32_t max_cta_tiles;          /* 128-key tiles of the CTA with the most */
+} gk_prompt_plan_summary;
+
+/* Plan a prompt step: cut the rows into items, balance them over the SMs by their
+ * key tiles (long key ranges of steps with few rows are split and joined by
+ * log-sum-exp, GraniKV Eq. 1; neighbouring requests with the same HOT prefix and
+ * few rows each are stacked over it, Section 2.3).  Depends only on the host
+ * arrays, so one plan serves every layer and may be replayed from a captured
+ * graph.  Tables and partial states are owned by the plan; calls that use a plan
+ * must be ordered on one stream.  GK_ERR_INVALID for a negative length, a HOT
+ * prefix that is not live with that length, a context longer than its
+ * block-table row, or more than 2^31 - 1 tokens.  Allocates device memory: not
+ * while the stream is capturing. */
+gk_status gk_prompt_plan_build(gk_pool* pool, const gk_prompt_batch* batch, void* stream, gk_prompt_plan** out);
+/* Re-plan for the next step, reusing the buffers; on the stream of the plan's earlier work. */
+gk_status gk_prompt_plan_update(gk_prompt_plan* plan, const gk_prompt_batch* batch, void* stream);
+/* Frees the plan's buffers; its enqueued work must have completed. */
+void gk_prompt_plan_destroy(gk_prompt_plan* plan);
+gk_status gk_prompt_plan_info(const gk_prompt_plan* plan, gk_prompt_plan_summary* out);
+/* The plan's work list (its host copy).  The counts come first: *n_ctas CTAs and
+ * *n_items items.  Then, when begin and items are not NULL, begin[0 .. n_ctas]
+ * receives the offsets of each CTA's items and items[8 * i .. 8 * i + 7] item i:
+ * request (the first of a stacked run), tokens of the stacked run (0: an item of
+ * one request), KV head, first token (of the request or run; an item covers
+ * 2 * floor(128 * Hkv / Hq)), first key tile, key tiles (128 keys each: the HOT
+ * prefix's, then COLD's, then the new tokens'), partial state (-1: the output),
+ * and the HOT prefix's tiles.  Host only. */
+gk_status gk_prompt_plan_items(const gk_prompt_plan* plan, int32_t* n_ctas, int32_t* n_items, int32_t* begin,
+                               int32_t* items);
+/* Attention of one layer of a planned prompt step: with s_j = q.k_j / sqrt(d) over
+ * the keys the row attends, out = sum_j e^(s_j) v_j / Z and lse = ln Z, Z = sum_j
+ * e^(s_j).  Products and sums are held in fp32; the weights are rounded to bf16
+ * before the product with V, the output to bf16 at the end.  Keys a row does not
+ * attend contribute nothing, whatever their K and V hold (infinities and NaN
+ * included).  Reads COLD through the block table (an out-of-range block id
+ * counts as zero K and V and is reported as GK_ERR_DEVICE_BOUNDS by
+ * gk_device_error()) and does not write the pool: gk_append_kv (or
+ * gk_write_prefix_kv) stores the new tokens, before or after.  The batch's
+ * lengths and HOT bases are the plan's; only its device pointers and strides are
+ * read.  May be captured. */
+gk_status gk_prompt_attn(gk_pool* pool, void* stream, int32_t layer, const gk_prompt_batch* batch,
+                         const gk_prompt_plan* plan);
+
 /* ---- per-step dispatch (GraniKV Section 3.6, Eq. 2) -------------------------- */
 
 typedef struct gk_cost_model {

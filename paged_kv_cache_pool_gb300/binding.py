@@ -69,6 +69,19 @@ class gk_cost_model(ctypes.Structure):
                 ("split_tensor_us", c_dbl)]
 
 
+class gk_prompt_batch(ctypes.Structure):
+    _fields_ = [("num_requests", c_i32), ("max_blocks", c_i32), ("new_len", ctypes.POINTER(c_i32)),
+                ("prefix_hot_base", ctypes.POINTER(c_i64)), ("prefix_len", ctypes.POINTER(c_i32)),
+                ("context_len", ctypes.POINTER(c_i32)), ("d_block_table", c_vp), ("d_q", c_vp), ("d_k", c_vp),
+                ("d_v", c_vp), ("d_out", c_vp), ("d_lse", c_vp), ("q_stride", c_i64), ("k_stride", c_i64),
+                ("v_stride", c_i64), ("out_stride", c_i64)]
+
+
+class gk_prompt_plan_summary(ctypes.Structure):
+    _fields_ = [("tokens", c_i64), ("flops", c_i64), ("bytes", c_i64), ("items", c_i32), ("ctas", c_i32),
+                ("stacked_requests", c_i32), ("partials", c_i32), ("max_pieces", c_i32), ("max_cta_tiles", c_i32)]
+
+
 P = ctypes.POINTER
 _SIGS = {
     "gk_pool_create": (c_i32, [P(gk_pool_config), P(c_vp)]),
@@ -106,6 +119,12 @@ _SIGS = {
     "gk_cascade_prefix": (c_i32, [c_vp, c_vp, c_i32, P(gk_batch), c_vp]),
     "gk_cascade_suffix": (c_i32, [c_vp, c_vp, c_i32, P(gk_batch), c_vp]),
     "gk_cascade_merge": (c_i32, [c_vp, c_vp, c_i32, P(gk_batch), c_vp]),
+    "gk_prompt_plan_build": (c_i32, [c_vp, P(gk_prompt_batch), c_vp, P(c_vp)]),
+    "gk_prompt_plan_update": (c_i32, [c_vp, P(gk_prompt_batch), c_vp]),
+    "gk_prompt_plan_destroy": (None, [c_vp]),
+    "gk_prompt_plan_info": (c_i32, [c_vp, P(gk_prompt_plan_summary)]),
+    "gk_prompt_plan_items": (c_i32, [c_vp, P(c_i32), P(c_i32), c_vp, c_vp]),
+    "gk_prompt_attn": (c_i32, [c_vp, c_vp, c_i32, P(gk_prompt_batch), c_vp]),
     "gk_dispatch": (c_i32, [c_vp, c_vp, P(c_i32), P(c_dbl), P(c_dbl)]),
     "gk_cost_model_set": (c_i32, [c_vp, P(gk_cost_model)]),
     "gk_cost_model_get": (c_i32, [c_vp, P(gk_cost_model)]),
@@ -421,6 +440,92 @@ def gk_cascade_suffix(pool, stream, layer, batch, plan):
 
 def gk_cascade_merge(pool, stream, layer, batch, plan):
     _check(lib().gk_cascade_merge(pool, _stream(stream), layer, ctypes.byref(batch.c), plan), pool)
+
+
+# ---- prompt step ---------------------------------------------------------------------
+def _token_stride(x, tokens, what):
+    """Elements from one token of x (bf16 [tokens, heads, d]) to the next; 0 (packed) for an address or one token."""
+    if x is None or isinstance(x, int):
+        return 0
+    n, heads, d = x.shape
+    if n != tokens or x.element_size() != 2 or (n and (x.stride(2) != 1 or (heads > 1 and x.stride(1) != d))):
+        raise ValueError(f"{what} must be bf16 [{tokens}, heads, d] with a token's heads and channels contiguous")
+    return x.stride(0) if n > 1 else 0
+
+
+class PromptBatch:
+    """Keeps the host arrays of a gk_prompt_batch alive; .set_device() swaps the per-layer device pointers."""
+
+    def __init__(self, new_len, prefix_hot_base=None, prefix_len=None, context_len=None, d_block_table=None,
+                 max_blocks=0):
+        self.new_len = np.ascontiguousarray(new_len, dtype=np.int32)
+        n = len(self.new_len)
+
+        def host(a, t):
+            if a is None:
+                return None
+            a = np.ascontiguousarray(a, dtype=t)
+            if a.shape != (n,):
+                raise ValueError("one entry per request")
+            return a
+        self.prefix_hot_base, self.prefix_len = host(prefix_hot_base, np.int64), host(prefix_len, np.int32)
+        self.context_len = host(context_len, np.int32)
+        self.tokens = int(self.new_len.astype(np.int64).sum())
+        self.c = gk_prompt_batch(n, max_blocks, _i32p(self.new_len),
+                                 None if self.prefix_hot_base is None else _i64p(self.prefix_hot_base),
+                                 None if self.prefix_len is None else _i32p(self.prefix_len),
+                                 None if self.context_len is None else _i32p(self.context_len))
+        self._table = d_block_table
+        self.c.d_block_table = _ptr(d_block_table)
+
+    def set_device(self, d_q, d_k, d_v, d_out, d_lse=None, d_block_table=None, max_blocks=None):
+        """bf16 [T, Hq, d] q and out, [T, Hkv, d] k and v, fp32 [T, Hq] lse: torch tensors
+        (tokens may be strided, as views of a fused projection are) or addresses of packed rows."""
+        c, T = self.c, self.tokens
+        c.q_stride, c.out_stride = _token_stride(d_q, T, "q"), _token_stride(d_out, T, "out")
+        c.k_stride, c.v_stride = _token_stride(d_k, T, "k"), _token_stride(d_v, T, "v")
+        c.d_q, c.d_k, c.d_v, c.d_out, c.d_lse = _ptr(d_q), _ptr(d_k), _ptr(d_v), _ptr(d_out), _ptr(d_lse)
+        if d_block_table is not None:
+            c.d_block_table = _ptr(d_block_table)
+            self._table = d_block_table
+        if max_blocks is not None:
+            c.max_blocks = max_blocks
+        return self
+
+
+def gk_prompt_plan_build(pool, batch, stream=None):
+    out = c_vp()
+    _check(lib().gk_prompt_plan_build(pool, ctypes.byref(batch.c), _stream(stream), ctypes.byref(out)), pool)
+    return out.value
+
+
+def gk_prompt_plan_update(pool, plan, batch, stream=None):
+    _check(lib().gk_prompt_plan_update(plan, ctypes.byref(batch.c), _stream(stream)), pool)
+
+
+def gk_prompt_plan_destroy(plan):
+    lib().gk_prompt_plan_destroy(plan)
+
+
+def gk_prompt_plan_info(plan):
+    s = gk_prompt_plan_summary()
+    _check(lib().gk_prompt_plan_info(plan, ctypes.byref(s)))
+    return {name: getattr(s, name) for name, _ in gk_prompt_plan_summary._fields_}
+
+
+def gk_prompt_plan_items(plan):
+    """(begin [n_ctas + 1], items [n_items, 8] = request, run tokens, head, first token, first tile, tiles, partial, HOT tiles)."""
+    n_ctas, n_items = c_i32(), c_i32()
+    _check(lib().gk_prompt_plan_items(plan, ctypes.byref(n_ctas), ctypes.byref(n_items), None, None))
+    begin = np.zeros(n_ctas.value + 1, dtype=np.int32)
+    items = np.zeros((n_items.value, 8), dtype=np.int32)
+    _check(lib().gk_prompt_plan_items(plan, ctypes.byref(n_ctas), ctypes.byref(n_items), begin.ctypes.data_as(c_vp),
+                                      items.ctypes.data_as(c_vp)))
+    return begin, items
+
+
+def gk_prompt_attn(pool, stream, layer, batch, plan):
+    _check(lib().gk_prompt_attn(pool, _stream(stream), layer, ctypes.byref(batch.c), plan), pool)
 
 
 def gk_dispatch(pool, plan):

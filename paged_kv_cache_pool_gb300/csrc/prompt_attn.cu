@@ -1,0 +1,809 @@
+// Prompt attention: causal attention of packed new tokens over their request's
+// HOT prefix, its COLD tokens and themselves, on 5th-generation tensor cores.
+//
+// For request r with Lp HOT, c COLD and n new tokens, token i and query head h
+// (KV head h / g), over the keys HOT 0..Lp-1, COLD 0..c-1, new 0..i:
+//   s_j = q.k_j / sqrt(d),  m = max_j s_j,  Z = sum_j e^(s_j - m),
+//   O = sum_j e^(s_j - m) v_j / Z,  LSE = m + ln Z.
+// 4 d flop per (row, key) against 4 d / g bytes per key and 256 rows, so any
+// prompt of more than a few tokens is bound by the tensor cores, not by HBM.
+//
+// One work item = one KV head x 2 * tpt consecutive tokens of one request (tpt =
+// floor(128 / g); the g query heads of a token are g consecutive rows, so an item
+// is two 128-row Q tiles) x a range of 128-key tiles.  Keys come in tiles of one
+// source each: HOT tiles (2D tensor map over the whole HOT pool), COLD tiles
+// (rows gathered through the block table by two warps with 16-byte cp.async),
+// then tiles of new tokens (3D tensor maps over the caller's packed tensors).
+// S_i = Q_i K^T and O_i += P_i V accumulate in tensor memory (512 columns: S_0
+// S_1 O_0 O_1; P_i overwrites S_i as bf16), softmax warpgroup i owns Q tile i,
+// one thread per row, and the MMA thread alternates PV_0(j), S_0(j+1), PV_1(j),
+// S_1(j+1), so that one tile's softmax runs under the other tile's products.
+// P is rounded to bf16 (half a step, 2^-9 to 2^-8 of the value) because V is
+// bf16 and both operands of the product have one type; the row sum adds the
+// unrounded fp32 values.  m is only raised when a row's maximum grows by more
+// than 2^8, which changes neither O nor LSE beyond fp32 rounding.
+//
+// CTAs are persistent (one per SM: 512 tensor-memory columns and 224 KB of
+// shared memory) and run the lists of items that the plan balanced.  K and V tiles
+// share one ring of stages, and the loads of the next item start while the
+// softmax of the last one ends.
+//
+// Masked keys.  Scores are masked by selection, so whatever K holds in a masked
+// place does no harm; the product P V, though, would turn a masked 0 times an
+// infinity or NaN in V into NaN.  So V tiles with masked places (the end of a HOT
+// prefix, the diagonal and the end of the new tokens) pass through the two
+// gather warps, which zero the rows past the end (another request's tokens)
+// and rows that hold an infinity or NaN and are hidden from some row of
+// the item; the rows that do see such a key add its term in the epilogue
+// (add_hidden_values, never taken for finite values).
+//
+// Warp roles (384 threads): 0 TMA, 1 MMA and tensor memory, 2-3 gather and
+// scan, 4-7 and 8-11 softmax of Q tiles 0 and 1.
+#include <cuda.h>
+
+#include <cmath>
+
+#include "prefix_body.cuh"
+#include "prompt.h"
+
+namespace gk {
+namespace prompt {
+
+using prefix::BM;
+using prefix::BN;
+using prefix::idesc;
+using prefix::kRegionKV;
+using prefix::kRegionQ;
+using prefix::kTmemCols;
+using prefix::sdesc;
+using prefix::tc_mma_ts;
+using prefix::wait_or_abort;
+
+constexpr int kThreads = 384;
+constexpr int kHelperThreads = 64;
+constexpr int kHelperBar = 1;     // named barrier of the gather and scan warps
+
+struct Params {
+  CUtensorMap tq, tk, tv;         // the call's packed tensors
+  CUtensorMap thk, thv;           // the HOT pool
+  const PromptReqDev* reqs;
+  const PromptItemDev* items;
+  const int32_t* cta_begin;       // [gridDim.x + 1]
+  const int32_t* block_table;
+  const uint16_t *cold_k, *cold_v;
+  const uint16_t *q, *k, *v;      // add_hidden_values only
+  uint16_t* out;
+  float* lse;
+  float* part_o;                  // [entries][256][D]
+  float* part_l;                  // [entries][256], log2
+  int64_t q_stride, k_stride, v_stride, out_stride;
+  int64_t cold_slots;
+  int64_t cold_blocks;
+  int32_t page, max_blocks;
+  int32_t Hq, Hkv, G, tpt, layer;
+  int32_t* err;
+  float scale_log2;               // log2(e) / sqrt(d)
+};
+
+template <int D>
+struct Layout {
+  static constexpr int NST = D == 128 ? 5 : 8;           // K/V tiles in the ring
+  static constexpr uint32_t kTile = BN * D * 2;
+  static constexpr uint32_t kQTile = BM * D * 2;
+  static constexpr uint32_t kRing = 2 * kQTile;
+  static constexpr uint32_t kData = kRing + NST * kTile;
+};
+
+enum : int {
+  B_QFULL = 0,
+  B_QEMPTY = 1,
+  B_SFULL = 2,                    // one per Q tile, also the next two
+  B_PFULL = 4,
+  B_OFULL = 6,
+  B_FINAL = 8,
+  B_RFULL = 9,                    // 8 each
+  B_REMPTY = 17,
+  B_RSCAN = 25,
+  B_COUNT = 33
+};
+constexpr uint32_t kCtlTmemSlot = B_COUNT * 8;
+constexpr uint32_t kCtlAbort = kCtlTmemSlot + 4;
+constexpr uint32_t kCtlHidden = kCtlAbort + 4;   // an infinity or NaN was hidden in this CTA's V tiles
+constexpr uint32_t kCtlBytes = 512;
+
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* tmap, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          dst),
+      "l"(tmap), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+// 16-byte copy, or 16 zero bytes when !valid (the source is then not read)
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool valid) {
+  const uint32_t n = valid ? 16u : 0u;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait_group() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// ring position: stage and phase parity of the current element
+template <int NST>
+struct Ring {
+  int st = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void next() {
+    if (++st == NST) {
+      st = 0;
+      ph ^= 1u;
+    }
+  }
+};
+
+// key tiles of Q tile i of an item, counted from the item's first
+__device__ __forceinline__ int tile_count(const PromptItemDev& it, const PromptReqDev& rq, int tpt, int i) {
+  const int a = it.tok0 + i * tpt;
+  if (a >= rq.n) return 0;
+  const int last = min(rq.n, a + tpt) - 1;
+  const int total = rq.nt_hot + rq.nt_cold + last / BN + 1;
+  return max(0, min(it.tile0 + it.ntile, total) - it.tile0);
+}
+
+// does a V tile hold places that some row of the item must not see?
+__device__ __forceinline__ bool scanned(const PromptItemDev& it, const PromptReqDev& rq, int t) {
+  if (t < rq.nt_hot) return (t + 1) * BN > rq.lp;
+  return (t - rq.nt_hot - rq.nt_cold + 1) * BN - 1 > it.tok0;
+}
+
+// The terms of new keys in (tok0, tk] whose V row holds an infinity or NaN: those
+// rows were zeroed in shared memory because other rows of the item must not see
+// them.  p_j v_j is added to O (tensor memory) for the rows that do.
+template <int D>
+__device__ __noinline__ void add_hidden_values(const Params& p, const PromptItemDev it, const PromptReqDev rq, int tk,
+                                               int qh, bool valid, float m, uint32_t tO) {
+  const int hi = valid ? tk : -1;
+  const int top = __reduce_max_sync(0xffffffffu, hi);
+  for (int j = it.tok0 + 1; j <= top; ++j) {
+    const int tile = j / BN + rq.nt_hot + rq.nt_cold;
+    if (tile < it.tile0 || tile >= it.tile0 + it.ntile) continue;
+    const uint16_t* vr = p.v + (int64_t)(rq.t0 + j) * p.v_stride + it.head * D;
+    bool bad = false;
+    for (int c = 0; c < D; ++c) bad |= (vr[c] & 0x7F80) == 0x7F80;
+    if (!bad) continue;   // warp-uniform: every lane read the same row
+    float w = 0.f;
+    if (j <= hi) {
+      const uint16_t* qr = p.q + (int64_t)(rq.t0 + tk) * p.q_stride + qh * D;
+      const uint16_t* kr = p.k + (int64_t)(rq.t0 + j) * p.k_stride + it.head * D;
+      float s = 0.f;
+      for (int c = 0; c < D; ++c) s = fmaf(bf_lo(qr[c]), bf_lo(kr[c]), s);
+      w = ex2(s * p.scale_log2 - m);
+    }
+    for (int c0 = 0; c0 < D; c0 += 32) {
+      float o[32];
+      tmem_ld32(tO + c0, o);
+      tc_wait_ld();
+      if (j <= hi)
+        for (int e = 0; e < 32; ++e) o[e] = fmaf(w, bf_lo(vr[c0 + e]), o[e]);
+      __syncwarp();
+      tmem_st32(tO + c0, o);
+      tc_wait_st();
+    }
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_constant__ Params p) {
+  using Lay = Layout<D>;
+  constexpr int NST = Lay::NST;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  const uint32_t ctl = base + Lay::kData;
+  uint8_t* ctl_ptr = smem_raw + (ctl - raw);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(ctl_ptr + kCtlAbort);
+  volatile int* hidden_flag = reinterpret_cast<volatile int*>(ctl_ptr + kCtlHidden);
+  auto bar = [&](int i) { return ctl + 8u * (uint32_t)i; };
+  const uint32_t sQ = base, sR = base + Lay::kRing;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  griddep_launch_dependents();
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
+    *hidden_flag = 0;
+    mbar_init(bar(B_QFULL), 1);
+    mbar_init(bar(B_QEMPTY), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(B_SFULL + i), 1);
+      mbar_init(bar(B_PFULL + i), 128);
+      mbar_init(bar(B_OFULL + i), 1);
+    }
+    mbar_init(bar(B_FINAL), 1);
+    for (int s = 0; s < NST; ++s) {
+      mbar_init(bar(B_RFULL + s), 1);
+      mbar_init(bar(B_REMPTY + s), 1);
+      mbar_init(bar(B_RSCAN + s), 1);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(ctl + kCtlTmemSlot, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(ctl_ptr + kCtlTmemSlot);
+  griddep_wait();
+  const int i0 = p.cta_begin[blockIdx.x], i1 = p.cta_begin[blockIdx.x + 1];
+  auto tS = [&](int i) { return tmem + (uint32_t)(i * 128); };
+  auto tO = [&](int i) { return tmem + 256u + (uint32_t)(i * 128); };
+
+  if (warp == 0) {
+    // ------------------------------ TMA producer ------------------------------
+    if (lane == 0) {
+      Ring<NST> ring;
+      uint32_t scan_ph = 0;                     // bit s: parity of RSCAN[s]'s current phase
+      uint32_t in_ring = 0, in_scan = 0, full_ph = 0;  // last load of each stage, for the drain below
+      uint32_t qn = 0;
+      bool ok = true;
+      for (int ii = i0; ok && ii < i1; ++ii) {
+        const PromptItemDev it = p.items[ii];
+        const PromptReqDev rq = p.reqs[it.req];
+        const int nctx = rq.nt_hot + rq.nt_cold;
+        auto load = [&](int j, bool is_v) {
+          const int t = it.tile0 + j;
+          const int st = ring.st;
+          const uint32_t ph = ring.ph;
+          ring.next();
+          // waited for whoever fills the stage: a parity wait may not fall a phase behind
+          if (!wait_or_abort(bar(B_REMPTY + st), ph ^ 1u, p.err, abort_flag)) return false;
+          if (t >= rq.nt_hot && t < nctx) return true;       // COLD: the gather warps
+          const bool scan = is_v && scanned(it, rq, t);
+          const uint32_t b = bar((scan ? B_RSCAN : B_RFULL) + st);
+          mbar_arrive_expect_tx(b, Lay::kTile);
+          const uint32_t dst = sR + (uint32_t)st * Lay::kTile;
+          if (t < rq.nt_hot) {
+            const int row = (int)(rq.hot_row + ((int64_t)p.layer * p.Hkv + it.head) * rq.lp + t * BN);
+            for (int h = 0; h < D / 64; ++h) tma_load_2d(dst + h * kRegionKV, is_v ? &p.thv : &p.thk, h * 64, row, b);
+          } else {
+            const int row = rq.t0 + (t - nctx) * BN;
+            for (int h = 0; h < D / 64; ++h)
+              tma_load_3d(dst + h * kRegionKV, is_v ? &p.tv : &p.tk, h * 64, it.head, row, b);
+          }
+          const uint32_t bit = 1u << st;
+          in_ring = scan ? in_ring & ~bit : in_ring | bit;
+          in_scan = scan ? in_scan | bit : in_scan & ~bit;
+          full_ph = (full_ph & ~bit) | (ph << st);
+          if (scan) scan_ph ^= bit;
+          return true;
+        };
+        ok = load(0, false) && load(0, true);
+        if (!ok) break;
+        // the Q tiles, once the last product with the item before has read its own
+        if (!wait_or_abort(bar(B_QEMPTY), (qn & 1u) ^ 1u, p.err, abort_flag)) { ok = false; break; }
+        const bool two = it.tok0 + p.tpt < rq.n;
+        const uint32_t q_bytes = (uint32_t)(p.tpt * p.G) * 128u * (D / 64);
+        mbar_arrive_expect_tx(bar(B_QFULL), two ? 2 * q_bytes : q_bytes);
+        for (int i = 0; i < (two ? 2 : 1); ++i)
+          for (int h = 0; h < D / 64; ++h)
+            tma_load_3d(sQ + i * Lay::kQTile + h * kRegionQ, &p.tq, h * 64, it.head * p.G, rq.t0 + it.tok0 + i * p.tpt,
+                        bar(B_QFULL));
+        ++qn;
+        for (int j = 1; ok && j < it.ntile; ++j) ok = load(j, false) && load(j, true);
+      }
+      if (!ok) {
+        // let the loads already issued land before shared memory goes away
+        for (int s = 0; s < NST; ++s) {
+          if (in_ring >> s & 1u) mbar_wait(bar(B_RFULL + s), full_ph >> s & 1u, nullptr);
+          if (in_scan >> s & 1u) mbar_wait(bar(B_RSCAN + s), (scan_ph >> s & 1u) ^ 1u, nullptr);
+        }
+        if (qn) mbar_wait(bar(B_QFULL), (qn - 1) & 1u, nullptr);
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------ MMA issuer --------------------------------
+    if (lane == 0) {
+      constexpr uint32_t kIdQK = idesc(BN, false);
+      constexpr uint32_t kIdPV = idesc(D, true);
+      const uint64_t dQ = sdesc(sQ, 16, 1024), dK = sdesc(sR, 16, 1024), dV = sdesc(sR, kRegionKV, 1024);
+      auto issue_s = [&](int i, int st) {
+        const uint64_t a0 = dQ + ((uint32_t)i * Lay::kQTile >> 4);
+        const uint64_t b0 = dK + ((uint32_t)st * Lay::kTile >> 4);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          tc_mma_ss(tS(i), a0 + (((kk / 4) * kRegionQ + (kk % 4) * 32) >> 4),
+                    b0 + (((kk / 4) * kRegionKV + (kk % 4) * 32) >> 4), kIdQK, kk > 0 ? 1u : 0u);
+      };
+      auto issue_pv = [&](int i, int st, bool first) {
+        const uint64_t b0 = dV + ((uint32_t)st * Lay::kTile >> 4);
+#pragma unroll
+        for (int kk = 0; kk < BN / 16; ++kk)
+          tc_mma_ts(tO(i), tS(i) + kk * 8, b0 + ((kk * 2048) >> 4), kIdPV, (!first || kk > 0) ? 1u : 0u);
+      };
+      Ring<NST> rk;                  // runs over the elements K0 V0 K1 V1 ...
+      uint32_t qn = 0, pn[2] = {0, 0};
+      bool ok = true;
+      for (int ii = i0; ok && ii < i1; ++ii) {
+        const PromptItemDev it = p.items[ii];
+        const PromptReqDev rq = p.reqs[it.req];
+        const int cnt[2] = {tile_count(it, rq, p.tpt, 0), tile_count(it, rq, p.tpt, 1)};
+        Ring<NST> k = rk;
+        if (!wait_or_abort(bar(B_QFULL), qn & 1u, p.err, abort_flag)) { ok = false; break; }
+        ++qn;
+        if (!wait_or_abort(bar(B_RFULL + k.st), k.ph, p.err, abort_flag)) { ok = false; break; }
+        tc_fence_after();
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (cnt[i] > 0) {
+            issue_s(i, k.st);
+            tc_commit(bar(B_SFULL + i));
+          }
+        tc_commit(bar(B_REMPTY + k.st));
+        if (it.ntile == 1) tc_commit(bar(B_QEMPTY));
+        for (int j = 0; ok && j < it.ntile; ++j) {
+          Ring<NST> v = k;
+          v.next();
+          k = v;
+          k.next();
+          const bool more = j + 1 < it.ntile;
+          bool have_k = false;
+          if (!wait_or_abort(bar(B_RFULL + v.st), v.ph, p.err, abort_flag)) { ok = false; break; }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if (j >= cnt[i]) continue;
+            if (!wait_or_abort(bar(B_PFULL + i), pn[i] & 1u, p.err, abort_flag)) { ok = false; break; }
+            ++pn[i];
+            tc_fence_after();
+            issue_pv(i, v.st, j == 0);
+            if (j + 1 < cnt[i]) {
+              if (!have_k) {
+                if (!wait_or_abort(bar(B_RFULL + k.st), k.ph, p.err, abort_flag)) { ok = false; break; }
+                tc_fence_after();
+                have_k = true;
+              }
+              issue_s(i, k.st);
+              tc_commit(bar(B_SFULL + i));
+            } else {
+              tc_commit(bar(B_OFULL + i));
+            }
+          }
+          if (!ok) break;
+          tc_commit(bar(B_REMPTY + v.st));
+          if (more) {
+            tc_commit(bar(B_REMPTY + k.st));
+            if (j + 2 == it.ntile) tc_commit(bar(B_QEMPTY));
+          }
+        }
+        rk = k;
+      }
+      // arrives once every MMA issued above has finished, aborted or not
+      tc_commit(bar(B_FINAL));
+    }
+  } else if (warp < 4) {
+    // ----------------------- COLD gather and V tile scan -----------------------
+    const int hw = warp - 2, ht = threadIdx.x - 64;
+    constexpr int kChunks = D / 8;               // 16-byte chunks per row
+    constexpr int kRowsPerCopy = 32 / kChunks;   // rows per warp instruction
+    const int ch = lane % kChunks, sub = lane / kChunks;
+    Ring<NST> ring;
+    uint32_t scan_ph = 0;
+    int pending = -1;                            // stage copied but not announced
+    bool ok = true;
+    auto helper_sync = [&]() { asm volatile("bar.sync %0, %1;" ::"n"(kHelperBar), "n"(kHelperThreads) : "memory"); };
+    auto announce = [&](int st) {                // the copies into st have landed (this thread's)
+      fence_async_shared();
+      helper_sync();
+      if (ht == 0) mbar_arrive(bar(B_RFULL + st));
+    };
+    auto flush = [&]() {
+      if (pending >= 0) {
+        cp_async_wait_group<0>();
+        announce(pending);
+        pending = -1;
+      }
+    };
+    // waits of the two warps end alike: both give up when the CTA is aborted
+    auto wait_all = [&](uint32_t b, uint32_t parity) {
+      return __all_sync(0xffffffffu, wait_or_abort(b, parity, p.err, abort_flag)) != 0;
+    };
+    for (int ii = i0; ok && ii < i1; ++ii) {
+      const PromptItemDev it = p.items[ii];
+      const PromptReqDev rq = p.reqs[it.req];
+      const int nctx = rq.nt_hot + rq.nt_cold;
+      int slot[2] = {-1, -1};                    // slots of rows 64 hw + lane and 64 hw + 32 + lane
+      for (int j = 0; ok && j < 2 * it.ntile; ++j) {
+        const int t = it.tile0 + (j >> 1);
+        const bool is_v = j & 1;
+        const int st = ring.st;
+        const uint32_t ph = ring.ph;
+        ring.next();
+        if (t >= rq.nt_hot && t < nctx) {
+          if (!is_v) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const int pos = (t - rq.nt_hot) * BN + hw * 64 + u * 32 + lane;
+              slot[u] = -1;
+              if (pos < rq.ctx) {
+                const int64_t blk = p.block_table[(int64_t)rq.row * p.max_blocks + pos / p.page];
+                if (blk >= 0 && blk < p.cold_blocks)
+                  slot[u] = (int)(blk * p.page + pos % p.page);
+                else
+                  report_error(p.err, kErrBounds);
+              }
+            }
+          }
+          if (!wait_all(bar(B_REMPTY + st), ph ^ 1u)) { ok = false; break; }
+          const uint16_t* src0 = (is_v ? p.cold_v : p.cold_k) + ((int64_t)p.layer * p.cold_slots * p.Hkv + it.head) * D + ch * 8;
+          const uint32_t dst0 = sR + (uint32_t)st * Lay::kTile + (uint32_t)(ch >> 3) * kRegionKV;
+#pragma unroll 8
+          for (int r0 = 0; r0 < 64; r0 += kRowsPerCopy) {
+            const int row = hw * 64 + r0 + sub;
+            const int s = __shfl_sync(0xffffffffu, slot[r0 >> 5], (r0 & 31) + sub);
+            cp_async16_or_zero(dst0 + row * 128 + (((ch & 7) ^ (row & 7)) << 4),
+                               src0 + (int64_t)max(s, 0) * p.Hkv * D, s >= 0);
+          }
+          cp_async_commit();
+          if (pending >= 0) {
+            cp_async_wait_group<1>();
+            announce(pending);
+          }
+          pending = st;
+          continue;
+        }
+        flush();    // before anything that could wait for the copied tile to be used
+        if (!wait_all(bar(B_REMPTY + st), ph ^ 1u)) { ok = false; break; }
+        if (is_v && scanned(it, rq, t)) {
+          if (!wait_all(bar(B_RSCAN + st), scan_ph >> st & 1u)) { ok = false; break; }
+          scan_ph ^= 1u << st;
+          const bool hot = t < rq.nt_hot;
+          const int key0 = (hot ? t : t - nctx) * BN;
+          const int end = hot ? rq.lp : rq.n;
+          const uint32_t tile = sR + (uint32_t)st * Lay::kTile;
+#pragma unroll 1
+          for (int row = ht; row < BN; row += kHelperThreads) {
+            const int key = key0 + row;
+            bool zero = key >= end;
+            if (!zero && !hot && key > it.tok0) {
+              uint32_t top = 0;
+#pragma unroll
+              for (int c = 0; c < kChunks; ++c) {
+                const uint4 w = lds128(tile + (c >> 3) * kRegionKV + row * 128 + (((c & 7) ^ (row & 7)) << 4));
+                // exponent bits all ones carry into the sign bit of their half
+                top |= ((w.x & 0x7F807F80u) + 0x00800080u) | ((w.y & 0x7F807F80u) + 0x00800080u) |
+                       ((w.z & 0x7F807F80u) + 0x00800080u) | ((w.w & 0x7F807F80u) + 0x00800080u);
+              }
+              if (top & 0x80008000u) {
+                zero = true;
+                *hidden_flag = 1;
+              }
+            }
+            if (zero) {
+#pragma unroll
+              for (int c = 0; c < kChunks; ++c)
+                sts128(tile + (c >> 3) * kRegionKV + row * 128 + (((c & 7) ^ (row & 7)) << 4), make_uint4(0, 0, 0, 0));
+            }
+          }
+          announce(st);
+        }
+      }
+    }
+    if (ok) flush();
+    else cp_async_wait_all();
+  } else {
+    // ---------------------- softmax / correction / epilogue ---------------------
+    const int qi = (warp - 4) >> 2;
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const int tr = row / p.G, hr = row % p.G;     // token within the Q tile, query head within the group
+    uint32_t sn = 0, on = 0;
+    bool ok = true;
+    for (int ii = i0; ok && ii < i1; ++ii) {
+      const PromptItemDev it = p.items[ii];
+      const PromptReqDev rq = p.reqs[it.req];
+      const int nctx = rq.nt_hot + rq.nt_cold;
+      const int cnt = tile_count(it, rq, p.tpt, qi);
+      const int tk = it.tok0 + qi * p.tpt + tr;
+      const bool valid = tr < p.tpt && tk < rq.n;
+      const int seen = min(tk, rq.n - 1);         // rows of no token mask like the last one
+      const int qh = it.head * p.G + hr;
+      float m_used = -INFINITY, l = 0.f;
+      for (int j = 0; ok && j < cnt; ++j) {
+        // warp-uniform: a lane that gave up takes its whole warp out of the loop
+        if (!__all_sync(0xffffffffu, wait_or_abort(bar(B_SFULL + qi), sn & 1u, p.err, abort_flag))) { ok = false; break; }
+        ++sn;
+        tc_fence_after();
+        float s[BN];
+#pragma unroll
+        for (int c = 0; c < BN / 32; ++c) tmem_ld32(tS(qi) + c * 32 + lane_off, s + c * 32);
+        tc_wait_ld();
+        const int t = it.tile0 + j;
+        const int lim = t < rq.nt_hot ? rq.lp - t * BN
+                        : t < nctx    ? rq.ctx - (t - rq.nt_hot) * BN
+                                      : seen + 1 - (t - nctx) * BN;
+        if (__any_sync(0xffffffffu, lim < BN)) {
+#pragma unroll
+          for (int c = 0; c < BN; ++c) s[c] = c < lim ? s[c] : -INFINITY;
+        }
+        float mx8[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) mx8[c] = s[c];
+#pragma unroll
+        for (int c = 8; c + 16 <= BN; c += 16)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) mx8[k] = fmax3(mx8[k], s[c + k], s[c + 8 + k]);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mx8[k] = fmaxf(mx8[k], s[BN - 8 + k]);
+        float mx = fmaxf(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(fmax3(mx8[3], mx8[4], mx8[5]), mx8[6], mx8[7]));
+        mx *= p.scale_log2;
+        if (__any_sync(0xffffffffu, mx > m_used + 8.0f)) {
+          const float m_new = fmaxf(m_used, mx);
+          if (j > 0) {
+            // S(j) completed after PV(j-1), so O holds keys 0..j-1 scaled by 2^-m_used
+            const float f = m_new == -INFINITY ? 1.f : ex2(m_used - m_new);
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              float o[32];
+              tmem_ld32(tO(qi) + c * 32 + lane_off, o);
+              tc_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] *= f;
+              tmem_st32(tO(qi) + c * 32 + lane_off, o);
+            }
+            l *= f;
+          }
+          m_used = m_new;
+        }
+        // a row whose keys so far are all masked keeps m = -inf: its exponents are -inf - 0
+        const float m_sub = m_used == -INFINITY ? 0.f : m_used;
+        const uint64_t sc2 = f2pack(p.scale_log2, p.scale_log2), nm2 = f2pack(-m_sub, -m_sub);
+        uint32_t pk[BN / 2];
+        uint64_t sum4[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int c = 0; c < BN / 2; ++c) {
+          float xa, xb;
+          f2unpack(ffma2(f2pack(s[2 * c], s[2 * c + 1]), sc2, nm2), xa, xb);
+          const float a = ex2(xa), b2 = ex2(xb);
+          sum4[c & 3] = fadd2(sum4[c & 3], f2pack(a, b2));
+          pk[c] = pack_bf16x2(a, b2);
+        }
+        {
+          float s0, s1, s2, s3;
+          f2unpack(fadd2(sum4[0], sum4[1]), s0, s1);
+          f2unpack(fadd2(sum4[2], sum4[3]), s2, s3);
+          l += (s0 + s1) + (s2 + s3);
+        }
+#pragma unroll
+        for (int c = 0; c < BN / 64; ++c)
+          tmem_st32(tS(qi) + c * 32 + lane_off, reinterpret_cast<const float*>(pk + c * 32));
+        tc_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar(B_PFULL + qi));
+      }
+      if (!ok) break;
+      if (cnt > 0) {
+        if (!__all_sync(0xffffffffu, wait_or_abort(bar(B_OFULL + qi), on & 1u, p.err, abort_flag))) { ok = false; break; }
+        ++on;
+        tc_fence_after();
+        if (__any_sync(0xffffffffu, *hidden_flag)) add_hidden_values<D>(p, it, rq, tk, qh, valid, m_used, tO(qi) + lane_off);
+      }
+      const float inv = l > 0.f || l != l ? 1.f / l : 0.f;   // no key in this range: O = 0, LSE = -inf
+      const float lse2 = m_used + __log2f(l);
+      const int64_t prow = (int64_t)it.entry * 256 + qi * BM + row;
+      const int64_t orow = (int64_t)(rq.t0 + tk);
+      if (valid) {
+        if (it.entry >= 0)
+          p.part_l[prow] = lse2;
+        else if (p.lse)
+          p.lse[orow * p.Hq + qh] = lse2 * kLn2;
+      }
+      if (cnt > 0) {
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          float o[32];
+          tmem_ld32(tO(qi) + c * 32 + lane_off, o);
+          tc_wait_ld();
+          if (valid && it.entry >= 0) {
+            uint4* dst = reinterpret_cast<uint4*>(p.part_o + prow * D + c * 32);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              dst[e] = make_uint4(__float_as_uint(o[4 * e] * inv), __float_as_uint(o[4 * e + 1] * inv),
+                                  __float_as_uint(o[4 * e + 2] * inv), __float_as_uint(o[4 * e + 3] * inv));
+          } else if (valid) {
+            uint4* dst = reinterpret_cast<uint4*>(p.out + orow * p.out_stride + qh * D + c * 32);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              dst[e] = make_uint4(pack_bf16x2(o[8 * e] * inv, o[8 * e + 1] * inv),
+                                  pack_bf16x2(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
+                                  pack_bf16x2(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
+                                  pack_bf16x2(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+          }
+          __syncwarp();
+        }
+      }
+    }
+    tc_fence_before();
+  }
+  // every MMA has finished (the MMA thread commits B_FINAL on every path, and its
+  // waits are bounded) and the loads have landed before memory is released
+  if (threadIdx.x == 0) mbar_wait(bar(B_FINAL), 0, nullptr);
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Joins the partial states of rows whose keys several items covered: with l_e the
+// states' LSE (log2), m = max l_e, w_e = 2^(l_e - m): O = sum w_e O_e / sum w_e,
+// LSE = (m + log2 sum w_e) ln 2.  One warp per row, 32 rows per CTA, at most 32
+// states per row (lane e holds state e's weight); bound by the read of the states
+// (4 d bytes each), four in flight per warp.
+template <int D>
+__global__ void __launch_bounds__(256) prompt_join_kernel(const PromptJoinDev* __restrict__ joins,
+                                                          const PromptReqDev* __restrict__ reqs,
+                                                          const float* __restrict__ part_o,
+                                                          const float* __restrict__ part_l, uint16_t* __restrict__ out,
+                                                          float* __restrict__ lse, int64_t out_stride, int32_t Hq,
+                                                          int32_t G, int32_t tpt) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const PromptJoinDev jn = joins[blockIdx.x];
+  const PromptReqDev rq = reqs[jn.req];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int own_ld = jn.own0, n = jn.own_n + jn.hot_n;
+#pragma unroll 1
+  for (int u = 0; u < 4; ++u) {
+    const int r = jn.row0 + u * 8 + warp;          // row of the block, counted token by token
+    const int local = r / G, h = r % G;            // token of the block, head of the group
+    const int tk = jn.tok0 + local;
+    if (local >= 2 * tpt || tk >= rq.n) break;     // warp-uniform
+    const int64_t own_row = (local / tpt) * 128 + (local % tpt) * G + h;
+    const int ht = jn.hot_tok + local, hb = ht / (2 * tpt), hl = ht % (2 * tpt);
+    const int64_t hot_row = (hl / tpt) * 128 + (hl % tpt) * G + h;
+    auto entry_row = [&](int e) {
+      return e < jn.own_n ? (int64_t)(own_ld + e) * 256 + own_row
+                          : (int64_t)(jn.hot0 + hb * jn.hot_n + (e - jn.own_n)) * 256 + hot_row;
+    };
+    const float le = lane < n ? __ldcg(part_l + entry_row(lane)) : -INFINITY;
+    float mx = le;
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+    float w = mx == -INFINITY ? 0.f : ex2(le - mx);
+    if (lane >= n) w = 0.f;
+    float z = w;
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) z += __shfl_xor_sync(0xffffffffu, z, off);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    const bool has = lane < D / 4;
+    for (int e0 = 0; e0 < n; e0 += 4) {
+      float4 v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        v[k] = has && e0 + k < n ? __ldcg(reinterpret_cast<const float4*>(part_o + entry_row(e0 + k) * D) + lane)
+                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float wk = __shfl_sync(0xffffffffu, w, (e0 + k) & 31);
+        if (wk != 0.f) {                           // an empty state's row may never have been written
+          o.x = fmaf(wk, v[k].x, o.x);
+          o.y = fmaf(wk, v[k].y, o.y);
+          o.z = fmaf(wk, v[k].z, o.z);
+          o.w = fmaf(wk, v[k].w, o.w);
+        }
+      }
+    }
+    const float inv = z > 0.f || z != z ? 1.f / z : 0.f;
+    const int64_t orow = rq.t0 + tk;
+    const int qh = jn.head * G + h;
+    if (has)
+      reinterpret_cast<uint2*>(out + orow * out_stride + qh * D)[lane] =
+          make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    if (lane == 0 && lse) lse[orow * Hq + qh] = (mx + __log2f(z)) * kLn2;
+  }
+}
+
+namespace {
+
+template <int D>
+int launch_t(const Params& pp, const PromptPlan* pl, const uint8_t* base, cudaStream_t st) {
+  auto kern = prompt_kernel<D>;
+  constexpr size_t smem = 1024 + Layout<D>::kData + kCtlBytes;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return (int)e;
+  const int ctas = (int)pl->cta_begin.size() - 1;
+  if (ctas > 0) {
+    e = launch_pdl(kern, dim3(ctas), dim3(kThreads), smem, st, pp);
+    if (e != cudaSuccess) return (int)e;
+  }
+  if (!pl->joins.empty())
+    e = launch_pdl(prompt_join_kernel<D>, dim3((unsigned)pl->joins.size()), dim3(256), 0, st,
+                   (const PromptJoinDev*)(base + pl->off_joins), pp.reqs, (const float*)pp.part_o,
+                   (const float*)pp.part_l, pp.out, pp.lse, pp.out_stride, pp.Hq, pp.G, pp.tpt);
+  return (int)e;
+}
+
+}  // namespace
+}  // namespace prompt
+
+// 3D map over a packed tensor [tokens][heads][d] with a token stride, 128-byte
+// swizzle; tokens past the end read as zeros
+static int encode_packed(CUtensorMap* tm, const void* ptr, int d, int heads, int64_t tokens, int64_t stride,
+                         int box_heads, int box_tokens) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return 1;
+  cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)tokens};
+  cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)stride * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_tokens};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? 0
+             : 2;
+}
+
+// 2D map over a whole HOT pool as rows of d elements
+static int encode_hot(CUtensorMap* tm, const void* ptr, int d, int64_t rows) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return 1;
+  cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)d * 2};
+  cuuint32_t box[2] = {64, (cuuint32_t)kPrefixTileN};
+  cuuint32_t estr[2] = {1, 1};
+  return enc(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? 0
+             : 2;
+}
+
+int launch_prompt(const LaunchCommon& lc, void* stream, int32_t layer, const gk_prompt_batch* b, const PromptPlan* pl) {
+  const gk_pool_config& c = *lc.cfg;
+  const uint8_t* base = (const uint8_t*)pl->d_buf;
+  const int D = c.head_dim, G = c.num_q_heads / c.num_kv_heads;
+  prompt::Params pp = {};
+  pp.Hq = c.num_q_heads;
+  pp.Hkv = c.num_kv_heads;
+  pp.G = G;
+  pp.tpt = kPrefixTileM / G;
+  pp.layer = layer;
+  pp.q_stride = b->q_stride ? b->q_stride : (int64_t)pp.Hq * D;
+  pp.k_stride = b->k_stride ? b->k_stride : (int64_t)pp.Hkv * D;
+  pp.v_stride = b->v_stride ? b->v_stride : (int64_t)pp.Hkv * D;
+  pp.out_stride = b->out_stride ? b->out_stride : (int64_t)pp.Hq * D;
+  int e = encode_packed(&pp.tq, b->d_q, D, pp.Hq, pl->tokens, pp.q_stride, G, pp.tpt);
+  if (!e) e = encode_packed(&pp.tk, b->d_k, D, pp.Hkv, pl->tokens, pp.k_stride, 1, kPrefixTileN);
+  if (!e) e = encode_packed(&pp.tv, b->d_v, D, pp.Hkv, pl->tokens, pp.v_stride, 1, kPrefixTileN);
+  if (!e && pl->any_hot) {
+    const int64_t rows = c.hot_tokens * c.num_layers * c.num_kv_heads;
+    e = encode_hot(&pp.thk, c.hot_k, D, rows);
+    if (!e) e = encode_hot(&pp.thv, c.hot_v, D, rows);
+  }
+  if (e) return (int)cudaErrorInvalidValue;
+  pp.reqs = (const PromptReqDev*)(base + pl->off_reqs);
+  pp.items = (const PromptItemDev*)(base + pl->off_items);
+  pp.cta_begin = (const int32_t*)(base + pl->off_begin);
+  pp.block_table = b->d_block_table;
+  pp.cold_k = (const uint16_t*)c.cold_k;
+  pp.cold_v = (const uint16_t*)c.cold_v;
+  pp.q = (const uint16_t*)b->d_q;
+  pp.k = (const uint16_t*)b->d_k;
+  pp.v = (const uint16_t*)b->d_v;
+  pp.out = (uint16_t*)b->d_out;
+  pp.lse = b->d_lse;
+  pp.part_o = pl->d_part_o;
+  pp.part_l = pl->d_part_l;
+  pp.cold_slots = c.cold_slots;
+  pp.cold_blocks = c.cold_slots / c.cold_page_size;
+  pp.page = c.cold_page_size;
+  pp.max_blocks = b->max_blocks;
+  pp.err = lc.d_error;
+  pp.scale_log2 = kLog2e / sqrtf((float)D);
+  if (D == 128) return prompt::launch_t<128>(pp, pl, base, (cudaStream_t)stream);
+  if (D == 64) return prompt::launch_t<64>(pp, pl, base, (cudaStream_t)stream);
+  return (int)cudaErrorInvalidValue;
+}
+
+}  // namespace gk

@@ -8,7 +8,12 @@ decode step, which the caller strings together in this order:
   append_slots (gk_seq_append_slots) -> append_kv (gk_append_kv, per layer;
   or the decode's fused append) -> plan (gk_plan_build / gk_plan_update)
   -> dispatch (gk_dispatch) -> decode (gk_decode_cascade | gk_decode_dense,
-  per layer).
+  per layer),
+
+and of a prompt step (the new tokens of prompts, turns or chunks):
+
+  append_slots -> prompt_batch, prompt_plan (gk_prompt_plan_build / _update)
+  -> per layer: append_kv, prompt (gk_prompt_attn).
 
 Every method is one library call; the work is in libgk.
 """
@@ -35,11 +40,15 @@ class Engine:
         self.pool = gk.gk_pool_create(L, Hq, Hkv, d, hot_tokens, cold_slots, page_size, seed,
                                       self.hot_k, self.hot_v, self.cold_k, self.cold_v)
         self._plans = []
+        self._prompt_plans = []
 
     def close(self):
         for p in self._plans:
             gk.gk_plan_destroy(p)
+        for p in self._prompt_plans:
+            gk.gk_prompt_plan_destroy(p)
         self._plans = []
+        self._prompt_plans = []
         if self.pool:
             gk.gk_pool_destroy(self.pool)
             self.pool = None
@@ -105,6 +114,23 @@ class Engine:
             gk.gk_decode_dense(self.pool, stream, layer, batch, plan)
         else:
             gk.gk_decode_cascade(self.pool, stream, layer, batch, plan)
+
+    # ---- prompt step --------------------------------------------------------------------
+    def prompt_batch(self, new_lens, prefix_bases=None, prefix_lens=None, context_lens=None, d_table=None, max_blocks=0):
+        return gk.PromptBatch(new_lens, prefix_bases, prefix_lens, context_lens, d_table, max_blocks)
+
+    def prompt_plan(self, batch, stream=None, plan=None):
+        if plan is None:
+            plan = gk.gk_prompt_plan_build(self.pool, batch, stream)
+            self._prompt_plans.append(plan)
+        else:
+            gk.gk_prompt_plan_update(self.pool, plan, batch, stream)
+        return plan
+
+    def prompt(self, layer, batch, plan, q, k, v, out, lse=None, stream=None):
+        """Causal attention of one layer's new tokens (bf16 q, out [T, Hq, d]; k, v [T, Hkv, d])."""
+        batch.set_device(q, k, v, out, lse)
+        gk.gk_prompt_attn(self.pool, stream, layer, batch, plan)
 
     def device_error(self, stream=None):
         return gk.gk_device_error(self.pool, stream)
