@@ -169,6 +169,47 @@ gk_status gk_seq_cache_blocks(gk_pool* pool, int32_t seq, int32_t n_tokens, cons
 /* Blocks in the cache, and those of them no sequence holds (evictable). */
 gk_status gk_cold_cache_stats(const gk_pool* pool, int64_t* cached_blocks, int64_t* evictable_blocks);
 
+/* Block tables and slot maps built on the device: the same bookkeeping for rows
+ * (one per request slot of an engine) that share no block, without a host loop
+ * per token or a copy of tables and slots, so a captured graph can contain it.
+ * The caller owns the arrays.  The blocks on the stack are the caller's to hand
+ * out: taken from the pool beforehand (a sequence that holds them keeps the
+ * pool's own manager off them) and given back when the rows are done.  Forked and
+ * cached sequences, whose blocks are shared, stay with gk_seq_*. */
+typedef struct gk_tables {
+  int32_t num_rows;       /* R, at most 2^20 */
+  int32_t max_blocks;     /* row stride of d_table: the most blocks a row can hold */
+  int32_t capacity;       /* entries of d_free */
+  int32_t reserved0;
+  int32_t* d_table;       /* device [R][max_blocks]: block ids, valid up to each row's length */
+  int32_t* d_free;        /* device [capacity]: stack of free block ids; the last one below the count is
+                             handed out next */
+  const int32_t* d_len;   /* device [R]: tokens of each row before the step ... */
+  int32_t* d_len_out;     /* ... and after it (may be d_len) */
+  const int32_t* d_num_free; /* device [1]: ids on the stack before the step ... */
+  int32_t* d_num_free_out;   /* ... and after it (may be d_num_free) */
+  void* d_work;           /* device, GK_TABLES_WORK_PER_ROW * (R + 1) bytes, 16-byte aligned: scratch of a step */
+} gk_tables;
+#define GK_TABLES_WORK_PER_ROW 32
+
+/* One step.  First every row r with d_release[r] != 0 (d_release NULL: none) gives
+ * its blocks back, in row order, and has length 0 (gk_seq_release).  Then every
+ * row r, in row order, gets d_add[r] tokens (gk_seq_append_slots): the slots of
+ * all rows' tokens follow one another in d_slot_mapping [n_slots] (gk_append_kv's
+ * input), places past the last token are -1.  When the stack runs empty, the token
+ * that needed the next block and every later one are not placed: their slots are
+ * -1, and d_done[r] tells how many tokens of each row were.  Lengths, tables, the
+ * stack and the slots come out bit for bit as from those calls.
+ * d_release, d_add, d_done: device int32 [R]; d_slot_mapping: device int64.
+ * A row with a negative length or add, a table too long for its row or for
+ * max_blocks after the append, or tokens past n_slots appends nothing; an id on
+ * the stack outside the pool gives slots of -1; a count outside [0, capacity], or
+ * releases past it, counts as an empty stack or releases nothing: each is reported
+ * as GK_ERR_DEVICE_BOUNDS by gk_device_error().  Nothing happens when R = 0.  Calls
+ * that share any of the arrays must be ordered. */
+gk_status gk_tables_step(gk_pool* pool, void* stream, const gk_tables* t, const int32_t* d_release,
+                         const int32_t* d_add, int64_t n_slots, int64_t* d_slot_mapping, int32_t* d_done);
+
 /* ---- KV writes (device) ---------------------------------------------------- */
 
 /* reshape_and_cache ("Paged KV cache", step 1) for one layer: first copy every

@@ -69,6 +69,15 @@ class gk_cost_model(ctypes.Structure):
                 ("split_tensor_us", c_dbl)]
 
 
+class gk_tables(ctypes.Structure):
+    _fields_ = [("num_rows", c_i32), ("max_blocks", c_i32), ("capacity", c_i32), ("reserved0", c_i32), ("d_table", c_vp),
+                ("d_free", c_vp), ("d_len", c_vp), ("d_len_out", c_vp), ("d_num_free", c_vp), ("d_num_free_out", c_vp),
+                ("d_work", c_vp)]
+
+
+GK_TABLES_WORK_PER_ROW = 32
+
+
 class gk_prompt_batch(ctypes.Structure):
     _fields_ = [("num_requests", c_i32), ("max_blocks", c_i32), ("new_len", ctypes.POINTER(c_i32)),
                 ("prefix_hot_base", ctypes.POINTER(c_i64)), ("prefix_len", ctypes.POINTER(c_i32)),
@@ -119,6 +128,7 @@ _SIGS = {
     "gk_cascade_prefix": (c_i32, [c_vp, c_vp, c_i32, P(gk_batch), c_vp]),
     "gk_cascade_suffix": (c_i32, [c_vp, c_vp, c_i32, P(gk_batch), c_vp]),
     "gk_cascade_merge": (c_i32, [c_vp, c_vp, c_i32, P(gk_batch), c_vp]),
+    "gk_tables_step": (c_i32, [c_vp, c_vp, P(gk_tables), c_vp, c_vp, c_i64, c_vp, c_vp]),
     "gk_prompt_plan_build": (c_i32, [c_vp, P(gk_prompt_batch), c_vp, P(c_vp)]),
     "gk_prompt_plan_update": (c_i32, [c_vp, P(gk_prompt_batch), c_vp]),
     "gk_prompt_plan_destroy": (None, [c_vp]),
@@ -338,6 +348,31 @@ def gk_block_refcount(pool, block):
     r = c_i32()
     _check(lib().gk_block_refcount(pool, block, ctypes.byref(r)), pool)
     return r.value
+
+
+class Tables:
+    """A gk_tables over int32 torch tensors: table [rows, max_blocks], free [capacity], length [rows],
+    num_free [1]; the step's outputs go to length_out and num_free_out (default: in place)."""
+
+    def __init__(self, table, free, length, num_free, length_out=None, num_free_out=None):
+        self.length_out = length if length_out is None else length_out
+        self.num_free_out = num_free if num_free_out is None else num_free_out
+        self.table, self.free, self.length, self.num_free = table, free, length, num_free
+        rows, width = table.shape
+        for x, n in ((table, rows * width), (free, free.numel()), (length, rows), (num_free, 1), (self.length_out, rows),
+                     (self.num_free_out, 1)):
+            if x.numel() != n or x.element_size() != 4 or x.is_floating_point() or not x.is_contiguous():
+                raise ValueError("tables are contiguous int32 tensors: table [rows, max_blocks], free, length [rows], num_free [1]")
+        # int32 words: allocations are at least 16-byte aligned
+        self.work = table.new_empty((rows + 1) * (GK_TABLES_WORK_PER_ROW // 4))
+        self.c = gk_tables(rows, width, free.numel(), 0, _ptr(table), _ptr(free), _ptr(length), _ptr(self.length_out),
+                           _ptr(num_free), _ptr(self.num_free_out), _ptr(self.work))
+
+
+def gk_tables_step(pool, stream, tables, d_add, d_slot_mapping, d_done, d_release=None, n_slots=None):
+    n_slots = d_slot_mapping.numel() if n_slots is None else n_slots
+    _check(lib().gk_tables_step(pool, _stream(stream), ctypes.byref(tables.c), _ptr(d_release), _ptr(d_add), n_slots,
+                                _ptr(d_slot_mapping), _ptr(d_done)), pool)
 
 
 # ---- device work -------------------------------------------------------------------

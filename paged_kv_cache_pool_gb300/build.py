@@ -30,7 +30,7 @@ SAN_FLAGS = [f for o in ("-fsanitize=address", "-fsanitize=undefined", "-fno-omi
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["host_pool.cpp", "plan.cpp", "kv_write.cu", "gather_attn.cu", "merge.cu", "prefix_tc.cu",
            "prefix_warp.cu", "cascade_split.cu", "static_scratch.cu", "calibrate.cu",
-           "prompt_plan.cpp", "prompt_attn.cu"]
+           "prompt_plan.cpp", "prompt_attn.cu", "tables.cu"]
 COMMON = ["-O3", "-std=c++17", "-Xcompiler", "-fPIC", "-lineinfo", "-I" + os.path.join(ROOT, "include")]
 
 

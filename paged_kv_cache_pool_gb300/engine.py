@@ -12,7 +12,8 @@ decode step, which the caller strings together in this order:
 
 and of a prompt step (the new tokens of prompts, turns or chunks):
 
-  append_slots -> prompt_batch, prompt_plan (gk_prompt_plan_build / _update)
+  append_slots (or tables_step, whose tables and slots stay on the device)
+  -> prompt_batch, prompt_plan (gk_prompt_plan_build / _update)
   -> per layer: append_kv, prompt (gk_prompt_attn).
 
 Every method is one library call; the work is in libgk.
@@ -93,6 +94,29 @@ class Engine:
 
     def seq_len(self, seq):
         return gk.gk_seq_table(self.pool, seq)[1]
+
+    # ---- COLD tables kept on the device ---------------------------------------------------
+    def device_tables(self, rows, max_blocks, n_blocks):
+        """Tables of `rows` empty rows over n_blocks of the pool's blocks, which gk_tables_step hands out in the
+        order the pool would have; -> (tables, seq): seq holds the blocks until seq_release."""
+        seq = self.seq_create()
+        try:
+            self.append_slots(np.full(n_blocks * self.page_size, seq, np.int32))
+        except gk.GkError:
+            self.seq_release(seq)
+            raise
+        ids = gk.gk_seq_table(self.pool, seq)[0]
+        zeros = lambda *n: self.torch.zeros(*n, dtype=self.torch.int32, device=self.device)  # noqa: E731
+        tables = gk.Tables(zeros(rows, max_blocks), self.to_device(ids[::-1]), zeros(rows),
+                           self.to_device(np.asarray([n_blocks], np.int32)))
+        return tables, seq
+
+    def tables_step(self, tables, d_add, n_slots, d_release=None, stream=None):
+        """-> (slot mapping [n_slots], tokens placed per row) of one step (gk_tables_step)."""
+        slots = self.torch.empty(n_slots, dtype=self.torch.int64, device=self.device)
+        done = self.torch.empty_like(tables.length)
+        gk.gk_tables_step(self.pool, stream, tables, d_add, slots, done, d_release)
+        return slots, done
 
     # ---- step -------------------------------------------------------------------------
     def batch(self, prefix_bases, prefix_lens, suffix_lens, d_table, max_blocks):
