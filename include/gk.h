@@ -440,7 +440,8 @@ gk_status gk_prompt_plan_items(const gk_prompt_plan* plan, int32_t* n_ctas, int3
 /* Attention of one layer of a planned prompt step: with s_j = q.k_j / sqrt(d) over
  * the keys the row attends, out = sum_j e^(s_j) v_j / Z and lse = ln Z, Z = sum_j
  * e^(s_j).  Products and sums are held in fp32; the weights are rounded to bf16
- * before the product with V, the output to bf16 at the end.  Keys a row does not
+ * before the product with V, the output to bf16 at the end; scores of magnitude
+ * 2^28 and more, which fp32 holds to whole tens only, are out of range.  Keys a row does not
  * attend contribute nothing, whatever their K and V hold (infinities and NaN
  * included).  Reads COLD through the block table (an out-of-range block id
  * counts as zero K and V and is reported as GK_ERR_DEVICE_BOUNDS by

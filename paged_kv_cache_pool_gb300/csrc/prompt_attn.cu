@@ -15,13 +15,18 @@
 // (rows gathered through the block table by two warps with 16-byte cp.async),
 // then tiles of new tokens (3D tensor maps over the caller's packed tensors).
 // S_i = Q_i K^T and O_i += P_i V accumulate in tensor memory (512 columns: S_0
-// S_1 O_0 O_1; P_i overwrites S_i as bf16), softmax warpgroup i owns Q tile i,
-// one thread per row, and the MMA thread alternates PV_0(j), S_0(j+1), PV_1(j),
-// S_1(j+1), so that one tile's softmax runs under the other tile's products.
+// S_1 O_0 O_1; P_i overwrites S_i as bf16).  Softmax warpgroup i owns Q tile i, one
+// thread per row, and one warp issues PV_0(j) S_0(j+1), PV_1(j) S_1(j+1), so that
+// one tile's softmax runs under the other's products.  A tile's two products take
+// 1024 tensor cycles, so its softmax has to come back in about as long; there is
+// no pass for the maximum: exponents are taken against a reference that is the
+// maximum of the row's first tile, raised between tiles when a tile's sum passed
+// 2^8 and within one (its exponentials are then done again) when it passed 2^64,
+// so that every value stays in fp32 and bf16 range.  O and LSE use the same
+// reference as P, so this changes neither beyond fp32 rounding.
 // P is rounded to bf16 (half a step, 2^-9 to 2^-8 of the value) because V is
 // bf16 and both operands of the product have one type; the row sum adds the
-// unrounded fp32 values.  m is only raised when a row's maximum grows by more
-// than 2^8, which changes neither O nor LSE beyond fp32 rounding.
+// unrounded fp32 values.
 //
 // CTAs are persistent (one per SM: 512 tensor-memory columns and 224 KB of
 // shared memory) and run the lists of items that the plan balanced.  K and V tiles
@@ -57,11 +62,8 @@ using prefix::kRegionQ;
 using prefix::kTmemCols;
 using prefix::sdesc;
 using prefix::tc_mma_ts;
-using prefix::wait_or_abort;
 
 constexpr int kThreads = 384;
-constexpr int kHelperThreads = 64;
-constexpr int kHelperBar = 1;     // named barrier of the gather and scan warps
 
 struct Params {
   CUtensorMap tq, tk, tv;         // the call's packed tensors
@@ -110,6 +112,9 @@ constexpr uint32_t kCtlTmemSlot = B_COUNT * 8;
 constexpr uint32_t kCtlAbort = kCtlTmemSlot + 4;
 constexpr uint32_t kCtlHidden = kCtlAbort + 4;   // an infinity or NaN was hidden in this CTA's V tiles
 constexpr uint32_t kCtlBytes = 512;
+static_assert(kCtlHidden + 4 <= kCtlBytes, "prompt control block");
+// dynamic shared memory starts 1024-byte aligned (checked by the kernel)
+static_assert(Layout<128>::kData + kCtlBytes <= 232448 && Layout<64>::kData + kCtlBytes <= 232448, "shared memory");
 
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* tmap, int x, int y, uint32_t bar) {
   asm volatile(
@@ -127,6 +132,25 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 template <int N>
 __device__ __forceinline__ void cp_async_wait_group() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Bounded wait; the clock and the CTA's abort flag are looked at every 256 tries only,
+// as reading the timer at each try delays what follows the barrier by 100 cycles and more.
+__device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, int32_t* err, volatile int* abort_flag) {
+  if (mbar_try_wait(bar, parity)) return true;
+  uint64_t t0 = 0;
+  for (uint32_t n = 1;; ++n) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (n & 255u) continue;
+    if (*abort_flag) return false;
+    const uint64_t now = globaltimer_ns();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > kWaitLimitNs) {
+      report_error(err, kErrTimeout);
+      *abort_flag = 1;
+      return false;
+    }
+  }
 }
 
 // ring position: stage and phase parity of the current element
@@ -193,15 +217,61 @@ __device__ __noinline__ void add_hidden_values(const Params& p, const PromptItem
   }
 }
 
+// a value every lane holds, in a form the compiler knows to be warp-uniform
+__device__ __forceinline__ int uniform(int x) { return __reduce_max_sync(0xffffffffu, x); }
+// true on one lane of the (converged) warp, always the same one
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e != 0;
+}
+
+// keeps uses of the registers of a tcgen05.ld behind its wait
+__device__ __forceinline__ void tie32(float* v) {
+#pragma unroll
+  for (int e = 0; e < 32; e += 8)
+    asm volatile("" : "+f"(v[e]), "+f"(v[e + 1]), "+f"(v[e + 2]), "+f"(v[e + 3]), "+f"(v[e + 4]), "+f"(v[e + 5]),
+                 "+f"(v[e + 6]), "+f"(v[e + 7]));
+}
+
+__device__ __forceinline__ float max32(const float* s) {
+  float a[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) a[k] = fmax3(s[k], s[k + 4], s[k + 8]);
+#pragma unroll
+  for (int c = 12; c < 28; c += 8)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) a[k] = fmax3(a[k], s[c + k], s[c + 4 + k]);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) a[k] = fmaxf(a[k], s[28 + k]);
+  return fmaxf(fmax3(a[0], a[1], a[2]), a[3]);
+}
+
+// 2^(s * scale - m) of 32 scores as 16 bf16 pairs, added to the running sums in fp32
+__device__ __forceinline__ void exp32(const float* s, uint32_t* pk, uint64_t* sum4, uint64_t sc2, uint64_t nm2) {
+#pragma unroll
+  for (int c = 0; c < 16; ++c) {
+    float xa, xb;
+    f2unpack(ffma2(f2pack(s[2 * c], s[2 * c + 1]), sc2, nm2), xa, xb);
+    const float a = ex2(xa), b = ex2(xb);
+    sum4[c & 3] = fadd2(sum4[c & 3], f2pack(a, b));
+    pk[c] = pack_bf16x2(a, b);
+  }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_constant__ Params p) {
   using Lay = Layout<D>;
   constexpr int NST = Lay::NST;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
-  const uint32_t base = (raw + 1023u) & ~1023u;
+  if (raw & 1023u) {              // the operand layouts need it
+    if (threadIdx.x == 0) report_error(p.err, kErrTimeout);
+    return;
+  }
+  const uint32_t base = raw;
   const uint32_t ctl = base + Lay::kData;
-  uint8_t* ctl_ptr = smem_raw + (ctl - raw);
+  uint8_t* ctl_ptr = smem_raw + Lay::kData;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(ctl_ptr + kCtlAbort);
   volatile int* hidden_flag = reinterpret_cast<volatile int*>(ctl_ptr + kCtlHidden);
   auto bar = [&](int i) { return ctl + 8u * (uint32_t)i; };
@@ -214,19 +284,25 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     *hidden_flag = 0;
     mbar_init(bar(B_QFULL), 1);
     mbar_init(bar(B_QEMPTY), 1);
+    mbar_init(bar(B_FINAL), 1);
+    for (int s = 0; s < NST; ++s) {
+      mbar_init(bar(B_REMPTY + s), 1);
+      mbar_init(bar(B_RFULL + s), 2);   // the TMA thread arrives twice, or each gather warp once
+      mbar_init(bar(B_RSCAN + s), 1);
+    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(B_SFULL + i), 1);
       mbar_init(bar(B_PFULL + i), 128);
       mbar_init(bar(B_OFULL + i), 1);
     }
-    mbar_init(bar(B_FINAL), 1);
-    for (int s = 0; s < NST; ++s) {
-      mbar_init(bar(B_RFULL + s), 1);
-      mbar_init(bar(B_REMPTY + s), 1);
-      mbar_init(bar(B_RSCAN + s), 1);
-    }
     fence_mbar_init();
   }
+  // rows of a Q tile that no token has (g = 5) stay zero
+  for (int c = threadIdx.x; c < 2 * (D / 64) * (BM - p.tpt * p.G) * 8; c += kThreads) {
+    const int per = (BM - p.tpt * p.G) * 8;
+    sts128(sQ + (uint32_t)(c / per) * kRegionQ + (uint32_t)(p.tpt * p.G * 8 + c % per) * 16, make_uint4(0, 0, 0, 0));
+  }
+  fence_async_shared();
   if (warp == 1) {
     tmem_alloc(ctl + kCtlTmemSlot, kTmemCols);
     tmem_relinquish();
@@ -240,58 +316,64 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   auto tS = [&](int i) { return tmem + (uint32_t)(i * 128); };
   auto tO = [&](int i) { return tmem + 256u + (uint32_t)(i * 128); };
 
+  // a wait of a whole warp, with a warp-uniform answer
+  auto wait = [&](int b, uint32_t parity) {
+    return __all_sync(0xffffffffu, wait_or_abort(bar(b), parity, p.err, abort_flag)) != 0;
+  };
+
   if (warp == 0) {
     // ------------------------------ TMA producer ------------------------------
     if (lane == 0) {
-      Ring<NST> ring;
-      uint32_t scan_ph = 0;                     // bit s: parity of RSCAN[s]'s current phase
-      uint32_t in_ring = 0, in_scan = 0, full_ph = 0;  // last load of each stage, for the drain below
+      Ring<NST> ring;                              // over the elements K0 V0 K1 V1 ...
+      uint32_t scan_ph = 0;                        // bit s: parity of RSCAN[s]'s current phase
+      uint32_t in_ring = 0, in_scan = 0, full_ph = 0;  // the last load of each stage, for the drain below
       uint32_t qn = 0;
       bool ok = true;
       for (int ii = i0; ok && ii < i1; ++ii) {
         const PromptItemDev it = p.items[ii];
         const PromptReqDev rq = p.reqs[it.req];
         const int nctx = rq.nt_hot + rq.nt_cold;
-        auto load = [&](int j, bool is_v) {
-          const int t = it.tile0 + j;
+        for (int j = 0; j < 2 * it.ntile; ++j) {
+          const int t = it.tile0 + (j >> 1);
+          const bool is_v = j & 1;
           const int st = ring.st;
           const uint32_t ph = ring.ph;
           ring.next();
           // waited for whoever fills the stage: a parity wait may not fall a phase behind
-          if (!wait_or_abort(bar(B_REMPTY + st), ph ^ 1u, p.err, abort_flag)) return false;
-          if (t >= rq.nt_hot && t < nctx) return true;       // COLD: the gather warps
-          const bool scan = is_v && scanned(it, rq, t);
-          const uint32_t b = bar((scan ? B_RSCAN : B_RFULL) + st);
-          mbar_arrive_expect_tx(b, Lay::kTile);
-          const uint32_t dst = sR + (uint32_t)st * Lay::kTile;
-          if (t < rq.nt_hot) {
-            const int row = (int)(rq.hot_row + ((int64_t)p.layer * p.Hkv + it.head) * rq.lp + t * BN);
-            for (int h = 0; h < D / 64; ++h) tma_load_2d(dst + h * kRegionKV, is_v ? &p.thv : &p.thk, h * 64, row, b);
-          } else {
-            const int row = rq.t0 + (t - nctx) * BN;
-            for (int h = 0; h < D / 64; ++h)
-              tma_load_3d(dst + h * kRegionKV, is_v ? &p.tv : &p.tk, h * 64, it.head, row, b);
+          if (!wait_or_abort(bar(B_REMPTY + st), ph ^ 1u, p.err, abort_flag)) { ok = false; break; }
+          if (t < rq.nt_hot || t >= nctx) {        // COLD tiles: the gather warps
+            const bool scan = is_v && scanned(it, rq, t);
+            const uint32_t b = bar((scan ? B_RSCAN : B_RFULL) + st);
+            const uint32_t tile = sR + (uint32_t)st * Lay::kTile;
+            if (!scan) mbar_arrive(b);
+            mbar_arrive_expect_tx(b, Lay::kTile);
+            if (t < rq.nt_hot) {
+              const int row = (int)(rq.hot_row + ((int64_t)p.layer * p.Hkv + it.head) * rq.lp + t * BN);
+              for (int h = 0; h < D / 64; ++h) tma_load_2d(tile + h * kRegionKV, is_v ? &p.thv : &p.thk, h * 64, row, b);
+            } else {
+              const int row = rq.t0 + (t - nctx) * BN;
+              for (int h = 0; h < D / 64; ++h)
+                tma_load_3d(tile + h * kRegionKV, is_v ? &p.tv : &p.tk, h * 64, it.head, row, b);
+            }
+            const uint32_t bit = 1u << st;
+            in_ring = scan ? in_ring & ~bit : in_ring | bit;
+            in_scan = scan ? in_scan | bit : in_scan & ~bit;
+            full_ph = (full_ph & ~bit) | (ph << st);
+            if (scan) scan_ph ^= bit;
           }
-          const uint32_t bit = 1u << st;
-          in_ring = scan ? in_ring & ~bit : in_ring | bit;
-          in_scan = scan ? in_scan | bit : in_scan & ~bit;
-          full_ph = (full_ph & ~bit) | (ph << st);
-          if (scan) scan_ph ^= bit;
-          return true;
-        };
-        ok = load(0, false) && load(0, true);
-        if (!ok) break;
-        // the Q tiles, once the last product with the item before has read its own
-        if (!wait_or_abort(bar(B_QEMPTY), (qn & 1u) ^ 1u, p.err, abort_flag)) { ok = false; break; }
-        const bool two = it.tok0 + p.tpt < rq.n;
-        const uint32_t q_bytes = (uint32_t)(p.tpt * p.G) * 128u * (D / 64);
-        mbar_arrive_expect_tx(bar(B_QFULL), two ? 2 * q_bytes : q_bytes);
-        for (int i = 0; i < (two ? 2 : 1); ++i)
-          for (int h = 0; h < D / 64; ++h)
-            tma_load_3d(sQ + i * Lay::kQTile + h * kRegionQ, &p.tq, h * 64, it.head * p.G, rq.t0 + it.tok0 + i * p.tpt,
-                        bar(B_QFULL));
-        ++qn;
-        for (int j = 1; ok && j < it.ntile; ++j) ok = load(j, false) && load(j, true);
+          if (j == 1) {
+            // the Q tiles, once the last product with the item before has read its own
+            if (!wait_or_abort(bar(B_QEMPTY), (qn & 1u) ^ 1u, p.err, abort_flag)) { ok = false; break; }
+            ++qn;
+            const bool two = it.tok0 + p.tpt < rq.n;
+            const uint32_t q_bytes = (uint32_t)(p.tpt * p.G) * 128u * (D / 64);
+            mbar_arrive_expect_tx(bar(B_QFULL), two ? 2 * q_bytes : q_bytes);
+            for (int i = 0; i < (two ? 2 : 1); ++i)
+              for (int h = 0; h < D / 64; ++h)
+                tma_load_3d(sQ + i * Lay::kQTile + h * kRegionQ, &p.tq, h * 64, it.head * p.G,
+                            rq.t0 + it.tok0 + i * p.tpt, bar(B_QFULL));
+          }
+        }
       }
       if (!ok) {
         // let the loads already issued land before shared memory goes away
@@ -304,98 +386,96 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     }
   } else if (warp == 1) {
     // ------------------------------ MMA issuer --------------------------------
-    if (lane == 0) {
-      constexpr uint32_t kIdQK = idesc(BN, false);
-      constexpr uint32_t kIdPV = idesc(D, true);
-      const uint64_t dQ = sdesc(sQ, 16, 1024), dK = sdesc(sR, 16, 1024), dV = sdesc(sR, kRegionKV, 1024);
-      auto issue_s = [&](int i, int st) {
-        const uint64_t a0 = dQ + ((uint32_t)i * Lay::kQTile >> 4);
-        const uint64_t b0 = dK + ((uint32_t)st * Lay::kTile >> 4);
+    // The whole warp walks the loop with warp-uniform values and one elected lane
+    // issues: the descriptors then stay in uniform registers, where a loop of one
+    // lane moves each of them there for every MMA (84 cycles per MMA measured, 64
+    // being the tensor cores' own).
+    constexpr uint32_t kIdQK = idesc(BN, false);
+    constexpr uint32_t kIdPV = idesc(D, true);
+    const uint64_t dQ = sdesc(sQ, 16, 1024), dK = sdesc(sR, 16, 1024), dV = sdesc(sR, kRegionKV, 1024);
+    auto issue_s = [&](int i, int st) {
+      const uint64_t a0 = dQ + ((uint32_t)i * Lay::kQTile >> 4);
+      const uint64_t b0 = dK + ((uint32_t)st * Lay::kTile >> 4);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          tc_mma_ss(tS(i), a0 + (((kk / 4) * kRegionQ + (kk % 4) * 32) >> 4),
-                    b0 + (((kk / 4) * kRegionKV + (kk % 4) * 32) >> 4), kIdQK, kk > 0 ? 1u : 0u);
-      };
-      auto issue_pv = [&](int i, int st, bool first) {
-        const uint64_t b0 = dV + ((uint32_t)st * Lay::kTile >> 4);
+      for (int kk = 0; kk < D / 16; ++kk)
+        tc_mma_ss(tS(i), a0 + (((kk / 4) * kRegionQ + (kk % 4) * 32) >> 4),
+                  b0 + (((kk / 4) * kRegionKV + (kk % 4) * 32) >> 4), kIdQK, kk > 0 ? 1u : 0u);
+      tc_commit(bar(B_SFULL + i));
+    };
+    auto issue_pv = [&](int i, int st, bool first) {
+      const uint64_t b0 = dV + ((uint32_t)st * Lay::kTile >> 4);
 #pragma unroll
-        for (int kk = 0; kk < BN / 16; ++kk)
-          tc_mma_ts(tO(i), tS(i) + kk * 8, b0 + ((kk * 2048) >> 4), kIdPV, (!first || kk > 0) ? 1u : 0u);
-      };
-      Ring<NST> rk;                  // runs over the elements K0 V0 K1 V1 ...
-      uint32_t qn = 0, pn[2] = {0, 0};
-      bool ok = true;
-      for (int ii = i0; ok && ii < i1; ++ii) {
-        const PromptItemDev it = p.items[ii];
-        const PromptReqDev rq = p.reqs[it.req];
-        const int cnt[2] = {tile_count(it, rq, p.tpt, 0), tile_count(it, rq, p.tpt, 1)};
-        Ring<NST> k = rk;
-        if (!wait_or_abort(bar(B_QFULL), qn & 1u, p.err, abort_flag)) { ok = false; break; }
-        ++qn;
-        if (!wait_or_abort(bar(B_RFULL + k.st), k.ph, p.err, abort_flag)) { ok = false; break; }
-        tc_fence_after();
+      for (int kk = 0; kk < BN / 16; ++kk)
+        tc_mma_ts(tO(i), tS(i) + kk * 8, b0 + ((kk * 2048) >> 4), kIdPV, (!first || kk > 0) ? 1u : 0u);
+    };
+    Ring<NST> k;                   // the next element: K0 V0 K1 V1 ...
+    uint32_t qn = 0, pn[2] = {0, 0};
+    bool ok = true;
+    const int u0 = uniform(i0), u1 = uniform(i1);
+    for (int ii = u0; ok && ii < u1; ++ii) {
+      const PromptItemDev it = p.items[ii];
+      const PromptReqDev rq = p.reqs[it.req];
+      const int ntile = uniform(it.ntile);
+      const int cnt[2] = {uniform(tile_count(it, rq, p.tpt, 0)), uniform(tile_count(it, rq, p.tpt, 1))};
+      if (!wait(B_QFULL, qn & 1u) || !wait(B_RFULL + k.st, k.ph)) { ok = false; break; }
+      ++qn;
+      tc_fence_after();
+      if (elect_one()) {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          if (cnt[i] > 0) {
-            issue_s(i, k.st);
-            tc_commit(bar(B_SFULL + i));
-          }
+          if (cnt[i] > 0) issue_s(i, k.st);
         tc_commit(bar(B_REMPTY + k.st));
-        if (it.ntile == 1) tc_commit(bar(B_QEMPTY));
-        for (int j = 0; ok && j < it.ntile; ++j) {
-          Ring<NST> v = k;
-          v.next();
-          k = v;
-          k.next();
-          const bool more = j + 1 < it.ntile;
-          bool have_k = false;
-          if (!wait_or_abort(bar(B_RFULL + v.st), v.ph, p.err, abort_flag)) { ok = false; break; }
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            if (j >= cnt[i]) continue;
-            if (!wait_or_abort(bar(B_PFULL + i), pn[i] & 1u, p.err, abort_flag)) { ok = false; break; }
-            ++pn[i];
-            tc_fence_after();
-            issue_pv(i, v.st, j == 0);
-            if (j + 1 < cnt[i]) {
-              if (!have_k) {
-                if (!wait_or_abort(bar(B_RFULL + k.st), k.ph, p.err, abort_flag)) { ok = false; break; }
-                tc_fence_after();
-                have_k = true;
-              }
-              issue_s(i, k.st);
-              tc_commit(bar(B_SFULL + i));
-            } else {
-              tc_commit(bar(B_OFULL + i));
-            }
-          }
-          if (!ok) break;
-          tc_commit(bar(B_REMPTY + v.st));
-          if (more) {
-            tc_commit(bar(B_REMPTY + k.st));
-            if (j + 2 == it.ntile) tc_commit(bar(B_QEMPTY));
-          }
-        }
-        rk = k;
+        if (ntile == 1) tc_commit(bar(B_QEMPTY));
       }
-      // arrives once every MMA issued above has finished, aborted or not
-      tc_commit(bar(B_FINAL));
+      __syncwarp();
+      for (int j = 0; ok && j < ntile; ++j) {
+        Ring<NST> v = k;
+        v.next();
+        k = v;
+        k.next();
+        const bool last = j + 1 == ntile;
+        // both operands before P: they are there long before it, and nothing waits after it
+        if (!wait(B_RFULL + v.st, v.ph) || (!last && !wait(B_RFULL + k.st, k.ph))) { ok = false; break; }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (j >= cnt[i]) continue;
+          if (!wait(B_PFULL + i, pn[i] & 1u)) { ok = false; break; }
+          ++pn[i];
+          tc_fence_after();
+          if (elect_one()) {
+            issue_pv(i, v.st, j == 0);
+            // S(j+1) over P(j), once the product has read it (one thread's MMAs run in order)
+            if (j + 1 < cnt[i]) issue_s(i, k.st);
+            else tc_commit(bar(B_OFULL + i));
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (elect_one()) {
+          tc_commit(bar(B_REMPTY + v.st));
+          if (!last) tc_commit(bar(B_REMPTY + k.st));
+          if (j + 2 == ntile) tc_commit(bar(B_QEMPTY));
+        }
+        __syncwarp();
+      }
     }
+    // arrives once every MMA issued above has finished, aborted or not
+    if (elect_one()) tc_commit(bar(B_FINAL));
+    __syncwarp();
   } else if (warp < 4) {
     // ----------------------- COLD gather and V tile scan -----------------------
-    const int hw = warp - 2, ht = threadIdx.x - 64;
     constexpr int kChunks = D / 8;               // 16-byte chunks per row
     constexpr int kRowsPerCopy = 32 / kChunks;   // rows per warp instruction
+    const int row0 = (warp - 2) * 64;            // this warp's rows of a tile
     const int ch = lane % kChunks, sub = lane / kChunks;
     Ring<NST> ring;
     uint32_t scan_ph = 0;
-    int pending = -1;                            // stage copied but not announced
+    int pending = -1;                            // stage this warp copied to but has not announced
     bool ok = true;
-    auto helper_sync = [&]() { asm volatile("bar.sync %0, %1;" ::"n"(kHelperBar), "n"(kHelperThreads) : "memory"); };
-    auto announce = [&](int st) {                // the copies into st have landed (this thread's)
+    auto announce = [&](int st) {                // this warp's rows of stage st are written
       fence_async_shared();
-      helper_sync();
-      if (ht == 0) mbar_arrive(bar(B_RFULL + st));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_RFULL + st));
     };
     auto flush = [&]() {
       if (pending >= 0) {
@@ -404,43 +484,49 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         pending = -1;
       }
     };
-    // waits of the two warps end alike: both give up when the CTA is aborted
-    auto wait_all = [&](uint32_t b, uint32_t parity) {
-      return __all_sync(0xffffffffu, wait_or_abort(b, parity, p.err, abort_flag)) != 0;
-    };
     for (int ii = i0; ok && ii < i1; ++ii) {
       const PromptItemDev it = p.items[ii];
       const PromptReqDev rq = p.reqs[it.req];
       const int nctx = rq.nt_hot + rq.nt_cold;
-      int slot[2] = {-1, -1};                    // slots of rows 64 hw + lane and 64 hw + 32 + lane
-      for (int j = 0; ok && j < 2 * it.ntile; ++j) {
+      // block ids of rows row0 + lane and row0 + 32 + lane of COLD tile t, fetched one tile ahead
+      int id[2] = {-1, -1}, slot[2] = {-1, -1};
+      auto fetch_ids = [&](int t) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int pos = (t - rq.nt_hot) * BN + row0 + u * 32 + lane;
+          id[u] = t >= rq.nt_hot && t < nctx && t < it.tile0 + it.ntile && pos < rq.ctx
+                      ? p.block_table[(int64_t)rq.row * p.max_blocks + pos / p.page]
+                      : -1;
+        }
+      };
+      fetch_ids(max(it.tile0, rq.nt_hot));
+      for (int j = 0; j < 2 * it.ntile; ++j) {
         const int t = it.tile0 + (j >> 1);
         const bool is_v = j & 1;
         const int st = ring.st;
         const uint32_t ph = ring.ph;
         ring.next();
-        if (t >= rq.nt_hot && t < nctx) {
+        const bool cold = t >= rq.nt_hot && t < nctx;
+        if (!cold) flush();    // before anything that could wait for the copied tile to be used
+        if (!wait(B_REMPTY + st, ph ^ 1u)) { ok = false; break; }
+        const uint32_t tile = sR + (uint32_t)st * Lay::kTile;
+        if (cold) {
           if (!is_v) {
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-              const int pos = (t - rq.nt_hot) * BN + hw * 64 + u * 32 + lane;
-              slot[u] = -1;
-              if (pos < rq.ctx) {
-                const int64_t blk = p.block_table[(int64_t)rq.row * p.max_blocks + pos / p.page];
-                if (blk >= 0 && blk < p.cold_blocks)
-                  slot[u] = (int)(blk * p.page + pos % p.page);
-                else
-                  report_error(p.err, kErrBounds);
-              }
+              const int pos = (t - rq.nt_hot) * BN + row0 + u * 32 + lane;
+              const bool in = pos < rq.ctx;
+              slot[u] = in && id[u] >= 0 && id[u] < p.cold_blocks ? id[u] * p.page + pos % p.page : -1;
+              if (in && slot[u] < 0) report_error(p.err, kErrBounds);
             }
+            fetch_ids(t + 1);
           }
-          if (!wait_all(bar(B_REMPTY + st), ph ^ 1u)) { ok = false; break; }
           const uint16_t* src0 = (is_v ? p.cold_v : p.cold_k) + ((int64_t)p.layer * p.cold_slots * p.Hkv + it.head) * D + ch * 8;
-          const uint32_t dst0 = sR + (uint32_t)st * Lay::kTile + (uint32_t)(ch >> 3) * kRegionKV;
+          const uint32_t dst0 = tile + (uint32_t)(ch >> 3) * kRegionKV;
 #pragma unroll 8
-          for (int r0 = 0; r0 < 64; r0 += kRowsPerCopy) {
-            const int row = hw * 64 + r0 + sub;
-            const int s = __shfl_sync(0xffffffffu, slot[r0 >> 5], (r0 & 31) + sub);
+          for (int r = 0; r < 64; r += kRowsPerCopy) {
+            const int row = row0 + r + sub;
+            const int s = __shfl_sync(0xffffffffu, slot[r >> 5], (r & 31) + sub);
             cp_async16_or_zero(dst0 + row * 128 + (((ch & 7) ^ (row & 7)) << 4),
                                src0 + (int64_t)max(s, 0) * p.Hkv * D, s >= 0);
           }
@@ -450,19 +536,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             announce(pending);
           }
           pending = st;
-          continue;
-        }
-        flush();    // before anything that could wait for the copied tile to be used
-        if (!wait_all(bar(B_REMPTY + st), ph ^ 1u)) { ok = false; break; }
-        if (is_v && scanned(it, rq, t)) {
-          if (!wait_all(bar(B_RSCAN + st), scan_ph >> st & 1u)) { ok = false; break; }
+        } else if (is_v && scanned(it, rq, t)) {
+          if (!wait(B_RSCAN + st, scan_ph >> st & 1u)) { ok = false; break; }
           scan_ph ^= 1u << st;
           const bool hot = t < rq.nt_hot;
           const int key0 = (hot ? t : t - nctx) * BN;
           const int end = hot ? rq.lp : rq.n;
-          const uint32_t tile = sR + (uint32_t)st * Lay::kTile;
 #pragma unroll 1
-          for (int row = ht; row < BN; row += kHelperThreads) {
+          for (int row = row0 + lane; row < row0 + 64; row += 32) {
             const int key = key0 + row;
             bool zero = key >= end;
             if (!zero && !hot && key > it.tok0) {
@@ -497,99 +578,138 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const int tr = row / p.G, hr = row % p.G;     // token within the Q tile, query head within the group
+    const uint32_t tSr = tS(qi) + lane_off, tOr = tO(qi) + lane_off;
     uint32_t sn = 0, on = 0;
     bool ok = true;
     for (int ii = i0; ok && ii < i1; ++ii) {
-      const PromptItemDev it = p.items[ii];
-      const PromptReqDev rq = p.reqs[it.req];
-      const int nctx = rq.nt_hot + rq.nt_cold;
-      const int cnt = tile_count(it, rq, p.tpt, qi);
-      const int tk = it.tok0 + qi * p.tpt + tr;
-      const bool valid = tr < p.tpt && tk < rq.n;
-      const int seen = min(tk, rq.n - 1);         // rows of no token mask like the last one
-      const int qh = it.head * p.G + hr;
-      float m_used = -INFINITY, l = 0.f;
-      for (int j = 0; ok && j < cnt; ++j) {
+      int cnt;
+      // tiles with masked places, counted from the item's first: the last HOT and COLD ones and
+      // those on the diagonal; how many of its keys the row sees there
+      int j_hot, j_cold, j_new, lim_hot, lim_cold, lim_new;
+      {
+        const PromptItemDev it = p.items[ii];
+        const PromptReqDev rq = p.reqs[it.req];
+        const int nctx = rq.nt_hot + rq.nt_cold, a = it.tok0 + qi * p.tpt;
+        cnt = tile_count(it, rq, p.tpt, qi);
+        lim_hot = rq.lp % BN;
+        lim_cold = rq.ctx % BN;
+        j_hot = rq.lp % BN ? rq.nt_hot - 1 - it.tile0 : -1;
+        j_cold = rq.ctx % BN ? nctx - 1 - it.tile0 : -1;
+        j_new = nctx - it.tile0 + (a + 1) / BN;
+        // rows of no token mask like the last one
+        lim_new = min(a + tr, rq.n - 1) + 1 + (nctx - it.tile0) * BN;
+      }
+      // m: the reference of every exponent so far (-inf: no key seen), part: the last tile's sum, l: the row's
+      float m = -INFINITY, part = 0.f, l = 0.f;
+      bool adjust = true;                         // some row of the warp needs another reference
+      // raise the reference to m_new: O and l hold the keys so far scaled by 2^-m
+      auto raise = [&](float m_new, bool have_o) {
+        const float f = m == -INFINITY ? 1.f : ex2(m - m_new);
+        if (have_o) {
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            float o[32];
+            tmem_ld32(tOr + c, o);
+            tc_wait_ld();
+            tie32(o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] *= f;
+            tmem_st32(tOr + c, o);
+          }
+          tc_wait_st();
+        }
+        l *= f;
+        m = m_new;
+      };
+      for (int j = 0; j < cnt; ++j) {
         // warp-uniform: a lane that gave up takes its whole warp out of the loop
-        if (!__all_sync(0xffffffffu, wait_or_abort(bar(B_SFULL + qi), sn & 1u, p.err, abort_flag))) { ok = false; break; }
+        if (!wait(B_SFULL + qi, sn & 1u)) { ok = false; break; }
         ++sn;
         tc_fence_after();
-        float s[BN];
+        int lim = BN;
+        if (j == j_hot || j == j_cold || j >= j_new)
+          lim = j == j_hot ? lim_hot : j == j_cold ? lim_cold : lim_new - j * BN;
+        const bool masked = __any_sync(0xffffffffu, lim < BN);
+        auto mask = [&](float* s, int c0) {
+          if (masked) {
 #pragma unroll
-        for (int c = 0; c < BN / 32; ++c) tmem_ld32(tS(qi) + c * 32 + lane_off, s + c * 32);
-        tc_wait_ld();
-        const int t = it.tile0 + j;
-        const int lim = t < rq.nt_hot ? rq.lp - t * BN
-                        : t < nctx    ? rq.ctx - (t - rq.nt_hot) * BN
-                                      : seen + 1 - (t - nctx) * BN;
-        if (__any_sync(0xffffffffu, lim < BN)) {
-#pragma unroll
-          for (int c = 0; c < BN; ++c) s[c] = c < lim ? s[c] : -INFINITY;
-        }
-        float mx8[8];
-#pragma unroll
-        for (int c = 0; c < 8; ++c) mx8[c] = s[c];
-#pragma unroll
-        for (int c = 8; c + 16 <= BN; c += 16)
-#pragma unroll
-          for (int k = 0; k < 8; ++k) mx8[k] = fmax3(mx8[k], s[c + k], s[c + 8 + k]);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) mx8[k] = fmaxf(mx8[k], s[BN - 8 + k]);
-        float mx = fmaxf(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(fmax3(mx8[3], mx8[4], mx8[5]), mx8[6], mx8[7]));
-        mx *= p.scale_log2;
-        if (__any_sync(0xffffffffu, mx > m_used + 8.0f)) {
-          const float m_new = fmaxf(m_used, mx);
-          if (j > 0) {
-            // S(j) completed after PV(j-1), so O holds keys 0..j-1 scaled by 2^-m_used
-            const float f = m_new == -INFINITY ? 1.f : ex2(m_used - m_new);
-#pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              float o[32];
-              tmem_ld32(tO(qi) + c * 32 + lane_off, o);
-              tc_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] *= f;
-              tmem_st32(tO(qi) + c * 32 + lane_off, o);
-            }
-            l *= f;
+            for (int e = 0; e < 32; ++e) s[e] = c0 + e < lim ? s[e] : -INFINITY;
           }
-          m_used = m_new;
+        };
+        // the row's maximum in this tile, in log2 units, rounded up: no exponent against it is above 0
+        auto maximum = [&]() {
+          float mx = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < BN; c += 32) {
+            float s[32];
+            tmem_ld32(tSr + c, s);
+            tc_wait_ld();
+            tie32(s);
+            mask(s, c);
+            mx = fmaxf(mx, max32(s));
+          }
+          return __fmul_ru(mx, p.scale_log2);
+        };
+        // S(j) completed after PV(j-1), so O may be rescaled here
+        if (adjust) {
+          float m_new = part > 256.f ? m + __log2f(part) : m;
+          if (__any_sync(0xffffffffu, m == -INFINITY)) {
+            const float mx = maximum();
+            if (m == -INFINITY) m_new = mx;
+          }
+          raise(m_new, j > 0);
         }
-        // a row whose keys so far are all masked keeps m = -inf: its exponents are -inf - 0
-        const float m_sub = m_used == -INFINITY ? 0.f : m_used;
-        const uint64_t sc2 = f2pack(p.scale_log2, p.scale_log2), nm2 = f2pack(-m_sub, -m_sub);
         uint32_t pk[BN / 2];
-        uint64_t sum4[4] = {0, 0, 0, 0};
+        while (true) {
+          const float m_sub = m == -INFINITY ? 0.f : m;     // a row that sees no key yet: -inf - 0
+          const uint64_t sc2 = f2pack(p.scale_log2, p.scale_log2), nm2 = f2pack(-m_sub, -m_sub);
+          uint64_t sum4[4] = {0, 0, 0, 0};
+          float sa[32], sb[32];
+          tmem_ld32(tSr, sa);
 #pragma unroll
-        for (int c = 0; c < BN / 2; ++c) {
-          float xa, xb;
-          f2unpack(ffma2(f2pack(s[2 * c], s[2 * c + 1]), sc2, nm2), xa, xb);
-          const float a = ex2(xa), b2 = ex2(xb);
-          sum4[c & 3] = fadd2(sum4[c & 3], f2pack(a, b2));
-          pk[c] = pack_bf16x2(a, b2);
-        }
-        {
+          for (int c = 0; c < BN; c += 64) {
+            tc_wait_ld();
+            tie32(sa);
+            tmem_ld32(tSr + c + 32, sb);
+            mask(sa, c);
+            exp32(sa, pk + c / 2, sum4, sc2, nm2);
+            tc_wait_ld();
+            tie32(sb);
+            if (c + 64 < BN) tmem_ld32(tSr + c + 64, sa);
+            mask(sb, c + 32);
+            exp32(sb, pk + c / 2 + 16, sum4, sc2, nm2);
+          }
           float s0, s1, s2, s3;
           f2unpack(fadd2(sum4[0], sum4[1]), s0, s1);
           f2unpack(fadd2(sum4[2], sum4[3]), s2, s3);
-          l += (s0 + s1) + (s2 + s3);
+          const bool again = part != -1.f;
+          part = (s0 + s1) + (s2 + s3);
+          if (!again || !__any_sync(0xffffffffu, part > 0x1p64f)) break;
+          // far above the reference: raise it and take the tile again (its S is still there)
+          raise(fmaxf(m, maximum()), j > 0);
+          part = -1.f;
         }
+        l += part;
 #pragma unroll
-        for (int c = 0; c < BN / 64; ++c)
-          tmem_st32(tS(qi) + c * 32 + lane_off, reinterpret_cast<const float*>(pk + c * 32));
+        for (int c = 0; c < BN / 2; c += 32) tmem_st32(tSr + c, reinterpret_cast<const float*>(pk + c));
         tc_wait_st();
         tc_fence_before();
         mbar_arrive(bar(B_PFULL + qi));
+        adjust = __any_sync(0xffffffffu, m == -INFINITY || part > 256.f);
       }
       if (!ok) break;
+      const PromptItemDev it = p.items[ii];
+      const PromptReqDev rq = p.reqs[it.req];
+      const int tk = it.tok0 + qi * p.tpt + tr, qh = it.head * p.G + hr;
+      const bool valid = tr < p.tpt && tk < rq.n;
       if (cnt > 0) {
         if (!__all_sync(0xffffffffu, wait_or_abort(bar(B_OFULL + qi), on & 1u, p.err, abort_flag))) { ok = false; break; }
         ++on;
         tc_fence_after();
-        if (__any_sync(0xffffffffu, *hidden_flag)) add_hidden_values<D>(p, it, rq, tk, qh, valid, m_used, tO(qi) + lane_off);
+        if (__any_sync(0xffffffffu, *hidden_flag)) add_hidden_values<D>(p, it, rq, tk, qh, valid, m, tOr);
       }
       const float inv = l > 0.f || l != l ? 1.f / l : 0.f;   // no key in this range: O = 0, LSE = -inf
-      const float lse2 = m_used + __log2f(l);
+      const float lse2 = m + __log2f(l);
       const int64_t prow = (int64_t)it.entry * 256 + qi * BM + row;
       const int64_t orow = (int64_t)(rq.t0 + tk);
       if (valid) {
@@ -600,18 +720,19 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       }
       if (cnt > 0) {
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
+        for (int c = 0; c < D; c += 32) {
           float o[32];
-          tmem_ld32(tO(qi) + c * 32 + lane_off, o);
+          tmem_ld32(tOr + c, o);
           tc_wait_ld();
+          tie32(o);
           if (valid && it.entry >= 0) {
-            uint4* dst = reinterpret_cast<uint4*>(p.part_o + prow * D + c * 32);
+            uint4* dst = reinterpret_cast<uint4*>(p.part_o + prow * D + c);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
               dst[e] = make_uint4(__float_as_uint(o[4 * e] * inv), __float_as_uint(o[4 * e + 1] * inv),
                                   __float_as_uint(o[4 * e + 2] * inv), __float_as_uint(o[4 * e + 3] * inv));
           } else if (valid) {
-            uint4* dst = reinterpret_cast<uint4*>(p.out + orow * p.out_stride + qh * D + c * 32);
+            uint4* dst = reinterpret_cast<uint4*>(p.out + orow * p.out_stride + qh * D + c);
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               dst[e] = make_uint4(pack_bf16x2(o[8 * e] * inv, o[8 * e + 1] * inv),
@@ -709,7 +830,7 @@ namespace {
 template <int D>
 int launch_t(const Params& pp, const PromptPlan* pl, const uint8_t* base, cudaStream_t st) {
   auto kern = prompt_kernel<D>;
-  constexpr size_t smem = 1024 + Layout<D>::kData + kCtlBytes;
+  constexpr size_t smem = Layout<D>::kData + kCtlBytes;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return (int)e;
   const int ctas = (int)pl->cta_begin.size() - 1;
