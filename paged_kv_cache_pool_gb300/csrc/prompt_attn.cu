@@ -20,7 +20,7 @@
 // one tile's softmax runs under the other's products.  A tile's two products take
 // 1024 tensor cycles, so its softmax has to come back in about as long; there is
 // no pass for the maximum: exponents are taken against a reference that is the
-// maximum of the row's first tile, raised between tiles when a tile's sum passed
+// maximum over the row's first keys, raised between tiles when a tile's sum passed
 // 2^8 and within one (its exponentials are then done again) when it passed 2^64,
 // so that every value stays in fp32 and bf16 range.  O and LSE use the same
 // reference as P, so this changes neither beyond fp32 rounding.
@@ -42,11 +42,15 @@
 // the item; the rows that do see such a key add its term in the epilogue
 // (add_hidden_values, never taken for finite values).
 //
-// Warp roles (384 threads): 0 TMA, 1 MMA and tensor memory, 2-3 gather and
-// scan, 4-7 and 8-11 softmax of Q tiles 0 and 1.
+// Warp roles (512 threads): 0 TMA, 1 MMA and tensor memory, 2-3 and 13-14 gather
+// and scan, 4-7 and 8-11 softmax of Q tiles 0 and 1, 12 operand relay, 15 idle.  The
+// block starts with 128 registers a thread; the softmax warpgroups take 176 and
+// the other two warpgroups give theirs up to 80 (a spill in the softmax loop was
+// measured to halve the kernel's speed).
 #include <cuda.h>
 
 #include <cmath>
+#include <type_traits>
 
 #include "prefix_body.cuh"
 #include "prompt.h"
@@ -63,7 +67,9 @@ using prefix::kTmemCols;
 using prefix::sdesc;
 using prefix::tc_mma_ts;
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 512;
+constexpr int kSoftmaxRegs = 176, kOtherRegs = 80;   // 128 * (2 * 176 + 2 * 80) = 512 * 128
+
 
 struct Params {
   CUtensorMap tq, tk, tv;         // the call's packed tensors
@@ -83,6 +89,7 @@ struct Params {
   int64_t cold_blocks;
   int32_t page, max_blocks;
   int32_t Hq, Hkv, G, tpt, layer;
+  bool out_wide;                  // rows of out are 32-byte aligned
   int32_t* err;
   float scale_log2;               // log2(e) / sqrt(d)
 };
@@ -111,11 +118,23 @@ enum : int {
 constexpr uint32_t kCtlTmemSlot = B_COUNT * 8;
 constexpr uint32_t kCtlAbort = kCtlTmemSlot + 4;
 constexpr uint32_t kCtlHidden = kCtlAbort + 4;   // an infinity or NaN was hidden in this CTA's V tiles
+// the records of the item whose Q tiles are in shared memory, and of the next: the TMA
+// thread passes them on, since every role's own two dependent reads would stand between
+// one item and the next
+struct Slot {
+  PromptItemDev it;
+  PromptReqDev rq;
+};
+constexpr uint32_t kCtlSlots = 288;
 constexpr uint32_t kCtlBytes = 512;
-static_assert(kCtlHidden + 4 <= kCtlBytes, "prompt control block");
+static_assert(kCtlHidden + 4 <= kCtlSlots && kCtlSlots + 2 * sizeof(Slot) <= kCtlBytes, "prompt control block");
+constexpr int kSlotReaders = 10;          // MMA, relay and softmax warps
 // dynamic shared memory starts 1024-byte aligned (checked by the kernel)
 static_assert(Layout<128>::kData + kCtlBytes <= 232448 && Layout<64>::kData + kCtlBytes <= 232448, "shared memory");
 
+__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
+  asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.shared::cta.b64 st, [%0], %1;\n\t}" ::"r"(bar), "r"(n) : "memory");
+}
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* tmap, int x, int y, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
@@ -226,6 +245,19 @@ __device__ __forceinline__ bool elect_one() {
   return e != 0;
 }
 
+// 32 bytes of a row: one store where the address allows it (a whole sector: half stores of
+// every row doubled the epilogue's time)
+__device__ __forceinline__ void store32(void* dst, const uint32_t* w, bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
 // keeps uses of the registers of a tcgen05.ld behind its wait
 __device__ __forceinline__ void tie32(float* v) {
 #pragma unroll
@@ -247,10 +279,10 @@ __device__ __forceinline__ float max32(const float* s) {
   return fmaxf(fmax3(a[0], a[1], a[2]), a[3]);
 }
 
-// 2^(s * scale - m) of 32 scores as 16 bf16 pairs, added to the running sums in fp32
-__device__ __forceinline__ void exp32(const float* s, uint32_t* pk, uint64_t* sum4, uint64_t sc2, uint64_t nm2) {
+// 2^(s * scale - m) of 64 scores as 32 bf16 pairs, added to the running sums in fp32
+__device__ __forceinline__ void exp64(const float* s, uint32_t* pk, uint64_t* sum4, uint64_t sc2, uint64_t nm2) {
 #pragma unroll
-  for (int c = 0; c < 16; ++c) {
+  for (int c = 0; c < 32; ++c) {
     float xa, xb;
     f2unpack(ffma2(f2pack(s[2 * c], s[2 * c + 1]), sc2, nm2), xa, xb);
     const float a = ex2(xa), b = ex2(xb);
@@ -275,6 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   volatile int* abort_flag = reinterpret_cast<volatile int*>(ctl_ptr + kCtlAbort);
   volatile int* hidden_flag = reinterpret_cast<volatile int*>(ctl_ptr + kCtlHidden);
   auto bar = [&](int i) { return ctl + 8u * (uint32_t)i; };
+  Slot* slots = reinterpret_cast<Slot*>(ctl_ptr + kCtlSlots);
   const uint32_t sQ = base, sR = base + Lay::kRing;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -283,16 +316,16 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     *abort_flag = 0;
     *hidden_flag = 0;
     mbar_init(bar(B_QFULL), 1);
-    mbar_init(bar(B_QEMPTY), 1);
+    mbar_init(bar(B_QEMPTY), kSlotReaders);   // the last S is done and everyone has read the slot
     mbar_init(bar(B_FINAL), 1);
     for (int s = 0; s < NST; ++s) {
       mbar_init(bar(B_REMPTY + s), 1);
-      mbar_init(bar(B_RFULL + s), 2);   // the TMA thread arrives twice, or each gather warp once
+      mbar_init(bar(B_RFULL + s), 4);   // the TMA thread arrives four times, or each gather warp once
       mbar_init(bar(B_RSCAN + s), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(B_SFULL + i), 1);
-      mbar_init(bar(B_PFULL + i), 128);
+      mbar_init(bar(B_PFULL + i), 129);   // the softmax threads and the relay
       mbar_init(bar(B_OFULL + i), 1);
     }
     fence_mbar_init();
@@ -321,6 +354,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     return __all_sync(0xffffffffu, wait_or_abort(bar(b), parity, p.err, abort_flag)) != 0;
   };
 
+  if (warp < 4 || warp >= 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
   if (warp == 0) {
     // ------------------------------ TMA producer ------------------------------
     if (lane == 0) {
@@ -329,9 +364,18 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       uint32_t in_ring = 0, in_scan = 0, full_ph = 0;  // the last load of each stage, for the drain below
       uint32_t qn = 0;
       bool ok = true;
+      Slot next = {};
+      if (i0 < i1) {
+        next.it = p.items[i0];
+        next.rq = p.reqs[next.it.req];
+      }
       for (int ii = i0; ok && ii < i1; ++ii) {
-        const PromptItemDev it = p.items[ii];
-        const PromptReqDev rq = p.reqs[it.req];
+        const PromptItemDev it = next.it;
+        const PromptReqDev rq = next.rq;
+        if (ii + 1 < i1) {
+          next.it = p.items[ii + 1];
+          next.rq = p.reqs[next.it.req];
+        }
         const int nctx = rq.nt_hot + rq.nt_cold;
         for (int j = 0; j < 2 * it.ntile; ++j) {
           const int t = it.tile0 + (j >> 1);
@@ -345,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             const bool scan = is_v && scanned(it, rq, t);
             const uint32_t b = bar((scan ? B_RSCAN : B_RFULL) + st);
             const uint32_t tile = sR + (uint32_t)st * Lay::kTile;
-            if (!scan) mbar_arrive(b);
+            if (!scan) mbar_arrive_n(b, 3);
             mbar_arrive_expect_tx(b, Lay::kTile);
             if (t < rq.nt_hot) {
               const int row = (int)(rq.hot_row + ((int64_t)p.layer * p.Hkv + it.head) * rq.lp + t * BN);
@@ -364,6 +408,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           if (j == 1) {
             // the Q tiles, once the last product with the item before has read its own
             if (!wait_or_abort(bar(B_QEMPTY), (qn & 1u) ^ 1u, p.err, abort_flag)) { ok = false; break; }
+            slots[qn & 1u].it = it;
+            slots[qn & 1u].rq = rq;
             ++qn;
             const bool two = it.tok0 + p.tpt < rq.n;
             const uint32_t q_bytes = (uint32_t)(p.tpt * p.G) * 128u * (D / 64);
@@ -413,11 +459,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     bool ok = true;
     const int u0 = uniform(i0), u1 = uniform(i1);
     for (int ii = u0; ok && ii < u1; ++ii) {
-      const PromptItemDev it = p.items[ii];
-      const PromptReqDev rq = p.reqs[it.req];
+      if (!wait(B_QFULL, qn & 1u)) { ok = false; break; }
+      const PromptItemDev it = slots[qn & 1u].it;
+      const PromptReqDev rq = slots[qn & 1u].rq;
       const int ntile = uniform(it.ntile);
       const int cnt[2] = {uniform(tile_count(it, rq, p.tpt, 0)), uniform(tile_count(it, rq, p.tpt, 1))};
-      if (!wait(B_QFULL, qn & 1u) || !wait(B_RFULL + k.st, k.ph)) { ok = false; break; }
+      if (!wait(B_RFULL + k.st, k.ph)) { ok = false; break; }
       ++qn;
       tc_fence_after();
       if (elect_one()) {
@@ -434,11 +481,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         k = v;
         k.next();
         const bool last = j + 1 == ntile;
-        // both operands before P: they are there long before it, and nothing waits after it
-        if (!wait(B_RFULL + v.st, v.ph) || (!last && !wait(B_RFULL + k.st, k.ph))) { ok = false; break; }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           if (j >= cnt[i]) continue;
+          // P, and through the relay V_j and K_(j+1)
           if (!wait(B_PFULL + i, pn[i] & 1u)) { ok = false; break; }
           ++pn[i];
           tc_fence_after();
@@ -462,11 +508,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     // arrives once every MMA issued above has finished, aborted or not
     if (elect_one()) tc_commit(bar(B_FINAL));
     __syncwarp();
-  } else if (warp < 4) {
+  } else if (warp == 2 || warp == 3 || warp == 13 || warp == 14) {
     // ----------------------- COLD gather and V tile scan -----------------------
     constexpr int kChunks = D / 8;               // 16-byte chunks per row
     constexpr int kRowsPerCopy = 32 / kChunks;   // rows per warp instruction
-    const int row0 = (warp - 2) * 64;            // this warp's rows of a tile
+    const int row0 = (warp < 4 ? warp - 2 : warp - 11) * 32;   // this warp's rows of a tile
     const int ch = lane % kChunks, sub = lane / kChunks;
     Ring<NST> ring;
     uint32_t scan_ph = 0;
@@ -488,16 +534,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       const PromptItemDev it = p.items[ii];
       const PromptReqDev rq = p.reqs[it.req];
       const int nctx = rq.nt_hot + rq.nt_cold;
-      // block ids of rows row0 + lane and row0 + 32 + lane of COLD tile t, fetched one tile ahead
-      int id[2] = {-1, -1}, slot[2] = {-1, -1};
+      // block id of row row0 + lane of COLD tile t, fetched one tile ahead
+      int id = -1, slot = -1;
       auto fetch_ids = [&](int t) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int pos = (t - rq.nt_hot) * BN + row0 + u * 32 + lane;
-          id[u] = t >= rq.nt_hot && t < nctx && t < it.tile0 + it.ntile && pos < rq.ctx
-                      ? p.block_table[(int64_t)rq.row * p.max_blocks + pos / p.page]
-                      : -1;
-        }
+        const int pos = (t - rq.nt_hot) * BN + row0 + lane;
+        id = t >= rq.nt_hot && t < nctx && t < it.tile0 + it.ntile && pos < rq.ctx
+                 ? p.block_table[(int64_t)rq.row * p.max_blocks + pos / p.page]
+                 : -1;
       };
       fetch_ids(max(it.tile0, rq.nt_hot));
       for (int j = 0; j < 2 * it.ntile; ++j) {
@@ -512,21 +555,18 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         const uint32_t tile = sR + (uint32_t)st * Lay::kTile;
         if (cold) {
           if (!is_v) {
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const int pos = (t - rq.nt_hot) * BN + row0 + u * 32 + lane;
-              const bool in = pos < rq.ctx;
-              slot[u] = in && id[u] >= 0 && id[u] < p.cold_blocks ? id[u] * p.page + pos % p.page : -1;
-              if (in && slot[u] < 0) report_error(p.err, kErrBounds);
-            }
+            const int pos = (t - rq.nt_hot) * BN + row0 + lane;
+            const bool in = pos < rq.ctx;
+            slot = in && id >= 0 && id < p.cold_blocks ? id * p.page + pos % p.page : -1;
+            if (in && slot < 0) report_error(p.err, kErrBounds);
             fetch_ids(t + 1);
           }
           const uint16_t* src0 = (is_v ? p.cold_v : p.cold_k) + ((int64_t)p.layer * p.cold_slots * p.Hkv + it.head) * D + ch * 8;
           const uint32_t dst0 = tile + (uint32_t)(ch >> 3) * kRegionKV;
 #pragma unroll 8
-          for (int r = 0; r < 64; r += kRowsPerCopy) {
+          for (int r = 0; r < 32; r += kRowsPerCopy) {
             const int row = row0 + r + sub;
-            const int s = __shfl_sync(0xffffffffu, slot[r >> 5], (r & 31) + sub);
+            const int s = __shfl_sync(0xffffffffu, slot, r + sub);
             cp_async16_or_zero(dst0 + row * 128 + (((ch & 7) ^ (row & 7)) << 4),
                                src0 + (int64_t)max(s, 0) * p.Hkv * D, s >= 0);
           }
@@ -542,29 +582,27 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           const bool hot = t < rq.nt_hot;
           const int key0 = (hot ? t : t - nctx) * BN;
           const int end = hot ? rq.lp : rq.n;
-#pragma unroll 1
-          for (int row = row0 + lane; row < row0 + 64; row += 32) {
-            const int key = key0 + row;
-            bool zero = key >= end;
-            if (!zero && !hot && key > it.tok0) {
-              uint32_t top = 0;
-#pragma unroll
-              for (int c = 0; c < kChunks; ++c) {
-                const uint4 w = lds128(tile + (c >> 3) * kRegionKV + row * 128 + (((c & 7) ^ (row & 7)) << 4));
-                // exponent bits all ones carry into the sign bit of their half
-                top |= ((w.x & 0x7F807F80u) + 0x00800080u) | ((w.y & 0x7F807F80u) + 0x00800080u) |
-                       ((w.z & 0x7F807F80u) + 0x00800080u) | ((w.w & 0x7F807F80u) + 0x00800080u);
-              }
-              if (top & 0x80008000u) {
-                zero = true;
-                *hidden_flag = 1;
-              }
+          const int row = row0 + lane, key = key0 + row;
+          const uint32_t src = tile + row * 128;
+          bool zero = key >= end;
+          if (!zero && !hot && key > it.tok0) {
+            uint32_t top = 0;
+#pragma unroll 4
+            for (int c = 0; c < kChunks; ++c) {
+              const uint4 w = lds128(src + (c >> 3) * kRegionKV + (((c & 7) ^ (row & 7)) << 4));
+              // exponent bits all ones carry into the sign bit of their half
+              top |= ((w.x & 0x7F807F80u) + 0x00800080u) | ((w.y & 0x7F807F80u) + 0x00800080u) |
+                     ((w.z & 0x7F807F80u) + 0x00800080u) | ((w.w & 0x7F807F80u) + 0x00800080u);
             }
-            if (zero) {
-#pragma unroll
-              for (int c = 0; c < kChunks; ++c)
-                sts128(tile + (c >> 3) * kRegionKV + row * 128 + (((c & 7) ^ (row & 7)) << 4), make_uint4(0, 0, 0, 0));
+            if (top & 0x80008000u) {
+              zero = true;
+              *hidden_flag = 1;
             }
+          }
+          if (zero) {
+#pragma unroll 4
+            for (int c = 0; c < kChunks; ++c)
+              sts128(src + (c >> 3) * kRegionKV + (((c & 7) ^ (row & 7)) << 4), make_uint4(0, 0, 0, 0));
           }
           announce(st);
         }
@@ -572,7 +610,44 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     }
     if (ok) flush();
     else cp_async_wait_all();
+  } else if (warp == 12) {
+    // ------------------------------ operand relay -------------------------------
+    // Waits for V_j and K_(j+1) and arrives for them on the barriers of P(j): the MMA
+    // warp then waits once per Q tile and key tile.  (Its own waits queue behind the
+    // MMAs that it has issued: two more cost it 500 cycles a key tile, with P ready.)
+    if (lane == 0) {
+      Ring<NST> ring;
+      uint32_t pn[2] = {0, 0};
+      bool ok = true;
+      auto full = [&]() {
+        const bool got = wait_or_abort(bar(B_RFULL + ring.st), ring.ph, p.err, abort_flag);
+        ring.next();
+        return got;
+      };
+      for (int ii = i0; ok && ii < i1; ++ii) {
+        const uint32_t qn = (uint32_t)(ii - i0) & 1u;
+        if (!wait_or_abort(bar(B_QFULL), qn, p.err, abort_flag)) break;
+        const PromptItemDev it = slots[qn].it;
+        const PromptReqDev rq = slots[qn].rq;
+        mbar_arrive(bar(B_QEMPTY));
+        const int cnt[2] = {tile_count(it, rq, p.tpt, 0), tile_count(it, rq, p.tpt, 1)};
+        ring.next();                   // K_0: the MMA warp waits for it
+        for (int j = 0; ok && j < it.ntile; ++j) {
+          ok = full() && (j + 1 == it.ntile || full());
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (ok && j < cnt[i]) {
+              // one arrival a phase: not before the last P's phase is over
+              if (pn[i] > 0) ok = wait_or_abort(bar(B_PFULL + i), (pn[i] - 1) & 1u, p.err, abort_flag);
+              ++pn[i];
+              if (ok) mbar_arrive(bar(B_PFULL + i));
+            }
+        }
+      }
+    }
+  }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     // ---------------------- softmax / correction / epilogue ---------------------
     const int qi = (warp - 4) >> 2;
     const int row = (warp & 3) * 32 + lane;
@@ -582,23 +657,23 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     uint32_t sn = 0, on = 0;
     bool ok = true;
     for (int ii = i0; ok && ii < i1; ++ii) {
-      int cnt;
+      const uint32_t qn = (uint32_t)(ii - i0) & 1u;
+      if (!wait(B_QFULL, qn)) { ok = false; break; }
+      const PromptItemDev it = slots[qn].it;
+      const PromptReqDev rq = slots[qn].rq;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_QEMPTY));
+      const int nctx = rq.nt_hot + rq.nt_cold;
+      const int cnt = tile_count(it, rq, p.tpt, qi);
+      const int tk = it.tok0 + qi * p.tpt + tr, qh = it.head * p.G + hr;
+      const bool valid = tr < p.tpt && tk < rq.n;
       // tiles with masked places, counted from the item's first: the last HOT and COLD ones and
-      // those on the diagonal; how many of its keys the row sees there
-      int j_hot, j_cold, j_new, lim_hot, lim_cold, lim_new;
-      {
-        const PromptItemDev it = p.items[ii];
-        const PromptReqDev rq = p.reqs[it.req];
-        const int nctx = rq.nt_hot + rq.nt_cold, a = it.tok0 + qi * p.tpt;
-        cnt = tile_count(it, rq, p.tpt, qi);
-        lim_hot = rq.lp % BN;
-        lim_cold = rq.ctx % BN;
-        j_hot = rq.lp % BN ? rq.nt_hot - 1 - it.tile0 : -1;
-        j_cold = rq.ctx % BN ? nctx - 1 - it.tile0 : -1;
-        j_new = nctx - it.tile0 + (a + 1) / BN;
-        // rows of no token mask like the last one
-        lim_new = min(a + tr, rq.n - 1) + 1 + (nctx - it.tile0) * BN;
-      }
+      // those on the diagonal; how many of its keys the row sees there (rows of no token: as the last one)
+      const int j_hot = rq.lp % BN ? rq.nt_hot - 1 - it.tile0 : -1;
+      const int j_cold = rq.ctx % BN ? nctx - 1 - it.tile0 : -1;
+      const int j_new = nctx - it.tile0 + (it.tok0 + qi * p.tpt + 1) / BN;
+      const int lim_hot = rq.lp % BN, lim_cold = rq.ctx % BN;
+      const int lim_new = min(tk, rq.n - 1) + 1 + (nctx - it.tile0) * BN;
       // m: the reference of every exponent so far (-inf: no key seen), part: the last tile's sum, l: the row's
       float m = -INFINITY, part = 0.f, l = 0.f;
       bool adjust = true;                         // some row of the warp needs another reference
@@ -627,20 +702,20 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         ++sn;
         tc_fence_after();
         int lim = BN;
-        if (j == j_hot || j == j_cold || j >= j_new)
+        bool masked = false;
+        if (j == j_hot || j == j_cold || j >= j_new) {
           lim = j == j_hot ? lim_hot : j == j_cold ? lim_cold : lim_new - j * BN;
-        const bool masked = __any_sync(0xffffffffu, lim < BN);
+          masked = __any_sync(0xffffffffu, lim < BN);
+        }
         auto mask = [&](float* s, int c0) {
-          if (masked) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) s[e] = c0 + e < lim ? s[e] : -INFINITY;
-          }
+          for (int e = 0; e < 32; ++e) s[e] = c0 + e < lim ? s[e] : -INFINITY;
         };
-        // the row's maximum in this tile, in log2 units, rounded up: no exponent against it is above 0
-        auto maximum = [&]() {
+        // the row's maximum over the tile's first keys, in log2 units, rounded up: no exponent against it is above 0
+        auto maximum = [&](int keys) {
           float mx = -INFINITY;
 #pragma unroll 1
-          for (int c = 0; c < BN; c += 32) {
+          for (int c = 0; c < keys; c += 32) {
             float s[32];
             tmem_ld32(tSr + c, s);
             tc_wait_ld();
@@ -654,40 +729,52 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         if (adjust) {
           float m_new = part > 256.f ? m + __log2f(part) : m;
           if (__any_sync(0xffffffffu, m == -INFINITY)) {
-            const float mx = maximum();
+            // rows without one start from 32 keys' maximum, or the tile's where they see none of those
+            float mx = maximum(32);
+            if (__any_sync(0xffffffffu, mx == -INFINITY)) mx = maximum(BN);
             if (m == -INFINITY) m_new = mx;
           }
           raise(m_new, j > 0);
         }
         uint32_t pk[BN / 2];
-        while (true) {
+        // P and the row's sum in the tile.  Straight-line code where nothing is masked: the
+        // selections' branches between the exponentials cost a quarter of their time.
+        auto exponentials = [&](auto with_mask) {
           const float m_sub = m == -INFINITY ? 0.f : m;     // a row that sees no key yet: -inf - 0
           const uint64_t sc2 = f2pack(p.scale_log2, p.scale_log2), nm2 = f2pack(-m_sub, -m_sub);
           uint64_t sum4[4] = {0, 0, 0, 0};
-          float sa[32], sb[32];
+          float sa[64], sb[64];
           tmem_ld32(tSr, sa);
-#pragma unroll
-          for (int c = 0; c < BN; c += 64) {
-            tc_wait_ld();
-            tie32(sa);
-            tmem_ld32(tSr + c + 32, sb);
-            mask(sa, c);
-            exp32(sa, pk + c / 2, sum4, sc2, nm2);
-            tc_wait_ld();
-            tie32(sb);
-            if (c + 64 < BN) tmem_ld32(tSr + c + 64, sa);
-            mask(sb, c + 32);
-            exp32(sb, pk + c / 2 + 16, sum4, sc2, nm2);
+          tmem_ld32(tSr + 32, sa + 32);
+          tc_wait_ld();
+          tie32(sa);
+          tie32(sa + 32);
+          tmem_ld32(tSr + 64, sb);
+          tmem_ld32(tSr + 96, sb + 32);
+          if (decltype(with_mask)::value) {
+            mask(sa, 0);
+            mask(sa + 32, 32);
           }
+          exp64(sa, pk, sum4, sc2, nm2);
+          tc_wait_ld();
+          tie32(sb);
+          tie32(sb + 32);
+          if (decltype(with_mask)::value) {
+            mask(sb, 64);
+            mask(sb + 32, 96);
+          }
+          exp64(sb, pk + 32, sum4, sc2, nm2);
           float s0, s1, s2, s3;
           f2unpack(fadd2(sum4[0], sum4[1]), s0, s1);
           f2unpack(fadd2(sum4[2], sum4[3]), s2, s3);
-          const bool again = part != -1.f;
           part = (s0 + s1) + (s2 + s3);
-          if (!again || !__any_sync(0xffffffffu, part > 0x1p64f)) break;
+        };
+        if (masked) exponentials(std::true_type());
+        else exponentials(std::false_type());
+        if (__any_sync(0xffffffffu, part > 0x1p64f)) {
           // far above the reference: raise it and take the tile again (its S is still there)
-          raise(fmaxf(m, maximum()), j > 0);
-          part = -1.f;
+          raise(fmaxf(m, maximum(BN)), j > 0);
+          exponentials(std::true_type());
         }
         l += part;
 #pragma unroll
@@ -698,10 +785,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         adjust = __any_sync(0xffffffffu, m == -INFINITY || part > 256.f);
       }
       if (!ok) break;
-      const PromptItemDev it = p.items[ii];
-      const PromptReqDev rq = p.reqs[it.req];
-      const int tk = it.tok0 + qi * p.tpt + tr, qh = it.head * p.G + hr;
-      const bool valid = tr < p.tpt && tk < rq.n;
       if (cnt > 0) {
         if (!__all_sync(0xffffffffu, wait_or_abort(bar(B_OFULL + qi), on & 1u, p.err, abort_flag))) { ok = false; break; }
         ++on;
@@ -720,25 +803,31 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       }
       if (cnt > 0) {
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          float o[32];
+        for (int c = 0; c < D; c += 64) {
+          float o[64];
           tmem_ld32(tOr + c, o);
+          tmem_ld32(tOr + c + 32, o + 32);
           tc_wait_ld();
           tie32(o);
+          tie32(o + 32);
           if (valid && it.entry >= 0) {
-            uint4* dst = reinterpret_cast<uint4*>(p.part_o + prow * D + c);
+            float* dst = p.part_o + prow * D + c;
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              dst[e] = make_uint4(__float_as_uint(o[4 * e] * inv), __float_as_uint(o[4 * e + 1] * inv),
-                                  __float_as_uint(o[4 * e + 2] * inv), __float_as_uint(o[4 * e + 3] * inv));
+            for (int e = 0; e < 64; e += 8) {
+              uint32_t w[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) w[k] = __float_as_uint(o[e + k] * inv);
+              store32(dst + e, w, true);
+            }
           } else if (valid) {
-            uint4* dst = reinterpret_cast<uint4*>(p.out + orow * p.out_stride + qh * D + c);
+            uint16_t* dst = p.out + orow * p.out_stride + qh * D + c;
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              dst[e] = make_uint4(pack_bf16x2(o[8 * e] * inv, o[8 * e + 1] * inv),
-                                  pack_bf16x2(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
-                                  pack_bf16x2(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
-                                  pack_bf16x2(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+            for (int e = 0; e < 64; e += 16) {
+              uint32_t w[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) w[k] = pack_bf16x2(o[e + 2 * k] * inv, o[e + 2 * k + 1] * inv);
+              store32(dst + e, w, p.out_wide);
+            }
           }
           __syncwarp();
         }
@@ -920,6 +1009,7 @@ int launch_prompt(const LaunchCommon& lc, void* stream, int32_t layer, const gk_
   pp.cold_blocks = c.cold_slots / c.cold_page_size;
   pp.page = c.cold_page_size;
   pp.max_blocks = b->max_blocks;
+  pp.out_wide = (uintptr_t)b->d_out % 32 == 0 && pp.out_stride % 16 == 0;
   pp.err = lc.d_error;
   pp.scale_log2 = kLog2e / sqrtf((float)D);
   if (D == 128) return prompt::launch_t<128>(pp, pl, base, (cudaStream_t)stream);
