@@ -31,7 +31,9 @@
 // CTAs are persistent (one per SM: 512 tensor-memory columns and 224 KB of
 // shared memory) and run the lists of items that the plan balanced.  K and V tiles
 // share one ring of stages, and the loads of the next item start while the
-// softmax of the last one ends.
+// softmax of the last one ends.  The ring's element after an item's last V tile
+// stages its output: rows of 128 bytes go out whole, where each thread's own stores
+// of its row took 5800 cycles an item.
 //
 // Masked keys.  Scores are masked by selection, so whatever K holds in a masked
 // place does no harm; the product P V, though, would turn a masked 0 times an
@@ -68,7 +70,7 @@ using prefix::sdesc;
 using prefix::tc_mma_ts;
 
 constexpr int kThreads = 512;
-constexpr int kSoftmaxRegs = 176, kOtherRegs = 80;   // 128 * (2 * 176 + 2 * 80) = 512 * 128
+constexpr int kSoftmaxRegs = 152, kOtherRegs = 104;   // 128 * (2 * 152 + 2 * 104) = 512 * 128
 
 
 struct Params {
@@ -89,7 +91,6 @@ struct Params {
   int64_t cold_blocks;
   int32_t page, max_blocks;
   int32_t Hq, Hkv, G, tpt, layer;
-  bool out_wide;                  // rows of out are 32-byte aligned
   int32_t* err;
   float scale_log2;               // log2(e) / sqrt(d)
 };
@@ -125,7 +126,7 @@ struct Slot {
   PromptItemDev it;
   PromptReqDev rq;
 };
-constexpr uint32_t kCtlSlots = 288;
+constexpr uint32_t kCtlSlots = 304;
 constexpr uint32_t kCtlBytes = 512;
 static_assert(kCtlHidden + 4 <= kCtlSlots && kCtlSlots + 2 * sizeof(Slot) <= kCtlBytes, "prompt control block");
 constexpr int kSlotReaders = 10;          // MMA, relay and softmax warps
@@ -182,6 +183,11 @@ struct Ring {
       st = 0;
       ph ^= 1u;
     }
+  }
+  __device__ __forceinline__ void skip(int n) {
+    const int at = st + n, laps = at / NST;
+    st = at - laps * NST;
+    ph ^= (uint32_t)laps & 1u;
   }
 };
 
@@ -245,19 +251,6 @@ __device__ __forceinline__ bool elect_one() {
   return e != 0;
 }
 
-// 32 bytes of a row: one store where the address allows it (a whole sector: half stores of
-// every row doubled the epilogue's time)
-__device__ __forceinline__ void store32(void* dst, const uint32_t* w, bool wide) {
-  if (wide) {
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                 : "memory");
-  } else {
-    reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-  }
-}
-
 // keeps uses of the registers of a tcgen05.ld behind its wait
 __device__ __forceinline__ void tie32(float* v) {
 #pragma unroll
@@ -319,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     mbar_init(bar(B_QEMPTY), kSlotReaders);   // the last S is done and everyone has read the slot
     mbar_init(bar(B_FINAL), 1);
     for (int s = 0; s < NST; ++s) {
-      mbar_init(bar(B_REMPTY + s), 1);
+      mbar_init(bar(B_REMPTY + s), 8);  // one arrival of the MMAs' end and seven of the relay, or the softmax warps'
       mbar_init(bar(B_RFULL + s), 4);   // the TMA thread arrives four times, or each gather warp once
       mbar_init(bar(B_RSCAN + s), 1);
     }
@@ -362,6 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       Ring<NST> ring;                              // over the elements K0 V0 K1 V1 ...
       uint32_t scan_ph = 0;                        // bit s: parity of RSCAN[s]'s current phase
       uint32_t in_ring = 0, in_scan = 0, full_ph = 0;  // the last load of each stage, for the drain below
+      uint32_t staged = 0;                         // stages that an epilogue wrote to last
       uint32_t qn = 0;
       bool ok = true;
       Slot next = {};
@@ -377,18 +371,36 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           next.rq = p.reqs[next.it.req];
         }
         const int nctx = rq.nt_hot + rq.nt_cold;
-        for (int j = 0; j < 2 * it.ntile; ++j) {
+        for (int j = 0; j <= 2 * it.ntile; ++j) {
           const int t = it.tile0 + (j >> 1);
           const bool is_v = j & 1;
           const int st = ring.st;
           const uint32_t ph = ring.ph;
           ring.next();
-          // waited for whoever fills the stage: a parity wait may not fall a phase behind
+          // waited for whoever fills the stage: a parity wait may be neither a phase ahead nor one
+          // behind.  The gather warps, which would fall behind over tiles that are none of theirs,
+          // learn through B_RSCAN which stage is theirs.
           if (!wait_or_abort(bar(B_REMPTY + st), ph ^ 1u, p.err, abort_flag)) { ok = false; break; }
-          if (t < rq.nt_hot || t >= nctx) {        // COLD tiles: the gather warps
+          if (j == 2 * it.ntile) {                 // the staging element
+            in_ring &= ~(1u << st);
+            in_scan &= ~(1u << st);
+            staged |= 1u << st;
+            mbar_arrive_n(bar(B_RFULL + st), 4);
+          } else if (t >= rq.nt_hot && t < nctx) { // COLD: to the gather warps
+            in_ring &= ~(1u << st);
+            in_scan &= ~(1u << st);
+            scan_ph ^= 1u << st;
+            mbar_arrive(bar(B_RSCAN + st));
+          } else {
             const bool scan = is_v && scanned(it, rq, t);
             const uint32_t b = bar((scan ? B_RSCAN : B_RFULL) + st);
             const uint32_t tile = sR + (uint32_t)st * Lay::kTile;
+            if (staged >> st & 1u) {
+              // the epilogue's ordinary writes before TMA's (a fence by the warps that wrote, behind
+              // their stores to global memory, took them 1500 cycles)
+              fence_async_shared();
+              staged &= ~(1u << st);
+            }
             if (!scan) mbar_arrive_n(b, 3);
             mbar_arrive_expect_tx(b, Lay::kTile);
             if (t < rq.nt_hot) {
@@ -504,6 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         }
         __syncwarp();
       }
+      k.next();                    // the staging element
     }
     // arrives once every MMA issued above has finished, aborted or not
     if (elect_one()) tc_commit(bar(B_FINAL));
@@ -547,11 +560,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         const int t = it.tile0 + (j >> 1);
         const bool is_v = j & 1;
         const int st = ring.st;
-        const uint32_t ph = ring.ph;
         ring.next();
         const bool cold = t >= rq.nt_hot && t < nctx;
         if (!cold) flush();    // before anything that could wait for the copied tile to be used
-        if (!wait(B_REMPTY + st, ph ^ 1u)) { ok = false; break; }
+        if (!cold && !(is_v && scanned(it, rq, t))) continue;
+        // the stage is free (COLD), or TMA has filled it
+        if (!wait(B_RSCAN + st, scan_ph >> st & 1u)) { ok = false; break; }
+        scan_ph ^= 1u << st;
         const uint32_t tile = sR + (uint32_t)st * Lay::kTile;
         if (cold) {
           if (!is_v) {
@@ -576,9 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             announce(pending);
           }
           pending = st;
-        } else if (is_v && scanned(it, rq, t)) {
-          if (!wait(B_RSCAN + st, scan_ph >> st & 1u)) { ok = false; break; }
-          scan_ph ^= 1u << st;
+        } else {
           const bool hot = t < rq.nt_hot;
           const int key0 = (hot ? t : t - nctx) * BN;
           const int end = hot ? rq.lp : rq.n;
@@ -607,6 +620,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           announce(st);
         }
       }
+      if (!ok) break;
+      flush();
+      ring.next();                                 // the staging element
     }
     if (ok) flush();
     else cp_async_wait_all();
@@ -620,9 +636,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       uint32_t pn[2] = {0, 0};
       bool ok = true;
       auto full = [&]() {
-        const bool got = wait_or_abort(bar(B_RFULL + ring.st), ring.ph, p.err, abort_flag);
+        if (!wait_or_abort(bar(B_RFULL + ring.st), ring.ph, p.err, abort_flag)) return false;
+        mbar_arrive_n(bar(B_REMPTY + ring.st), 7);
         ring.next();
-        return got;
+        return true;
       };
       for (int ii = i0; ok && ii < i1; ++ii) {
         const uint32_t qn = (uint32_t)(ii - i0) & 1u;
@@ -631,7 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         const PromptReqDev rq = slots[qn].rq;
         mbar_arrive(bar(B_QEMPTY));
         const int cnt[2] = {tile_count(it, rq, p.tpt, 0), tile_count(it, rq, p.tpt, 1)};
-        ring.next();                   // K_0: the MMA warp waits for it
+        ok = full();                   // K_0: the MMA warp waits for it too
         for (int j = 0; ok && j < it.ntile; ++j) {
           ok = full() && (j + 1 == it.ntile || full());
 #pragma unroll
@@ -643,6 +660,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
               if (ok) mbar_arrive(bar(B_PFULL + i));
             }
         }
+        ring.next();                   // the staging element
       }
     }
   }
@@ -655,6 +673,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     const int tr = row / p.G, hr = row % p.G;     // token within the Q tile, query head within the group
     const uint32_t tSr = tS(qi) + lane_off, tOr = tO(qi) + lane_off;
     uint32_t sn = 0, on = 0;
+    Ring<NST> ring;                               // moved to each item's staging element
     bool ok = true;
     for (int ii = i0; ok && ii < i1; ++ii) {
       const uint32_t qn = (uint32_t)(ii - i0) & 1u;
@@ -663,10 +682,19 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       const PromptReqDev rq = slots[qn].rq;
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B_QEMPTY));
+      ring.skip(2 * it.ntile);
       const int nctx = rq.nt_hot + rq.nt_cold;
       const int cnt = tile_count(it, rq, p.tpt, qi);
-      const int tk = it.tok0 + qi * p.tpt + tr, qh = it.head * p.G + hr;
-      const bool valid = tr < p.tpt && tk < rq.n;
+      const int tk = it.tok0 + qi * p.tpt + tr;
+      // where the row's output goes (0: nowhere), found while the first scores are on their way
+      const bool part_row = it.entry >= 0;
+      uint64_t dst = 0, lse_dst = 0;
+      if (tr < p.tpt && tk < rq.n) {
+        const int qh = it.head * p.G + hr;
+        const int64_t prow = (int64_t)it.entry * 256 + qi * BM + row, orow = rq.t0 + tk;
+        dst = part_row ? (uint64_t)(p.part_o + prow * D) : (uint64_t)(p.out + orow * p.out_stride + qh * D);
+        lse_dst = part_row ? (uint64_t)(p.part_l + prow) : p.lse ? (uint64_t)(p.lse + orow * p.Hq + qh) : 0;
+      }
       // tiles with masked places, counted from the item's first: the last HOT and COLD ones and
       // those on the diagonal; how many of its keys the row sees there (rows of no token: as the last one)
       const int j_hot = rq.lp % BN ? rq.nt_hot - 1 - it.tile0 : -1;
@@ -789,49 +817,72 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         if (!__all_sync(0xffffffffu, wait_or_abort(bar(B_OFULL + qi), on & 1u, p.err, abort_flag))) { ok = false; break; }
         ++on;
         tc_fence_after();
-        if (__any_sync(0xffffffffu, *hidden_flag)) add_hidden_values<D>(p, it, rq, tk, qh, valid, m, tOr);
+        if (__any_sync(0xffffffffu, *hidden_flag))
+          add_hidden_values<D>(p, slots[qn].it, slots[qn].rq, tk, slots[qn].it.head * p.G + hr, dst != 0, m, tOr);
       }
-      const float inv = l > 0.f || l != l ? 1.f / l : 0.f;   // no key in this range: O = 0, LSE = -inf
+      const float inv = l > 0.f || l != l ? __fdividef(1.f, l) : 0.f;   // no key in this range: O = 0, LSE = -inf
       const float lse2 = m + __log2f(l);
-      const int64_t prow = (int64_t)it.entry * 256 + qi * BM + row;
-      const int64_t orow = (int64_t)(rq.t0 + tk);
-      if (valid) {
-        if (it.entry >= 0)
-          p.part_l[prow] = lse2;
-        else if (p.lse)
-          p.lse[orow * p.Hq + qh] = lse2 * kLn2;
-      }
+      if (lse_dst) *reinterpret_cast<float*>(lse_dst) = part_row ? lse2 : lse2 * kLn2;
       if (cnt > 0) {
-#pragma unroll 1
-        for (int c = 0; c < D; c += 64) {
-          float o[64];
-          tmem_ld32(tOr + c, o);
-          tmem_ld32(tOr + c + 32, o + 32);
-          tc_wait_ld();
-          tie32(o);
-          tie32(o + 32);
-          if (valid && it.entry >= 0) {
-            float* dst = p.part_o + prow * D + c;
+        // the staging element (its stage's earlier tiles were used by this Q tile, or by an earlier
+        // item: the wait cannot be a phase behind)
+        if (!wait(B_RFULL + ring.st, ring.ph)) { ok = false; break; }
+        // kRow bytes of each of the warp's 32 rows at a time, 16-byte chunks swizzled so that
+        // neither a thread's row nor a quarter warp's chunks meet in a bank
+        constexpr int kRow = D, kChunks = kRow / 16;
+        const uint32_t stage = sR + (uint32_t)ring.st * Lay::kTile + (uint32_t)(qi * 4 + (warp & 3)) * (32 * kRow);
+        auto chunk = [&](int r, int c) { return stage + r * kRow + ((c ^ (kChunks == 8 ? r & 7 : (r >> 1) & 3)) << 4); };
+        auto send = [&](int offset) {              // the staged bytes to their rows, at this byte of each
+          __syncwarp();
 #pragma unroll
-            for (int e = 0; e < 64; e += 8) {
-              uint32_t w[8];
-#pragma unroll
-              for (int k = 0; k < 8; ++k) w[k] = __float_as_uint(o[e + k] * inv);
-              store32(dst + e, w, true);
-            }
-          } else if (valid) {
-            uint16_t* dst = p.out + orow * p.out_stride + qh * D + c;
-#pragma unroll
-            for (int e = 0; e < 64; e += 16) {
-              uint32_t w[8];
-#pragma unroll
-              for (int k = 0; k < 8; ++k) w[k] = pack_bf16x2(o[e + 2 * k] * inv, o[e + 2 * k + 1] * inv);
-              store32(dst + e, w, p.out_wide);
-            }
+          for (int k = 0; k < kChunks; ++k) {
+            const int at = k * 32 + lane, r = at / kChunks, c = at % kChunks;
+            const uint64_t to = __shfl_sync(0xffffffffu, dst, r);
+            const uint4 v = lds128(chunk(r, c));
+            if (to) *reinterpret_cast<uint4*>(to + offset + c * 16) = v;
           }
           __syncwarp();
+        };
+        if (part_row) {
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            float o[32];
+            tmem_ld32(tOr + c, o);
+            tc_wait_ld();
+            tie32(o);
+#pragma unroll
+            for (int h = 0; h < 32; h += kRow / 4) {
+#pragma unroll
+              for (int e = 0; e < kRow / 4; e += 4)
+                sts128(chunk(lane, e / 4),
+                       make_uint4(__float_as_uint(o[h + e] * inv), __float_as_uint(o[h + e + 1] * inv),
+                                  __float_as_uint(o[h + e + 2] * inv), __float_as_uint(o[h + e + 3] * inv)));
+              send((c + h) * 4);
+            }
+          }
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < D; c += kRow / 2) {
+            float o[kRow / 2];
+#pragma unroll
+            for (int h = 0; h < kRow / 2; h += 32) tmem_ld32(tOr + c + h, o + h);
+            tc_wait_ld();
+#pragma unroll
+            for (int h = 0; h < kRow / 2; h += 32) tie32(o + h);
+#pragma unroll
+            for (int e = 0; e < kRow / 2; e += 8)
+              sts128(chunk(lane, e / 8),
+                     make_uint4(pack_bf16x2(o[e] * inv, o[e + 1] * inv), pack_bf16x2(o[e + 2] * inv, o[e + 3] * inv),
+                                pack_bf16x2(o[e + 4] * inv, o[e + 5] * inv),
+                                pack_bf16x2(o[e + 6] * inv, o[e + 7] * inv)));
+            send(c * 2);
+          }
         }
+        // eight arrivals give it back: a Q tile without tiles stays out of it altogether, as nothing
+        // would keep its warps from arriving for a stage that is still another element's
+        if (lane == 0) mbar_arrive_n(bar(B_REMPTY + ring.st), tile_count(it, rq, p.tpt, qi ^ 1) > 0 ? 1 : 2);
       }
+      ring.next();
     }
     tc_fence_before();
   }
@@ -1009,7 +1060,6 @@ int launch_prompt(const LaunchCommon& lc, void* stream, int32_t layer, const gk_
   pp.cold_blocks = c.cold_slots / c.cold_page_size;
   pp.page = c.cold_page_size;
   pp.max_blocks = b->max_blocks;
-  pp.out_wide = (uintptr_t)b->d_out % 32 == 0 && pp.out_stride % 16 == 0;
   pp.err = lc.d_error;
   pp.scale_log2 = kLog2e / sqrtf((float)D);
   if (D == 128) return prompt::launch_t<128>(pp, pl, base, (cudaStream_t)stream);
