@@ -251,6 +251,13 @@ __device__ __forceinline__ bool elect_one() {
   return e != 0;
 }
 
+__device__ __forceinline__ void stg128_if(bool doit, uint64_t addr, uint4 v) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %0, 0;\n\t@p st.global.v4.b32 [%1], {%2,%3,%4,%5};\n\t}" ::"r"(
+                   (int)doit),
+               "l"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+
 // keeps uses of the registers of a tcgen05.ld behind its wait
 __device__ __forceinline__ void tie32(float* v) {
 #pragma unroll
@@ -797,12 +804,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           f2unpack(fadd2(sum4[2], sum4[3]), s2, s3);
           part = (s0 + s1) + (s2 + s3);
         };
-        if (masked) exponentials(std::true_type());
-        else exponentials(std::false_type());
-        if (__any_sync(0xffffffffu, part > 0x1p64f)) {
+        for (bool again = false;; again = true) {
+          if (masked || again) exponentials(std::true_type());
+          else exponentials(std::false_type());
+          if (again || !__any_sync(0xffffffffu, part > 0x1p64f)) break;
           // far above the reference: raise it and take the tile again (its S is still there)
           raise(fmaxf(m, maximum(BN)), j > 0);
-          exponentials(std::true_type());
         }
         l += part;
 #pragma unroll
@@ -834,13 +841,16 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         auto chunk = [&](int r, int c) { return stage + r * kRow + ((c ^ (kChunks == 8 ? r & 7 : (r >> 1) & 3)) << 4); };
         auto send = [&](int offset) {              // the staged bytes to their rows, at this byte of each
           __syncwarp();
+          uint4 v[kChunks];
+          uint64_t to[kChunks];
 #pragma unroll
-          for (int k = 0; k < kChunks; ++k) {
-            const int at = k * 32 + lane, r = at / kChunks, c = at % kChunks;
-            const uint64_t to = __shfl_sync(0xffffffffu, dst, r);
-            const uint4 v = lds128(chunk(r, c));
-            if (to) *reinterpret_cast<uint4*>(to + offset + c * 16) = v;
+          for (int k = 0; k < kChunks; ++k) {      // all on their way before the first is used
+            const int r = (k * 32 + lane) / kChunks;
+            v[k] = lds128(chunk(r, lane % kChunks));
+            to[k] = __shfl_sync(0xffffffffu, dst, r);
           }
+#pragma unroll
+          for (int k = 0; k < kChunks; ++k) stg128_if(to[k] != 0, to[k] + offset + (lane % kChunks) * 16, v[k]);
           __syncwarp();
         };
         if (part_row) {
