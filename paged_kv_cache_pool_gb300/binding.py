@@ -367,11 +367,12 @@ class Tables:
         self.work = table.new_empty((rows + 1) * (GK_TABLES_WORK_PER_ROW // 4))
         self.c = gk_tables(rows, width, free.numel(), 0, _ptr(table), _ptr(free), _ptr(length), _ptr(self.length_out),
                            _ptr(num_free), _ptr(self.num_free_out), _ptr(self.work))
+        self.ref = ctypes.byref(self.c)
 
 
 def gk_tables_step(pool, stream, tables, d_add, d_slot_mapping, d_done, d_release=None, n_slots=None):
     n_slots = d_slot_mapping.numel() if n_slots is None else n_slots
-    _check(lib().gk_tables_step(pool, _stream(stream), ctypes.byref(tables.c), _ptr(d_release), _ptr(d_add), n_slots,
+    _check(lib().gk_tables_step(pool, _stream(stream), tables.ref, _ptr(d_release), _ptr(d_add), n_slots,
                                 _ptr(d_slot_mapping), _ptr(d_done)), pool)
 
 
@@ -483,9 +484,10 @@ def _token_stride(x, tokens, what):
     if x is None or isinstance(x, int):
         return 0
     n, heads, d = x.shape
-    if n != tokens or x.element_size() != 2 or (n and (x.stride(2) != 1 or (heads > 1 and x.stride(1) != d))):
+    row, head, channel = x.stride()
+    if n != tokens or x.element_size() != 2 or (n and (channel != 1 or (heads > 1 and head != d))):
         raise ValueError(f"{what} must be bf16 [{tokens}, heads, d] with a token's heads and channels contiguous")
-    return x.stride(0) if n > 1 else 0
+    return row if n > 1 else 0
 
 
 class PromptBatch:
@@ -512,6 +514,7 @@ class PromptBatch:
                                  None if self.context_len is None else _i32p(self.context_len))
         self._table = d_block_table
         self.c.d_block_table = _ptr(d_block_table)
+        self.ref = ctypes.byref(self.c)
 
     def set_device(self, d_q, d_k, d_v, d_out, d_lse=None, d_block_table=None, max_blocks=None):
         """bf16 [T, Hq, d] q and out, [T, Hkv, d] k and v, fp32 [T, Hq] lse: torch tensors
@@ -560,7 +563,7 @@ def gk_prompt_plan_items(plan):
 
 
 def gk_prompt_attn(pool, stream, layer, batch, plan):
-    _check(lib().gk_prompt_attn(pool, _stream(stream), layer, ctypes.byref(batch.c), plan), pool)
+    _check(lib().gk_prompt_attn(pool, _stream(stream), layer, batch.ref, plan), pool)
 
 
 def gk_dispatch(pool, plan):

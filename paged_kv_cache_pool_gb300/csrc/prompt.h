@@ -49,6 +49,7 @@ struct PromptPlan {
   std::vector<int32_t> cta_begin;        // [CTAs + 1]
   std::vector<PromptJoinDev> joins;
   int32_t n_entries = 0;
+  uint8_t hot_maps[256] = {};            // tensor maps of the HOT pool's K and V (any_hot)
   void* d_buf = nullptr;
   void* h_stage = nullptr;
   cudaEvent_t upload_done = nullptr;
@@ -61,6 +62,8 @@ struct PromptPlan {
   bool uploaded = false;
 };
 
+// the tensor maps of a pool's HOT K and V, 128 bytes each
+int encode_hot_maps(const gk_pool_config* cfg, uint8_t* out);
 int launch_prompt(const LaunchCommon& lc, void* stream, int32_t layer, const gk_prompt_batch* b, const PromptPlan* pl);
 
 }  // namespace gk

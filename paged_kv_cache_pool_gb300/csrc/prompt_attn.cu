@@ -52,6 +52,7 @@
 #include <cuda.h>
 
 #include <cmath>
+#include <cstring>
 #include <type_traits>
 
 #include "prefix_body.cuh"
@@ -1030,6 +1031,17 @@ static int encode_hot(CUtensorMap* tm, const void* ptr, int d, int64_t rows) {
              : 2;
 }
 
+int encode_hot_maps(const gk_pool_config* cfg, uint8_t* out) {
+  const int64_t rows = cfg->hot_tokens * cfg->num_layers * cfg->num_kv_heads;
+  const void* pools[2] = {cfg->hot_k, cfg->hot_v};
+  for (int i = 0; i < 2; ++i) {
+    CUtensorMap tm;
+    if (encode_hot(&tm, pools[i], cfg->head_dim, rows)) return 1;
+    std::memcpy(out + i * sizeof(CUtensorMap), &tm, sizeof(CUtensorMap));
+  }
+  return 0;
+}
+
 int launch_prompt(const LaunchCommon& lc, void* stream, int32_t layer, const gk_prompt_batch* b, const PromptPlan* pl) {
   const gk_pool_config& c = *lc.cfg;
   const uint8_t* base = (const uint8_t*)pl->d_buf;
@@ -1047,12 +1059,9 @@ int launch_prompt(const LaunchCommon& lc, void* stream, int32_t layer, const gk_
   int e = encode_packed(&pp.tq, b->d_q, D, pp.Hq, pl->tokens, pp.q_stride, G, pp.tpt);
   if (!e) e = encode_packed(&pp.tk, b->d_k, D, pp.Hkv, pl->tokens, pp.k_stride, 1, kPrefixTileN);
   if (!e) e = encode_packed(&pp.tv, b->d_v, D, pp.Hkv, pl->tokens, pp.v_stride, 1, kPrefixTileN);
-  if (!e && pl->any_hot) {
-    const int64_t rows = c.hot_tokens * c.num_layers * c.num_kv_heads;
-    e = encode_hot(&pp.thk, c.hot_k, D, rows);
-    if (!e) e = encode_hot(&pp.thv, c.hot_v, D, rows);
-  }
   if (e) return (int)cudaErrorInvalidValue;
+  std::memcpy(&pp.thk, pl->hot_maps, sizeof(CUtensorMap));
+  std::memcpy(&pp.thv, pl->hot_maps + sizeof(CUtensorMap), sizeof(CUtensorMap));
   pp.reqs = (const PromptReqDev*)(base + pl->off_reqs);
   pp.items = (const PromptItemDev*)(base + pl->off_items);
   pp.cta_begin = (const int32_t*)(base + pl->off_begin);

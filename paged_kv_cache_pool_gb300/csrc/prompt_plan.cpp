@@ -317,6 +317,8 @@ size_t region(size_t* off, size_t bytes) {
 
 gk_status upload(Pool* p, PromptPlan* pl, void* stream) {
   cudaStream_t st = (cudaStream_t)stream;
+  if (pl->any_hot && encode_hot_maps(&p->cfg, pl->hot_maps))
+    return fail(p, GK_ERR_CUDA, "encoding the HOT pool's tensor maps failed");
   size_t off = 0;
   pl->off_reqs = region(&off, pl->reqs.size() * sizeof(PromptReqDev));
   pl->off_items = region(&off, pl->items.size() * sizeof(PromptItemDev));

@@ -11,13 +11,15 @@
 // asks for the next block and every later one get nothing, as there:
 //   done_r = min(add_r, (have_r + n - B_r) P - len_r) where B_r <= n, else 0.
 //
-// tables_scan_kernel (one CTA) does the three exclusive sums over the rows
-// (tokens, new blocks, released blocks), writes lengths, counts and, per row, what
-// the wide kernels need; tables_push_kernel copies released blocks to the stack;
-// tables_fill_kernel writes one slot and at most one table entry per token.
-// Nothing is computed twice and no order depends on scheduling.  A step moves at
-// most 8 bytes per token and 8 per block: it is bound by launches and by the scan's
-// round trips.
+// One launch of one thread-block cluster.  Up to 1024 rows, every CTA scans all of
+// them (one row a thread) and keeps their records in shared memory; with more, each
+// CTA sums its share, the CTAs exchange their totals through distributed shared
+// memory, and the records go through the workspace.  Released blocks are copied to
+// the stack by all threads of the cluster; behind a cluster barrier every thread
+// writes up to four consecutive slots and at most a table entry for each.  No order depends
+// on scheduling.  A step moves 8 bytes per token and 8 per block: it is bound by round
+// trips to L2 and by its launch, which is why it is one launch (three of them, a scan,
+// a push and a fill kernel, took 9-13 us on the GPU and 13 us of the host's time).
 #include <algorithm>
 
 #include "device_common.cuh"
@@ -26,22 +28,24 @@
 namespace gk {
 namespace {
 
-constexpr int kScanThreads = 1024;
+constexpr int kThreads = 1024;
+constexpr int kMaxCtas = 16;
+constexpr int kUnroll = 4;         // independent loads in flight per thread
 
-// per row, written by the scan for the kernels after it
+// per row, for the kernel's later phases
 struct TableRowDev {
   int64_t tok0;      // its first token's place in the slot map
   int32_t len;       // tokens before the append (0 for a released row)
   int32_t done;      // tokens appended
   int32_t pop0;      // blocks the rows before it took
-  int32_t push0;     // released blocks of the rows before it
-  int32_t pushed;    // released blocks of this row
-  int32_t pad0;
+  int32_t have;      // blocks before the append
+  int32_t pad[2];
 };
 static_assert(sizeof(TableRowDev) == GK_TABLES_WORK_PER_ROW, "workspace size in gk.h");
 
 struct StepParams {
   int32_t rows, max_blocks, capacity, page;
+  int32_t page_shift;               // log2(page), -1 where it is no power of two
   int64_t n_blocks;                 // COLD blocks of the pool
   int64_t n_slots;
   int32_t* table;
@@ -55,33 +59,42 @@ struct StepParams {
   int64_t* slots;
   int32_t* done;
   TableRowDev* work;
-  int32_t* top;                     // blocks on the stack after the releases
   int32_t* err;
 };
 
-__device__ __forceinline__ int32_t blocks_of(int64_t tokens, int32_t page) { return (int32_t)((tokens + page - 1) / page); }
-
-// one token of row r, k-th of its new ones, at place t of the slot map
-__device__ __forceinline__ void place(const StepParams& p, const TableRowDev& w, int r, int32_t k, int64_t t, int32_t top) {
-  int64_t slot = -1;
-  if (k < w.done) {
-    const int32_t pos = w.len + k, b = pos / p.page, have = blocks_of(w.len, p.page);
-    int32_t* cell = p.table + (int64_t)r * p.max_blocks + b;
-    int32_t id;
-    if (b >= have) {
-      const int32_t from = top - 1 - (w.pop0 + (b - have));
-      id = from >= 0 && from < p.capacity ? p.free[from] : -1;
-      if (pos % p.page == 0) *cell = id;       // a new block's first token writes its table entry
-    } else {
-      id = *cell;
-    }
-    if (id >= 0 && id < p.n_blocks) slot = (int64_t)id * p.page + pos % p.page;
-    else report_error(p.err, kErrBounds);
-  }
-  p.slots[t] = slot;
+// 32-bit quotients, by shifts for the usual pages: 64-bit division held the fill to 9 us
+// for 119 thousand tokens
+__device__ __forceinline__ int32_t page_of(const StepParams& p, int32_t pos) {
+  return p.page_shift >= 0 ? pos >> p.page_shift : (int32_t)((uint32_t)pos / (uint32_t)p.page);
+}
+// blocks of tokens in [0, 2^31)
+__device__ __forceinline__ int32_t blocks_of(const StepParams& p, int32_t tokens) {
+  return tokens > 0 ? page_of(p, tokens - 1) + 1 : 0;
 }
 
-// exclusive sums over the CTA of three values per thread; total in sum[]
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_ctas() {
+  uint32_t n;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
+  return n;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// 64-bit value at shared address `addr` of CTA `rank` of the cluster
+__device__ __forceinline__ int64_t ld_cluster(uint32_t addr, uint32_t rank) {
+  uint32_t a;
+  int64_t v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.s64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
+  return v;
+}
+
+// exclusive sums over the CTA of three values per thread; the totals in sum[]
 __device__ __forceinline__ void scan3(int64_t v[3], int64_t sum[3], int64_t (*warp_sum)[3]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t inc[3];
@@ -97,17 +110,14 @@ __device__ __forceinline__ void scan3(int64_t v[3], int64_t sum[3], int64_t (*wa
     if (lane == 31) warp_sum[warp][i] = x;
   }
   __syncthreads();
-  if (warp == 0) {
+  if (warp < 3) {
+    int64_t x = warp_sum[lane][warp];
 #pragma unroll
-    for (int i = 0; i < 3; ++i) {
-      int64_t x = warp_sum[lane][i];
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, x, off);
-        if (lane >= off) x += y;
-      }
-      warp_sum[lane][i] = x;
+    for (int off = 1; off < 32; off <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, off);
+      if (lane >= off) x += y;
     }
+    warp_sum[lane][warp] = x;
   }
   __syncthreads();
 #pragma unroll
@@ -119,104 +129,235 @@ __device__ __forceinline__ void scan3(int64_t v[3], int64_t sum[3], int64_t (*wa
   __syncthreads();
 }
 
-__global__ void __launch_bounds__(kScanThreads) tables_scan_kernel(const StepParams p) {
+// last i of [0, n) with key(i) <= x (key ascending, key(0) <= x)
+template <typename Key>
+__device__ __forceinline__ int last_at_most(int n, int64_t x, Key key) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (key(mid) <= x) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// what a row asks for
+struct RowAsk {
+  int64_t asked;     // its places in the slot map
+  int32_t need;      // new blocks
+  int32_t pushed;    // released blocks
+  int32_t len;       // tokens it starts the append with
+  int32_t have;      // their blocks
+  bool bad;          // its length or table cannot be: it keeps both
+  bool skip;         // it appends nothing
+  bool wrong;        // ... and asked for something
+};
+__device__ __forceinline__ RowAsk row_ask(const StepParams& p, int r, bool releases) {
+  RowAsk a{0, 0, 0, 0, 0, false, true, false};
+  if (r >= p.rows) return a;
+  const int32_t len = p.len[r], add = p.add[r], rel = releases ? p.release[r] : 0;
+  a.asked = add > 0 ? add : 0;
+  a.len = len;
+  a.bad = len < 0 || blocks_of(p, len) > p.max_blocks;
+  if (!a.bad && rel != 0) {
+    a.pushed = blocks_of(p, len);
+    a.len = 0;
+  }
+  a.skip = a.bad || add < 0 || a.len + a.asked > INT32_MAX || blocks_of(p, a.len + (int32_t)a.asked) > p.max_blocks;
+  a.wrong = a.skip && add != 0;
+  if (!a.bad) a.have = blocks_of(p, a.len);
+  if (!a.skip) a.need = blocks_of(p, a.len + (int32_t)a.asked) - a.have;
+  return a;
+}
+
+// kFit: the rows are at most kThreads
+template <bool kFit>
+__global__ void __launch_bounds__(kThreads) tables_step_kernel(const StepParams p) {
   __shared__ int64_t warp_sum[32][3];
+  __shared__ int64_t total[2][3];           // this CTA's rows: tokens, new blocks, released blocks
+  __shared__ int64_t totals[kMaxCtas][3];
+  __shared__ int32_t push_at[kThreads];     // released blocks of the chunk's rows before each
+  __shared__ TableRowDev rows_s[kFit ? kThreads : 1];  // every row's record
+  const int tid = (int)threadIdx.x;
+  const int rank = (int)cluster_rank(), ctas = (int)cluster_ctas();
   griddep_launch_dependents();
   griddep_wait();
-  int64_t base[3] = {0, 0, 0};      // tokens, new blocks, released blocks of the rows before this chunk
+  const int span = kFit ? p.rows : (p.rows + ctas - 1) / ctas;   // rows that this CTA scans
+  const int r_begin = kFit ? 0 : min(p.rows, rank * span), r_end = min(p.rows, r_begin + span);
   const int32_t n_in = *p.n_free;
   const bool stack_ok = n_in >= 0 && n_in <= p.capacity;
   const int32_t n0 = stack_ok ? n_in : 0;
-  // the released blocks first: how high the stack is before any append
-  int64_t released = 0;
-  if (p.release) {
-    for (int r0 = 0; r0 < p.rows; r0 += kScanThreads) {
-      const int r = r0 + (int)threadIdx.x;
-      int64_t v[3] = {0, 0, 0}, sum[3];
-      if (r < p.rows && p.release[r] != 0) {
-        const int32_t len = p.len[r];
-        if (len >= 0 && blocks_of(len, p.page) <= p.max_blocks) v[2] = blocks_of(len, p.page);
-      }
+
+  // ---- totals: this CTA's, then everyone's -------------------------------------------
+  bool releases = p.release != nullptr;
+  int64_t base[3], all[3];
+  RowAsk a;                                 // the last chunk's row, and its place in the chunk
+  int64_t v[3], sum[3];
+  for (int pass = 0;; ++pass) {
+    int64_t mine[3] = {0, 0, 0};
+    for (int r0 = r_begin; r0 < r_end || r0 == r_begin; r0 += kThreads) {
+      a = row_ask(p, r0 + tid < r_end ? r0 + tid : p.rows, releases);
+      v[0] = a.asked;
+      v[1] = a.need;
+      v[2] = a.pushed;
       scan3(v, sum, warp_sum);
-      released += sum[2];
+#pragma unroll
+      for (int i = 0; i < 3; ++i) mine[i] += sum[i];
     }
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      base[i] = 0;
+      all[i] = mine[i];
+    }
+    if (!kFit && ctas > 1) {
+      // the totals stay until the cluster barrier behind the rows' results, so no CTA changes or
+      // leaves them while another reads
+      if (tid < 3) total[pass][tid] = tid == 0 ? mine[0] : tid == 1 ? mine[1] : mine[2];
+      cluster_sync();
+      if (tid < 3 * ctas) totals[tid / 3][tid % 3] = ld_cluster(smem_u32(&total[pass][tid % 3]), (uint32_t)(tid / 3));
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        all[i] = 0;
+        for (int c = 0; c < ctas; ++c) {
+          if (c < rank) base[i] += totals[c][i];
+          all[i] += totals[c][i];
+        }
+      }
+      __syncthreads();
+    }
+    if (stack_ok && n0 + all[2] <= p.capacity) break;
+    if (pass == 0 && rank == 0 && tid == 0) report_error(p.err, kErrBounds);
+    if (!releases || pass == 1) break;
+    releases = false;                       // the stack cannot take them: nothing is released
   }
-  const bool push_ok = stack_ok && n0 + released <= p.capacity;
-  const int64_t top = push_ok ? n0 + released : n0;
-  if (!push_ok && threadIdx.x == 0) report_error(p.err, kErrBounds);
-  int64_t taken_all = 0;
-  for (int r0 = 0; r0 < p.rows; r0 += kScanThreads) {
-    const int r = r0 + (int)threadIdx.x;
-    int32_t len = 0, add = 0, pushed = 0;
-    bool bad = false;
-    if (r < p.rows) {
-      len = p.len[r];
-      add = p.add[r];
-      bad = len < 0 || blocks_of(len, p.page) > p.max_blocks;
-      if (!bad && p.release && p.release[r] != 0 && push_ok) {
-        pushed = blocks_of(len, p.page);
-        len = 0;
+  const int64_t top = n0 + all[2];          // blocks on the stack after the releases
+
+  // ---- per-row results, and released blocks to the stack -------------------------------
+  const bool once = kFit || r_end - r_begin <= kThreads;   // a, v and sum are still those of the only chunk
+  int32_t done = 0;
+  int64_t taken = 0;
+  bool overflow = false;
+  auto write_row = [&](int r) {
+    p.done[r] = done;
+    p.len_out[r] = a.bad ? a.len : a.len + done;
+    if (overflow && stack_ok) *p.n_free_out = (int32_t)(top - taken);
+  };
+  for (int r0 = r_begin; r0 < r_end; r0 += kThreads) {
+    const int r = r0 + tid, n_here = min(kThreads, r_end - r0);
+    if (!once) {
+      a = row_ask(p, r < r_end ? r : p.rows, releases);
+      v[0] = a.asked;
+      v[1] = a.need;
+      v[2] = a.pushed;
+      scan3(v, sum, warp_sum);
+    }
+    const int64_t tok0 = base[0] + v[0], pop0 = base[1] + v[1];
+    if (r < r_end) {
+      const int64_t end = tok0 + a.asked;
+      done = 0;
+      if (!a.skip && end <= p.n_slots && pop0 <= top)
+        done = (int32_t)min(a.asked, (a.have + top - pop0) * p.page - a.len);
+      if ((!kFit || rank == 0) && (a.bad || a.wrong || end > p.n_slots)) report_error(p.err, kErrBounds);
+      // the first row without room in the slot map: no row from there on takes a block
+      overflow = end > p.n_slots && tok0 <= p.n_slots;
+      taken = min(pop0, top);
+      const TableRowDev w{tok0, a.len, done, (int32_t)min(pop0, (int64_t)INT32_MAX), a.have, {0, 0}};
+      if (kFit) {
+        rows_s[r] = w;
+      } else {
+        p.work[r] = w;
+        write_row(r);
       }
     }
-    const int64_t asked = add > 0 ? add : 0;
-    // a row whose length or table cannot hold the append takes no part in it
-    bool skip = bad || add < 0 || (int64_t)len + asked > INT32_MAX || blocks_of((int64_t)len + asked, p.page) > p.max_blocks;
-    int64_t v[3] = {asked, skip ? 0 : blocks_of((int64_t)len + asked, p.page) - blocks_of(len, p.page), pushed}, sum[3];
-    const int64_t need = v[1];
-    scan3(v, sum, warp_sum);
-    const int64_t tok0 = base[0] + v[0], pop0 = base[1] + v[1], push0 = base[2] + v[2];
-    int64_t taken = 0;
-    if (r < p.rows) {
-      if (tok0 + asked > p.n_slots) skip = true;      // no room in the slot map
-      int32_t done = 0;
-      if (!skip && pop0 <= top) {
-        const int64_t fits = ((int64_t)blocks_of(len, p.page) + top - pop0) * p.page - len;
-        done = (int32_t)min(asked, fits);
-        taken = min(need, top - pop0);
+    if (releases) {
+      push_at[tid] = (int32_t)v[2];
+      __syncthreads();
+      int32_t* dst = p.free + n0 + base[2];
+      const int32_t stride = kFit ? ctas * kThreads : kThreads;
+      for (int32_t i0 = (kFit ? rank * kThreads : 0) + tid; i0 < sum[2]; i0 += kUnroll * stride) {
+        int32_t id[kUnroll];
+#pragma unroll
+        for (int k = 0; k < kUnroll; ++k) {
+          const int32_t i = i0 + k * stride;
+          if (i < sum[2]) {
+            const int q = last_at_most(n_here, i, [&](int x) { return (int64_t)push_at[x]; });
+            id[k] = p.table[(int64_t)(r0 + q) * p.max_blocks + (i - push_at[q])];
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < kUnroll; ++k)
+          if (i0 + k * stride < sum[2]) dst[i0 + k * stride] = id[k];
       }
-      if (bad || (skip && (add != 0))) report_error(p.err, kErrBounds);
-      p.work[r] = {tok0, len, done, (int32_t)min(pop0, (int64_t)INT32_MAX), (int32_t)push0, pushed, 0};
-      p.done[r] = done;
-      p.len_out[r] = bad ? p.len[r] : len + done;
+      __syncthreads();
     }
-    int64_t t3[3] = {taken, 0, 0}, tsum[3];
-    scan3(t3, tsum, warp_sum);
-    taken_all += tsum[0];
 #pragma unroll
     for (int i = 0; i < 3; ++i) base[i] += sum[i];
   }
-  if (threadIdx.x == 0) {
-    *p.n_free_out = stack_ok ? (int32_t)(top - taken_all) : n_in;
-    *p.top = (int32_t)top;
-    p.top[1] = n0;
-  }
-}
+  if (ctas > 1) cluster_sync();
+  else __syncthreads();
+  // outputs that may be the inputs' own arrays: behind everyone's reads
+  if (kFit && rank == 0 && tid < p.rows) write_row(tid);
+  if (rank == 0 && tid == 0 && (!stack_ok || all[0] <= p.n_slots))
+    *p.n_free_out = stack_ok ? (int32_t)(top - min(all[1], top)) : n_in;
 
-// one CTA per released row: its blocks onto the stack
-__global__ void tables_push_kernel(const StepParams p) {
-  griddep_launch_dependents();
-  griddep_wait();
-  const TableRowDev w = p.work[blockIdx.x];
-  const int32_t* row = p.table + (int64_t)blockIdx.x * p.max_blocks;
-  int32_t* dst = p.free + p.top[1] + w.push0;
-  for (int i = threadIdx.x; i < w.pushed; i += blockDim.x) dst[i] = row[i];
-}
-
-__global__ void tables_fill_kernel(const StepParams p) {
-  griddep_launch_dependents();
-  griddep_wait();
-  const int32_t top = *p.top;
-  for (int64_t t = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; t < p.n_slots; t += (int64_t)gridDim.x * blockDim.x) {
-    // the last row that starts at or before t holds it, or t is past them all
-    int lo = 0, hi = p.rows - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (p.work[mid].tok0 <= t) lo = mid;
-      else hi = mid - 1;
+  // ---- a slot and at most a table entry per token ----------------------------------------
+  const TableRowDev* rows = kFit ? rows_s : p.work;
+  auto row_of = [&](int64_t t) { return last_at_most(p.rows, t, [&](int x) { return rows[x].tok0; }); };
+  const bool wide = (uintptr_t)p.slots % 16 == 0;
+  // consecutive tokens a thread takes at a time: few where the threads outnumber the tokens, as
+  // each may need a search of its own (a decode step's tokens are all of different rows)
+  const int64_t threads = (int64_t)ctas * kThreads;
+  const int per = (int)min((int64_t)kUnroll, (p.n_slots + threads - 1) / threads);
+  for (int64_t t0 = ((int64_t)rank * kThreads + tid) * per; t0 < p.n_slots; t0 += threads * per) {
+    int32_t id[kUnroll], pos[kUnroll];
+    int64_t cell[kUnroll];                  // -1: nothing to place, -2: nothing to write
+    int64_t slot[kUnroll];
+    int r = 0;
+    int64_t next = t0;                      // first token of the row after r
+    TableRowDev w;
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) {
+      const int64_t t = t0 + k;
+      cell[k] = -1;
+      id[k] = -1;
+      pos[k] = 0;
+      if (k >= per || t >= p.n_slots || t >= all[0]) continue;
+      if (t >= next) {
+        r = row_of(t);
+        w = rows[r];
+        next = r + 1 < p.rows ? rows[r + 1].tok0 : all[0];
+      }
+      const int64_t j = t - w.tok0;
+      if (j >= w.done) continue;
+      pos[k] = w.len + (int32_t)j;
+      const int32_t b = page_of(p, pos[k]);
+      pos[k] -= b * p.page;                 // within the block
+      cell[k] = (int64_t)r * p.max_blocks + b;
+      const int64_t from = top - 1 - ((int64_t)w.pop0 + b - w.have);
+      if (b < w.have) id[k] = p.table[cell[k]];
+      else if (from >= 0 && from < p.capacity) id[k] = p.free[from];
+      // a new block's first token writes its table entry
+      if (b < w.have || pos[k] != 0) cell[k] = -2;
     }
-    const TableRowDev w = p.work[lo];
-    const int64_t k = t - w.tok0;
-    place(p, w, lo, (int32_t)min(k, (int64_t)INT32_MAX), t, top);
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) {
+      if (cell[k] >= 0) p.table[cell[k]] = id[k];
+      slot[k] = -1;
+      if (cell[k] != -1) {
+        if (id[k] >= 0 && id[k] < p.n_blocks) slot[k] = (int64_t)id[k] * p.page + pos[k];
+        else report_error(p.err, kErrBounds);
+      }
+    }
+    if (wide && per == kUnroll && t0 + kUnroll <= p.n_slots) {
+#pragma unroll
+      for (int k = 0; k < kUnroll; k += 2)
+        *reinterpret_cast<longlong2*>(p.slots + t0 + k) = make_longlong2(slot[k], slot[k + 1]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k)
+        if (k < per && t0 + k < p.n_slots) p.slots[t0 + k] = slot[k];
+    }
   }
 }
 
@@ -230,6 +371,9 @@ int launch_tables_step(const LaunchCommon& lc, void* stream, const gk_tables* t,
   p.max_blocks = t->max_blocks;
   p.capacity = t->capacity;
   p.page = c.cold_page_size;
+  p.page_shift = -1;
+  for (int s = 0; s < 31; ++s)
+    if (c.cold_page_size == 1 << s) p.page_shift = s;
   p.n_blocks = c.cold_slots / c.cold_page_size;
   p.n_slots = n_slots;
   p.table = t->d_table;
@@ -242,17 +386,30 @@ int launch_tables_step(const LaunchCommon& lc, void* stream, const gk_tables* t,
   p.add = d_add;
   p.slots = d_slots;
   p.done = d_done;
-  p.top = (int32_t*)t->d_work;
-  p.work = (TableRowDev*)((uint8_t*)t->d_work + GK_TABLES_WORK_PER_ROW);
+  p.work = (TableRowDev*)t->d_work;
   p.err = lc.d_error;
-  cudaStream_t st = (cudaStream_t)stream;
-  cudaError_t e = launch_pdl(tables_scan_kernel, dim3(1), dim3(kScanThreads), 0, st, p);
-  if (e == cudaSuccess && d_release) e = launch_pdl(tables_push_kernel, dim3((unsigned)p.rows), dim3(256), 0, st, p);
-  if (e == cudaSuccess && n_slots > 0) {
-    const int64_t blocks = std::min<int64_t>((n_slots + 255) / 256, (int64_t)lc.num_sms * 8);
-    e = launch_pdl(tables_fill_kernel, dim3((unsigned)blocks), dim3(256), 0, st, p);
+  // The CTAs of the cluster: one where its threads have a round of four tokens each at most
+  // and nothing is released, else eight; sixteen (the most a cluster has) for longer maps.
+  const bool fit = p.rows <= kThreads;
+  const int ctas = n_slots > 8 * kUnroll * kThreads ? 16 : d_release || n_slots > kUnroll * kThreads || !fit ? 8 : 1;
+  auto kern = fit ? tables_step_kernel<true> : tables_step_kernel<false>;
+  if (ctas > 8) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return (int)e;
   }
-  return (int)e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = (cudaStream_t)stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ctas;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return (int)cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 }  // namespace gk
