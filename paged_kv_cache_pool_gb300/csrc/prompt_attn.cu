@@ -345,7 +345,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(ctl_ptr + kCtlTmemSlot);
-  griddep_wait();
+  // The plan's tables are written before the kernel ahead of this one starts and by no kernel,
+  // so they are read while it still runs; what reads or writes a call's data waits for it
+  // (griddep_wait in the roles below).
   const int i0 = p.cta_begin[blockIdx.x], i1 = p.cta_begin[blockIdx.x + 1];
   auto tS = [&](int i) { return tmem + (uint32_t)(i * 128); };
   auto tO = [&](int i) { return tmem + 256u + (uint32_t)(i * 128); };
@@ -371,6 +373,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         next.it = p.items[i0];
         next.rq = p.reqs[next.it.req];
       }
+      for (const CUtensorMap* tm : {&p.tq, &p.tk, &p.tv})
+        asm volatile("prefetch.tensormap [%0];" ::"l"(tm) : "memory");
+      griddep_wait();
       for (int ii = i0; ok && ii < i1; ++ii) {
         const PromptItemDev it = next.it;
         const PromptReqDev rq = next.rq;
@@ -535,6 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     constexpr int kRowsPerCopy = 32 / kChunks;   // rows per warp instruction
     const int row0 = (warp < 4 ? warp - 2 : warp - 11) * 32;   // this warp's rows of a tile
     const int ch = lane % kChunks, sub = lane / kChunks;
+    griddep_wait();
     Ring<NST> ring;
     uint32_t scan_ph = 0;
     int pending = -1;                            // stage this warp copied to but has not announced
@@ -680,6 +686,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const int tr = row / p.G, hr = row % p.G;     // token within the Q tile, query head within the group
     const uint32_t tSr = tS(qi) + lane_off, tOr = tO(qi) + lane_off;
+    griddep_wait();
     uint32_t sn = 0, on = 0;
     Ring<NST> ring;                               // moved to each item's staging element
     bool ok = true;

@@ -15,9 +15,9 @@ namespace {
 // What the planner weighs, in us on one SM of a GB300 (the measurements are in
 // prompt_attn.cu): a 128-key tile of an item with two Q tiles and of one with
 // one, an item's fixed cost, and 32 joined rows.
-constexpr double kTile2Us = 1.25;
-constexpr double kTile1Us = 0.85;
-constexpr double kItemUs = 2.5;
+constexpr double kTile2Us = 1.55;
+constexpr double kTile1Us = 1.45;
+constexpr double kItemUs = 4.5;
 constexpr double kJoinLaunchUs = 4.0;
 constexpr double kJoinUs = 1.0;
 constexpr int32_t kMaxPieces = 16;      // items over one block's own keys, and over its stacked prefix
