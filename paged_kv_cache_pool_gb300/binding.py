@@ -169,19 +169,21 @@ def lib():
 
 def _ptr(x):
     """Device address of a torch tensor, an int, or None."""
-    if x is None:
-        return None
-    if isinstance(x, int):
-        return x
-    return x.data_ptr()
+    try:
+        return x.data_ptr()
+    except AttributeError:
+        if x is None or isinstance(x, int):
+            return x
+        raise
 
 
 def _stream(s):
-    if s is None:
-        return None
-    if isinstance(s, int):
-        return s
-    return s.cuda_stream
+    try:
+        return s.cuda_stream
+    except AttributeError:
+        if s is None or isinstance(s, int):
+            return s
+        raise
 
 
 def _check(st, pool=None):
@@ -371,9 +373,10 @@ class Tables:
 
 
 def gk_tables_step(pool, stream, tables, d_add, d_slot_mapping, d_done, d_release=None, n_slots=None):
-    n_slots = d_slot_mapping.numel() if n_slots is None else n_slots
-    _check(lib().gk_tables_step(pool, _stream(stream), tables.ref, _ptr(d_release), _ptr(d_add), n_slots,
-                                _ptr(d_slot_mapping), _ptr(d_done)), pool)
+    st = lib().gk_tables_step(pool, _stream(stream), tables.ref, None if d_release is None else _ptr(d_release), _ptr(d_add),
+                              d_slot_mapping.numel() if n_slots is None else n_slots, _ptr(d_slot_mapping), _ptr(d_done))
+    if st:
+        _check(st, pool)
 
 
 # ---- device work -------------------------------------------------------------------
@@ -563,7 +566,9 @@ def gk_prompt_plan_items(plan):
 
 
 def gk_prompt_attn(pool, stream, layer, batch, plan):
-    _check(lib().gk_prompt_attn(pool, _stream(stream), layer, batch.ref, plan), pool)
+    st = lib().gk_prompt_attn(pool, _stream(stream), layer, batch.ref, plan)
+    if st:
+        _check(st, pool)
 
 
 def gk_dispatch(pool, plan):

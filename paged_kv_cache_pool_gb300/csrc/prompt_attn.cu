@@ -12,7 +12,7 @@
 // floor(128 / g); the g query heads of a token are g consecutive rows, so an item
 // is two 128-row Q tiles) x a range of 128-key tiles.  Keys come in tiles of one
 // source each: HOT tiles (2D tensor map over the whole HOT pool), COLD tiles
-// (rows gathered through the block table by two warps with 16-byte cp.async),
+// (rows gathered through the block table by four warps with 16-byte cp.async),
 // then tiles of new tokens (3D tensor maps over the caller's packed tensors).
 // S_i = Q_i K^T and O_i += P_i V accumulate in tensor memory (512 columns: S_0
 // S_1 O_0 O_1; P_i overwrites S_i as bf16).  Softmax warpgroup i owns Q tile i, one
@@ -32,23 +32,35 @@
 // shared memory) and run the lists of items that the plan balanced.  K and V tiles
 // share one ring of stages, and the loads of the next item start while the
 // softmax of the last one ends.  The ring's element after an item's last V tile
-// stages its output: rows of 128 bytes go out whole, where each thread's own stores
-// of its row took 5800 cycles an item.
+// stages its output, so that rows go out in whole 128-byte lines.
+//
+// What it measured (GB300, one layer, CUDA graph replays): 16384 tokens on 40/8 heads of
+// 128 in 1700 us, 1.62 PFLOP/s, 83 % of the measured bf16 peak; 8192 tokens on 32/8 heads
+// 343 us.  A key tile of two Q tiles takes 1.54 us, about 3100 cycles, where its four
+// products alone are 2048: what bounds it is the chain S -> softmax -> PV and next S ->
+// softmax through four hand-overs, of which the two Q tiles overlap only part.  An item
+// costs 4.5 us besides (first Q, first reference, output), which is what bounds short
+// prompts: 64 prompts of 256 tokens on 32/8 heads take 94 us.  Tried and slower, in ns
+// a key tile: an issuing warp per Q tile (24 % more), two threads a row (2516, spilling),
+// probabilities stored as they come (1643 -> 1876), handed over in two halves (1542 ->
+// 1674: the issuing warp's waits queue behind its own products), the first reference
+// from registers already loaded (1542 -> 1677, spilling), and at d = 64 P in columns of
+// its own with S issued a tile ahead (6 %).
 //
 // Masked keys.  Scores are masked by selection, so whatever K holds in a masked
 // place does no harm; the product P V, though, would turn a masked 0 times an
 // infinity or NaN in V into NaN.  So V tiles with masked places (the end of a HOT
-// prefix, the diagonal and the end of the new tokens) pass through the two
-// gather warps, which zero the rows past the end (another request's tokens)
-// and rows that hold an infinity or NaN and are hidden from some row of
-// the item; the rows that do see such a key add its term in the epilogue
-// (add_hidden_values, never taken for finite values).
+// prefix, the diagonal and the end of the new tokens) pass through the gather
+// warps, which zero the rows past the end (another request's tokens) and rows that
+// hold an infinity or NaN and are hidden from some row of the item; the rows that
+// do see such a key add its term in the epilogue (add_hidden_values, never taken
+// for finite values).
 //
 // Warp roles (512 threads): 0 TMA, 1 MMA and tensor memory, 2-3 and 13-14 gather
 // and scan, 4-7 and 8-11 softmax of Q tiles 0 and 1, 12 operand relay, 15 idle.  The
-// block starts with 128 registers a thread; the softmax warpgroups take 176 and
-// the other two warpgroups give theirs up to 80 (a spill in the softmax loop was
-// measured to halve the kernel's speed).
+// block starts with 128 registers a thread; the softmax warpgroups take 152 and the
+// other two keep 104 (spills in the softmax loop were measured to halve the kernel's
+// speed, spills in the other roles to cost 6 %).
 #include <cuda.h>
 
 #include <cmath>
