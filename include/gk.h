@@ -391,6 +391,7 @@ typedef struct gk_prompt_batch {
   const void* d_v;                /* device bf16 [T][Hkv][d] */
   void* d_out;                    /* device bf16 [T][Hq][d] */
   float* d_lse;                   /* device fp32 [T][Hq], natural log; may be NULL */
+  /* out and lse overlap no input */
   int64_t q_stride;               /* elements from one token's row to the next (views of a fused q k v */
   int64_t k_stride;               /* projection): a multiple of 8, at least heads * d; 0 = packed rows */
   int64_t v_stride;
@@ -419,10 +420,13 @@ typedef struct gk_prompt_plan_summary {
  * graph.  Tables and partial states are owned by the plan; calls that use a plan
  * must be ordered on one stream.  GK_ERR_INVALID for a negative length, a HOT
  * prefix that is not live with that length, a context longer than its
- * block-table row, or more than 2^31 - 1 tokens.  Allocates device memory: not
- * while the stream is capturing. */
+ * block-table row, or more than 2^31 - 1 tokens.  Allocates device memory and
+ * uploads from a buffer that the next plan rewrites: on a stream that is capturing
+ * it does nothing and returns GK_ERR_UNSUPPORTED. */
 gk_status gk_prompt_plan_build(gk_pool* pool, const gk_prompt_batch* batch, void* stream, gk_prompt_plan** out);
-/* Re-plan for the next step, reusing the buffers; on the stream of the plan's earlier work. */
+/* Re-plan for the next step, reusing the buffers; on the stream of the plan's earlier
+ * work.  A graph captured with the plan holds the launch of the step planned then:
+ * after an update it must not be replayed, but captured again. */
 gk_status gk_prompt_plan_update(gk_prompt_plan* plan, const gk_prompt_batch* batch, void* stream);
 /* Frees the plan's buffers; its enqueued work must have completed. */
 void gk_prompt_plan_destroy(gk_prompt_plan* plan);

@@ -20,6 +20,9 @@
 // on scheduling.  A step moves 8 bytes per token and 8 per block: it is bound by round
 // trips to L2 and by its launch, which is why it is one launch (three of them, a scan,
 // a push and a fill kernel, took 9-13 us on the GPU and 13 us of the host's time).
+// What it measured (GB300, CUDA graph replays): a decode step of 368 rows of which eight
+// give back 10900 blocks 6.2 us; 48 rows taking 20 thousand slots in pages of 16 6.8 us;
+// 24 rows taking 119 thousand slots 11.4 us; 1024 rows running out of blocks 7.5 us.
 #include <algorithm>
 
 #include "device_common.cuh"
@@ -274,20 +277,21 @@ __global__ void __launch_bounds__(kThreads) tables_step_kernel(const StepParams 
       push_at[tid] = (int32_t)v[2];
       __syncthreads();
       int32_t* dst = p.free + n0 + base[2];
-      const int32_t stride = kFit ? ctas * kThreads : kThreads;
-      for (int32_t i0 = (kFit ? rank * kThreads : 0) + tid; i0 < sum[2]; i0 += kUnroll * stride) {
+      const uint32_t n_push = (uint32_t)sum[2];            // below 2^31: the strides cannot wrap
+      const uint32_t stride = kFit ? ctas * kThreads : kThreads;
+      for (uint32_t i0 = (kFit ? rank * kThreads : 0) + tid; i0 < n_push; i0 += kUnroll * stride) {
         int32_t id[kUnroll];
 #pragma unroll
         for (int k = 0; k < kUnroll; ++k) {
-          const int32_t i = i0 + k * stride;
-          if (i < sum[2]) {
+          const uint32_t i = i0 + k * stride;
+          if (i < n_push) {
             const int q = last_at_most(n_here, i, [&](int x) { return (int64_t)push_at[x]; });
-            id[k] = p.table[(int64_t)(r0 + q) * p.max_blocks + (i - push_at[q])];
+            id[k] = p.table[(int64_t)(r0 + q) * p.max_blocks + ((int32_t)i - push_at[q])];
           }
         }
 #pragma unroll
         for (int k = 0; k < kUnroll; ++k)
-          if (i0 + k * stride < sum[2]) dst[i0 + k * stride] = id[k];
+          if (i0 + k * stride < n_push) dst[i0 + k * stride] = id[k];
       }
       __syncthreads();
     }
@@ -388,12 +392,15 @@ int launch_tables_step(const LaunchCommon& lc, void* stream, const gk_tables* t,
   p.done = d_done;
   p.work = (TableRowDev*)t->d_work;
   p.err = lc.d_error;
-  // The CTAs of the cluster: one where its threads have a round of four tokens each at most
-  // and nothing is released, else eight; sixteen (the most a cluster has) for longer maps.
+  // The CTAs of the cluster: one for few tokens and no releases, else sixteen (the most a
+  // cluster has).  One against sixteen on a GB300: 64 rows of a token each 4.6 / 4.8 us, 1000
+  // rows of a token each 6.5 / 7.0, 64 rows of 64 tokens 6.4 / 5.4, 64 rows of 500 tokens
+  // 21.9 / 5.8, 368 rows of a token each while eight rows give back 10900 blocks 12.4 / 6.3.
+  // Eight CTAs were no faster than sixteen anywhere (119 thousand tokens: 16.8 against 11.4).
   const bool fit = p.rows <= kThreads;
-  const int ctas = n_slots > 8 * kUnroll * kThreads ? 16 : d_release || n_slots > kUnroll * kThreads || !fit ? 8 : 1;
+  const int ctas = d_release || n_slots > 2 * kThreads || !fit ? kMaxCtas : 1;
   auto kern = fit ? tables_step_kernel<true> : tables_step_kernel<false>;
-  if (ctas > 8) {
+  if (ctas > 1) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return (int)e;
   }
@@ -425,6 +432,11 @@ extern "C" gk_status gk_tables_step(gk_pool* pool, void* stream, const gk_tables
     if (!t->d_len || !t->d_len_out || !t->d_num_free || !t->d_num_free_out || !t->d_work || !d_add || !d_done ||
         (t->max_blocks > 0 && !t->d_table) || (t->capacity > 0 && !t->d_free) || (n_slots > 0 && !d_slot_mapping))
       return gk::fail(p, GK_ERR_INVALID, "null device pointer");
+    for (const void* ptr : {(const void*)t->d_table, (const void*)t->d_free, (const void*)t->d_len, (const void*)t->d_len_out,
+                            (const void*)t->d_num_free, (const void*)t->d_num_free_out, (const void*)d_release,
+                            (const void*)d_add, (const void*)d_done})
+      if ((uintptr_t)ptr % 4 != 0) return gk::fail(p, GK_ERR_INVALID, "int32 arrays must be 4-byte aligned");
+    if ((uintptr_t)d_slot_mapping % 8 != 0) return gk::fail(p, GK_ERR_INVALID, "the slot map must be 8-byte aligned");
     if ((uintptr_t)t->d_work % 16 != 0) return gk::fail(p, GK_ERR_INVALID, "d_work must be 16-byte aligned");
   }
   gk_status st = gk::ensure_device(p);

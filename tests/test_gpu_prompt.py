@@ -2,6 +2,8 @@
 from none to several tiles, each source of keys alone and together, strides,
 hidden infinities and NaN, bad block ids, captured graphs, other streams, and a
 whole step (slots, K/V writes, prompt attention, then decode over what it wrote)."""
+import random
+
 import numpy as np
 import pytest
 
@@ -27,7 +29,7 @@ class Prompts:
     """A pool with HOT prefixes and COLD contexts, and the packed new tokens of one step."""
 
     def __init__(self, d, g, hkv, new, prefixes=(), which=None, cold=None, page=16, layers=2, layer=1, seed=0, scale=1.0,
-                 fused=False, spare_nan=True):
+                 fused=False, spare_nan=True, spare_blocks=3, hot_skip=0):
         rng = torch.Generator(device="cuda").manual_seed(seed)
         bf = torch.bfloat16
         self.new, self.layer, self.d, self.hkv, self.hq, self.page = list(new), layer, d, hkv, hkv * g, page
@@ -36,15 +38,17 @@ class Prompts:
 
         def rand(*shape):
             return torch.randn(*shape, generator=rng, device="cuda").to(bf)
-        hot = max(1, sum(prefixes)) + 5
+        hot = max(1, sum(prefixes)) + 5 + hot_skip
         blocks = [-(-c // page) for c in cold]
-        slots = (sum(blocks) + 3) * page
+        slots = (sum(blocks) + spare_blocks) * page
         # everything that no key lives in holds NaN
         junk = float("nan") if spare_nan else 0.0
         self.hot = [torch.full((hot * layers * hkv * d,), junk, dtype=bf, device="cuda") for _ in range(2)]
         self.cold = [torch.full((layers, slots, hkv, d), junk, dtype=bf, device="cuda") for _ in range(2)]
         self.pool = gk.gk_pool_create(layers, self.hq, hkv, d, hot, slots, page, 11, *self.hot, *self.cold)
         bases, pre = [], []
+        if hot_skip:
+            gk.gk_prefix_alloc(self.pool, hot_skip)      # the prefixes come behind it
         for lp in prefixes:
             bases.append(gk.gk_prefix_alloc(self.pool, lp))
             k, v = rand(lp, hkv, d), rand(lp, hkv, d)
@@ -333,3 +337,121 @@ def test_chunks_of_a_prompt_equal_the_whole():
         torch.cuda.synchronize()
         assert (l1[0] - lse[-1]).abs().max() < 1e-3 and (o1[0] - out[-1].float()).abs().max() < 2e-2
     eng.close()
+
+
+def test_strided_output():
+    """Rows of out inside a wider tensor, whose other columns stay."""
+    p = Prompts(128, 4, 2, [70, 3, 200], prefixes=[130], which=[0, -1, -1], cold=[0, 900, 0], fused=True)
+    wide = torch.full((p.T, p.hq * p.d + 24), 5.0, dtype=torch.bfloat16, device="cuda")
+    p.out = wide[:, 8:8 + p.hq * p.d].view(p.T, p.hq, p.d)
+    p.run().verify("strided out")
+    assert (wide[:, :8] == 5).all() and (wide[:, 8 + p.hq * p.d:] == 5).all()
+    p.close()
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_random_steps(seed):
+    r = random.Random(seed)
+    d, g = r.choice(GEOMETRIES)
+    page, b = r.choice([1, 3, 16, 64]), r.choice([1, 2, 5, 12, 30])
+    most = r.choice([3, 40, 300, 900]) if b < 12 else r.choice([1, 8, 60])
+    prefixes = [r.randint(1, 1500) for _ in range(r.randint(1, 3))]
+    prompts(d, g, r.choice([1, 2, 3]), [r.randint(0, most) for _ in range(b)], prefixes=prefixes,
+            which=[r.randint(-1, len(prefixes) - 1) for _ in range(b)], cold=[r.choice([0, r.randint(0, 700)]) for _ in range(b)],
+            page=page, seed=seed, fused=r.random() < 0.5, scale=r.choice([1.0, 1.0, 6.0]))
+
+
+def test_many_small_requests():
+    r = random.Random(5)
+    prompts(128, 4, 2, [r.randint(0, 9) for _ in range(400)], prefixes=[700, 129, 1], which=[min(3, i // 120) - 1 for i in range(400)],
+            cold=[r.choice([0, 1, 17, 150]) for _ in range(400)], page=4)
+
+
+@pytest.mark.parametrize("d,g", [(64, 4), (128, 5)])
+def test_one_long_prompt(d, g):
+    prompts(d, g, 1, [4500], cold=[1000])
+
+
+@pytest.mark.parametrize("bad", [-float("inf"), -1e30])
+def test_keys_that_score_the_lowest(bad):
+    """Visible keys whose scores are minus infinity, or far below every other, weigh nothing; also as a row's first keys."""
+    p = Prompts(128, 4, 2, [200, 40], cold=[0, 150])
+    p.q[:, :, 0] = p.q[:, :, 0].abs() + 0.5
+    p.k[0:70, :, 0] = bad            # hides the first keys of request 0; its own rows 70.. see others
+    p.k[130:141, :, 0] = bad
+    p.k[230:235, :, 0] = bad
+    p.run()
+    torch.cuda.synchronize()
+    O, A, L = p.want()
+    seen = np.isfinite(L).all(1) & (L > -1e20).all(1)
+    assert seen.sum() == 240 - 70
+    check(p.host(p.out)[seen], p.host(p.lse)[seen], (O[seen], A[seen], L[seen]), f"lowest {bad}")
+    p.close()
+
+
+@pytest.mark.parametrize("where", ["cold", "hot"])
+def test_caches_past_32_bit_offsets(where):
+    """K and V of the pool lie more than 2^31 elements behind its first."""
+    if where == "cold":
+        p = Prompts(128, 4, 8, [100], cold=[400], page=16, spare_blocks=140000)
+        at = p.cold[0].numel()
+    else:
+        p = Prompts(128, 4, 8, [100], prefixes=[333], which=[0], hot_skip=1100000)
+        at = p.hot[0].numel()
+    assert at > 2 ** 31
+    p.run().verify(where)
+    p.close()
+
+
+def test_plans_are_not_built_or_updated_while_capturing():
+    p = Prompts(128, 4, 2, [30, 2], cold=[0, 300])
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        p.run(side)
+        side.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            with pytest.raises(gk.GkError) as e:
+                gk.gk_prompt_plan_build(p.pool, p.batch, side)
+            assert e.value.status == gk.GK_ERR_UNSUPPORTED
+            with pytest.raises(gk.GkError) as e:
+                gk.gk_prompt_plan_update(p.pool, p.plan, p.batch, side)
+            assert e.value.status == gk.GK_ERR_UNSUPPORTED
+            p.run(side)              # the plan is as it was
+    p.out.fill_(0)
+    graph.replay()
+    p.verify("after refusals")
+    p.close()
+
+
+def test_two_graphs_of_one_plan_replayed_in_turn():
+    """They share the plan's partial states; on one stream each replay ends before the next begins."""
+    p = Prompts(128, 4, 2, [6], cold=[3000])
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    outs, graphs = [], []
+    with torch.cuda.stream(side):
+        p.run(side)
+        side.synchronize()
+        assert p.info()["partials"] > 0
+        q2 = (p.q * -0.5).contiguous()
+        for q in (p.q, q2):
+            out = torch.zeros_like(p.out)
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=side):
+                p.batch.set_device(q, p.k, p.v, out, p.lse)
+                gk.gk_prompt_attn(p.pool, side, p.layer, p.batch, p.plan)
+            outs.append(out)
+            graphs.append(graph)
+        for i in range(20):
+            graphs[i & 1].replay()
+    torch.cuda.synchronize()
+    p.out = outs[1]
+    p.q.copy_(q2)
+    p.verify("second graph")
+    p.q.copy_(q2 * -2)
+    p.run()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], p.out)
+    p.close()

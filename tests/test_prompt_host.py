@@ -147,6 +147,11 @@ def test_launch_refusals(gk):
         batch.set_device(4096, 4096 + 8, 4096, 4096, None, 4096, 2)
         refused("aligned")
         batch.set_device(4096, 4096, 4096, 4096)
+        for field, bad in (("d_lse", 4098), ("d_block_table", 4097)):
+            was = getattr(batch.c, field)
+            setattr(batch.c, field, bad)
+            refused("4-byte aligned")
+            setattr(batch.c, field, was)
         for field, bad in (("q_stride", 1016), ("q_stride", 1028), ("k_stride", 248), ("v_stride", -256), ("out_stride", 2 ** 39)):
             setattr(batch.c, field, bad)
             refused("stride")

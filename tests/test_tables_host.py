@@ -34,6 +34,9 @@ def test_refusals(gk):
         refused("null", done=None)
         refused("null", slots=None, n_slots=3)
         refused("aligned", d_work=4096 + 8)
+        for field in ("d_table", "d_free", "d_len", "d_len_out", "d_num_free", "d_num_free_out"):
+            refused("4-byte aligned", **{field: 4096 + 2})
+        refused("8-byte aligned", slots=4096 + 4, n_slots=3)
         refused("no device storage")
         assert gk.lib().gk_tables_step(None, None, None, None, None, 0, None, None) == gk.GK_ERR_INVALID
         for bad in (dict(table=ints(4, 3).float()), dict(length=ints(3)), dict(num_free=ints(2)), dict(table=ints(3, 4).t()),
