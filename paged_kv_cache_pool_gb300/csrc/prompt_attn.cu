@@ -87,7 +87,7 @@ constexpr int kSoftmaxRegs = 152, kOtherRegs = 104;   // 128 * (2 * 152 + 2 * 10
 
 
 struct Params {
-  CUtensorMap tq, tk, tv;         // the call's packed tensors
+  CUtensorMap tq, tk, tv, tout;   // the call's packed tensors
   CUtensorMap thk, thv;           // the HOT pool
   const PromptReqDev* reqs;
   const PromptItemDev* items;
@@ -127,7 +127,8 @@ enum : int {
   B_RFULL = 9,                    // 8 each
   B_REMPTY = 17,
   B_RSCAN = 25,
-  B_COUNT = 33
+  B_ROUT = 33,
+  B_COUNT = 41
 };
 constexpr uint32_t kCtlTmemSlot = B_COUNT * 8;
 constexpr uint32_t kCtlAbort = kCtlTmemSlot + 4;
@@ -139,10 +140,10 @@ struct Slot {
   PromptItemDev it;
   PromptReqDev rq;
 };
-constexpr uint32_t kCtlSlots = 304;
+constexpr uint32_t kCtlSlots = 352;
 constexpr uint32_t kCtlBytes = 512;
 static_assert(kCtlHidden + 4 <= kCtlSlots && kCtlSlots + 2 * sizeof(Slot) <= kCtlBytes, "prompt control block");
-constexpr int kSlotReaders = 10;          // MMA, relay and softmax warps
+constexpr int kSlotReaders = 2;           // MMA and relay warps
 // dynamic shared memory starts 1024-byte aligned (checked by the kernel)
 static_assert(Layout<128>::kData + kCtlBytes <= 232448 && Layout<64>::kData + kCtlBytes <= 232448, "shared memory");
 
@@ -156,6 +157,20 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* tmap, int 
       "l"(tmap), "r"(x), "r"(y), "r"(bar)
       : "memory");
 }
+__device__ __forceinline__ void tma_prefetch_3d(const void* tmap, int x, int y, int z) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(tmap), "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
+// a whole tile from shared memory to global memory, in the thread's current bulk group
+__device__ __forceinline__ void tma_store_3d(const void* tmap, int x, int y, int z, uint32_t src) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(tmap), "r"(x),
+               "r"(y), "r"(z), "r"(src)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// the thread's bulk stores have read their sources; or are done
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 // 16-byte copy, or 16 zero bytes when !valid (the source is then not read)
 __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool valid) {
   const uint32_t n = valid ? 16u : 0u;
@@ -213,6 +228,21 @@ __device__ __forceinline__ int tile_count(const PromptItemDev& it, const PromptR
   return max(0, min(it.tile0 + it.ntile, total) - it.tile0);
 }
 
+// the ring's elements that stage an item's output: one for each Q tile with key tiles
+__device__ __forceinline__ int staging_count(const PromptItemDev& it, const PromptReqDev& rq, int tpt) {
+  return (tile_count(it, rq, tpt, 0) > 0) + (tile_count(it, rq, tpt, 1) > 0);
+}
+// Partial rows staged kRowBytes at a time: the byte of 16-byte chunk c of row r.  Neither a
+// thread's row nor the chunks that a quarter warp reads of one meet in a bank.
+template <int kRowBytes>
+__device__ __forceinline__ uint32_t staged(int r, int c) {
+  return (uint32_t)(r * kRowBytes + ((c ^ (kRowBytes >= 128 ? r & 7 : (r >> 1) & 3)) << 4));
+}
+// Output rows staged as TMA's 128-byte swizzle has them, 64 columns a region
+__device__ __forceinline__ uint32_t staged_out(int r, int c) {
+  return (uint32_t)(c >> 3) * kRegionQ + (uint32_t)(r * 128 + (((c ^ r) & 7) << 4));
+}
+
 // does a V tile hold places that some row of the item must not see?
 __device__ __forceinline__ bool scanned(const PromptItemDev& it, const PromptReqDev& rq, int t) {
   if (t < rq.nt_hot) return (t + 1) * BN > rq.lp;
@@ -223,8 +253,10 @@ __device__ __forceinline__ bool scanned(const PromptItemDev& it, const PromptReq
 // rows were zeroed in shared memory because other rows of the item must not see
 // them.  p_j v_j is added to O (tensor memory) for the rows that do.
 template <int D>
-__device__ __noinline__ void add_hidden_values(const Params& p, const PromptItemDev it, const PromptReqDev rq, int tk,
-                                               int qh, bool valid, float m, uint32_t tO) {
+__device__ __noinline__ void add_hidden_values(const Params& p, int item, int token, int hr, bool valid, float m, uint32_t tO) {
+  const PromptItemDev it = p.items[item];
+  const PromptReqDev rq = p.reqs[it.req];
+  const int tk = it.tok0 + token, qh = it.head * p.G + hr;
   const int hi = valid ? tk : -1;
   const int top = __reduce_max_sync(0xffffffffu, hi);
   for (int j = it.tok0 + 1; j <= top; ++j) {
@@ -335,6 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       mbar_init(bar(B_REMPTY + s), 8);  // one arrival of the MMAs' end and seven of the relay, or the softmax warps'
       mbar_init(bar(B_RFULL + s), 4);   // the TMA thread arrives four times, or each gather warp once
       mbar_init(bar(B_RSCAN + s), 1);
+      mbar_init(bar(B_ROUT + s), 4);    // a Q tile's softmax warps: its output is staged
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(B_SFULL + i), 1);
@@ -385,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         next.it = p.items[i0];
         next.rq = p.reqs[next.it.req];
       }
-      for (const CUtensorMap* tm : {&p.tq, &p.tk, &p.tv})
+      for (const CUtensorMap* tm : {&p.tq, &p.tk, &p.tv, &p.tout})
         asm volatile("prefetch.tensormap [%0];" ::"l"(tm) : "memory");
       griddep_wait();
       for (int ii = i0; ok && ii < i1; ++ii) {
@@ -396,7 +429,22 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           next.rq = p.reqs[next.it.req];
         }
         const int nctx = rq.nt_hot + rq.nt_cold;
-        for (int j = 0; j <= 2 * it.ntile; ++j) {
+        const int n_el = 2 * it.ntile + staging_count(it, rq, p.tpt);
+        for (int j = 0; j < n_el; ++j) {
+          if (j == 1) {
+            // the Q tiles, once the last product with the item before has read its own
+            if (!wait_or_abort(bar(B_QEMPTY), (qn & 1u) ^ 1u, p.err, abort_flag)) { ok = false; break; }
+            slots[qn & 1u].it = it;
+            slots[qn & 1u].rq = rq;
+            ++qn;
+            const bool two = it.tok0 + p.tpt < rq.n;
+            const uint32_t q_bytes = (uint32_t)(p.tpt * p.G) * 128u * (D / 64);
+            mbar_arrive_expect_tx(bar(B_QFULL), two ? 2 * q_bytes : q_bytes);
+            for (int i = 0; i < (two ? 2 : 1); ++i)
+              for (int h = 0; h < D / 64; ++h)
+                tma_load_3d(sQ + i * Lay::kQTile + h * kRegionQ, &p.tq, h * 64, it.head * p.G,
+                            rq.t0 + it.tok0 + i * p.tpt, bar(B_QFULL));
+          }
           const int t = it.tile0 + (j >> 1);
           const bool is_v = j & 1;
           const int st = ring.st;
@@ -406,10 +454,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           // behind.  The gather warps, which would fall behind over tiles that are none of theirs,
           // learn through B_RSCAN which stage is theirs.
           if (!wait_or_abort(bar(B_REMPTY + st), ph ^ 1u, p.err, abort_flag)) { ok = false; break; }
-          if (j == 2 * it.ntile) {                 // the staging element
+          if (j >= 2 * it.ntile) {                 // a staging element
             in_ring &= ~(1u << st);
             in_scan &= ~(1u << st);
-            staged |= 1u << st;
+            if (it.entry >= 0) staged |= 1u << st;   // written and read by the softmax warps only
             mbar_arrive_n(bar(B_RFULL + st), 4);
           } else if (t >= rq.nt_hot && t < nctx) { // COLD: to the gather warps
             in_ring &= ~(1u << st);
@@ -442,19 +490,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             full_ph = (full_ph & ~bit) | (ph << st);
             if (scan) scan_ph ^= bit;
           }
-          if (j == 1) {
-            // the Q tiles, once the last product with the item before has read its own
-            if (!wait_or_abort(bar(B_QEMPTY), (qn & 1u) ^ 1u, p.err, abort_flag)) { ok = false; break; }
-            slots[qn & 1u].it = it;
-            slots[qn & 1u].rq = rq;
-            ++qn;
-            const bool two = it.tok0 + p.tpt < rq.n;
-            const uint32_t q_bytes = (uint32_t)(p.tpt * p.G) * 128u * (D / 64);
-            mbar_arrive_expect_tx(bar(B_QFULL), two ? 2 * q_bytes : q_bytes);
-            for (int i = 0; i < (two ? 2 : 1); ++i)
+          if (j == 1 && ii + 1 < i1) {
+            // the next item's Q tiles to L2: they are waited for at each item's start
+            for (int i = 0; i < (next.it.tok0 + p.tpt < next.rq.n ? 2 : 1); ++i)
               for (int h = 0; h < D / 64; ++h)
-                tma_load_3d(sQ + i * Lay::kQTile + h * kRegionQ, &p.tq, h * 64, it.head * p.G,
-                            rq.t0 + it.tok0 + i * p.tpt, bar(B_QFULL));
+                tma_prefetch_3d(&p.tq, h * 64, next.it.head * p.G, next.rq.t0 + next.it.tok0 + i * p.tpt);
           }
         }
       }
@@ -541,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         }
         __syncwarp();
       }
-      k.next();                    // the staging element
+      k.skip((cnt[0] > 0) + (cnt[1] > 0));
     }
     // arrives once every MMA issued above has finished, aborted or not
     if (elect_one()) tc_commit(bar(B_FINAL));
@@ -648,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       }
       if (!ok) break;
       flush();
-      ring.next();                                 // the staging element
+      ring.skip(staging_count(it, rq, p.tpt));
     }
     if (ok) flush();
     else cp_async_wait_all();
@@ -686,9 +726,62 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
               if (ok) mbar_arrive(bar(B_PFULL + i));
             }
         }
-        ring.next();                   // the staging element
+        ring.skip((cnt[0] > 0) + (cnt[1] > 0));
       }
     }
+  } else {
+    // ------------------------------- output rows --------------------------------
+    // Staged bf16 rows to global memory while the softmax warps are at the next item (they
+    // took 2300 cycles an item to write them themselves): whole Q tiles by TMA, the last
+    // rows of a request, whose tile holds another's behind them, 512 bytes an instruction.
+    constexpr int kChunks = D / 8, kRows = 32 / kChunks;
+    const int ch = lane % kChunks, sub = lane / kChunks;
+    const uint32_t inv_g = 65536u / (uint32_t)p.G + 1u;   // r * inv_g >> 16 = r / G for r < 128
+    griddep_wait();
+    Ring<NST> ring;
+    uint32_t out_ph = 0;
+    bool ok = true;
+    for (int ii = i0; ok && ii < i1; ++ii) {
+      const PromptItemDev it = p.items[ii];
+      const PromptReqDev rq = p.reqs[it.req];
+      ring.skip(2 * it.ntile);
+      for (int i = 0; i < 2; ++i) {
+        if (tile_count(it, rq, p.tpt, i) == 0) continue;
+        const int st = ring.st;
+        ring.next();
+        if (it.entry >= 0) continue;               // a partial state: the softmax warps write it
+        if (!wait(B_ROUT + st, out_ph >> st & 1u)) { ok = false; break; }
+        out_ph ^= 1u << st;
+        const uint32_t tile = sR + (uint32_t)st * Lay::kTile;
+        const int tok0 = it.tok0 + i * p.tpt;
+        if (lane == 0) fence_async_shared();       // the softmax warps' writes before TMA's reads, now or later
+        if (tok0 + p.tpt <= rq.n) {
+          if (lane == 0) {
+            for (int h = 0; h < D / 64; ++h)
+              tma_store_3d(&p.tout, h * 64, it.head * p.G, rq.t0 + tok0, tile + h * kRegionQ);
+            bulk_commit();
+            bulk_wait_read();
+          }
+        } else {
+          const int n = (rq.n - tok0) * p.G;
+          uint16_t* const out0 = p.out + (int64_t)(rq.t0 + tok0) * p.out_stride + it.head * p.G * D + ch * 8;
+#pragma unroll 1
+          for (int r0 = sub; r0 - sub < n; r0 += 8 * kRows) {
+            uint4 v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = lds128(tile + staged_out(r0 + k * kRows, ch));
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int r = r0 + k * kRows, tok = (int)((uint32_t)r * inv_g >> 16);
+              stg128_if(r < n, (uint64_t)(out0 + (int64_t)tok * p.out_stride + (r - tok * p.G) * D), v[k]);
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive_n(bar(B_REMPTY + st), 8);
+      }
+    }
+    if (lane == 0) bulk_wait();
   }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
@@ -700,35 +793,43 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     const uint32_t tSr = tS(qi) + lane_off, tOr = tO(qi) + lane_off;
     griddep_wait();
     uint32_t sn = 0, on = 0;
-    Ring<NST> ring;                               // moved to each item's staging element
+    Ring<NST> ring;                               // moved to the Q tile's staging element of each item
     bool ok = true;
-    for (int ii = i0; ok && ii < i1; ++ii) {
-      const uint32_t qn = (uint32_t)(ii - i0) & 1u;
-      if (!wait(B_QFULL, qn)) { ok = false; break; }
-      const PromptItemDev it = slots[qn].it;
-      const PromptReqDev rq = slots[qn].rq;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(B_QEMPTY));
-      ring.skip(2 * it.ntile);
+    // what the warp keeps of an item: the Q tile's key tiles, its staging element's place behind
+    // the item before and the elements after it, where the row's output goes (0: nowhere; the
+    // output warp has the address of an output row itself), the tiles with masked places counted
+    // from the item's first (the last HOT and COLD ones, and those on the diagonal), and how many
+    // keys the row sees there (rows of no token: as the last one)
+    int cnt = 0, skip = 0, rest = 0, j_hot = -1, j_cold = -1, j_new = 0, lim_hot = 0, lim_cold = 0, lim_new = 0;
+    bool part_row = false;
+    uint64_t dst = 0, lse_dst = 0;
+    auto open_item = [&](int ii) {
+      const PromptItemDev it = p.items[ii];
+      const PromptReqDev rq = p.reqs[it.req];
       const int nctx = rq.nt_hot + rq.nt_cold;
-      const int cnt = tile_count(it, rq, p.tpt, qi);
+      cnt = tile_count(it, rq, p.tpt, qi);
+      const bool other = tile_count(it, rq, p.tpt, qi ^ 1) > 0;
+      skip = 2 * it.ntile + (qi && other);
+      rest = (cnt > 0) + (!qi && other);
       const int tk = it.tok0 + qi * p.tpt + tr;
-      // where the row's output goes (0: nowhere), found while the first scores are on their way
-      const bool part_row = it.entry >= 0;
-      uint64_t dst = 0, lse_dst = 0;
+      part_row = it.entry >= 0;
+      dst = lse_dst = 0;
       if (tr < p.tpt && tk < rq.n) {
         const int qh = it.head * p.G + hr;
         const int64_t prow = (int64_t)it.entry * 256 + qi * BM + row, orow = rq.t0 + tk;
-        dst = part_row ? (uint64_t)(p.part_o + prow * D) : (uint64_t)(p.out + orow * p.out_stride + qh * D);
+        dst = part_row ? (uint64_t)(p.part_o + prow * D) : 1;
         lse_dst = part_row ? (uint64_t)(p.part_l + prow) : p.lse ? (uint64_t)(p.lse + orow * p.Hq + qh) : 0;
       }
-      // tiles with masked places, counted from the item's first: the last HOT and COLD ones and
-      // those on the diagonal; how many of its keys the row sees there (rows of no token: as the last one)
-      const int j_hot = rq.lp % BN ? rq.nt_hot - 1 - it.tile0 : -1;
-      const int j_cold = rq.ctx % BN ? nctx - 1 - it.tile0 : -1;
-      const int j_new = nctx - it.tile0 + (it.tok0 + qi * p.tpt + 1) / BN;
-      const int lim_hot = rq.lp % BN, lim_cold = rq.ctx % BN;
-      const int lim_new = min(tk, rq.n - 1) + 1 + (nctx - it.tile0) * BN;
+      j_hot = rq.lp % BN ? rq.nt_hot - 1 - it.tile0 : -1;
+      j_cold = rq.ctx % BN ? nctx - 1 - it.tile0 : -1;
+      j_new = nctx - it.tile0 + (it.tok0 + qi * p.tpt + 1) / BN;
+      lim_hot = rq.lp % BN;
+      lim_cold = rq.ctx % BN;
+      lim_new = min(tk, rq.n - 1) + 1 + (nctx - it.tile0) * BN;
+    };
+    if (i0 < i1) open_item(i0);
+    for (int ii = i0; ok && ii < i1; ++ii) {
+      ring.skip(skip);
       // m: the reference of every exponent so far (-inf: no key seen), part: the last tile's sum, l: the row's
       float m = -INFINITY, part = 0.f, l = 0.f;
       bool adjust = true;                         // some row of the warp needs another reference
@@ -756,16 +857,23 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         if (!wait(B_SFULL + qi, sn & 1u)) { ok = false; break; }
         ++sn;
         tc_fence_after();
-        int lim = BN;
-        bool masked = false;
         if (j == j_hot || j == j_cold || j >= j_new) {
-          lim = j == j_hot ? lim_hot : j == j_cold ? lim_cold : lim_new - j * BN;
-          masked = __any_sync(0xffffffffu, lim < BN);
-        }
-        auto mask = [&](float* s, int c0) {
+          // minus infinity over the hidden scores, in tensor memory: one copy of the code below then
+          // serves every tile (with two, the second one's instructions were fetched anew each item)
+          const int lim = j == j_hot ? lim_hot : j == j_cold ? lim_cold : lim_new - j * BN;
+#pragma unroll 1
+          for (int c = 0; c < BN; c += 32) {
+            if (__all_sync(0xffffffffu, lim >= c + 32)) continue;
+            float s[32];
+            tmem_ld32(tSr + c, s);
+            tc_wait_ld();
+            tie32(s);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) s[e] = c0 + e < lim ? s[e] : -INFINITY;
-        };
+            for (int e = 0; e < 32; ++e) s[e] = e < lim - c ? s[e] : -INFINITY;
+            tmem_st32(tSr + c, s);
+          }
+          tc_wait_st();
+        }
         // the row's maximum over the tile's first keys, in log2 units, rounded up: no exponent against it is above 0
         auto maximum = [&](int keys) {
           float mx = -INFINITY;
@@ -775,7 +883,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             tmem_ld32(tSr + c, s);
             tc_wait_ld();
             tie32(s);
-            mask(s, c);
             mx = fmaxf(mx, max32(s));
           }
           return __fmul_ru(mx, p.scale_log2);
@@ -792,9 +899,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           raise(m_new, j > 0);
         }
         uint32_t pk[BN / 2];
-        // P and the row's sum in the tile.  Straight-line code where nothing is masked: the
-        // selections' branches between the exponentials cost a quarter of their time.
-        auto exponentials = [&](auto with_mask) {
+        // P and the row's sum in the tile
+        auto exponentials = [&]() {
           const float m_sub = m == -INFINITY ? 0.f : m;     // a row that sees no key yet: -inf - 0
           const uint64_t sc2 = f2pack(p.scale_log2, p.scale_log2), nm2 = f2pack(-m_sub, -m_sub);
           uint64_t sum4[4] = {0, 0, 0, 0};
@@ -806,18 +912,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           tie32(sa + 32);
           tmem_ld32(tSr + 64, sb);
           tmem_ld32(tSr + 96, sb + 32);
-          if (decltype(with_mask)::value) {
-            mask(sa, 0);
-            mask(sa + 32, 32);
-          }
           exp64(sa, pk, sum4, sc2, nm2);
           tc_wait_ld();
           tie32(sb);
           tie32(sb + 32);
-          if (decltype(with_mask)::value) {
-            mask(sb, 64);
-            mask(sb + 32, 96);
-          }
           exp64(sb, pk + 32, sum4, sc2, nm2);
           float s0, s1, s2, s3;
           f2unpack(fadd2(sum4[0], sum4[1]), s0, s1);
@@ -825,8 +923,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           part = (s0 + s1) + (s2 + s3);
         };
         for (bool again = false;; again = true) {
-          if (masked || again) exponentials(std::true_type());
-          else exponentials(std::false_type());
+          exponentials();
           if (again || !__any_sync(0xffffffffu, part > 0x1p64f)) break;
           // far above the reference: raise it and take the tile again (its S is still there)
           raise(fmaxf(m, maximum(BN)), j > 0);
@@ -840,40 +937,30 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         adjust = __any_sync(0xffffffffu, m == -INFINITY || part > 256.f);
       }
       if (!ok) break;
-      if (cnt > 0) {
-        if (!__all_sync(0xffffffffu, wait_or_abort(bar(B_OFULL + qi), on & 1u, p.err, abort_flag))) { ok = false; break; }
+      // the next item's records while the last product runs
+      const int cnt_now = cnt, rest_now = rest;
+      const bool part_now = part_row;
+      const uint64_t dst_now = dst, lse_now = lse_dst;
+      if (ii + 1 < i1) open_item(ii + 1);
+      if (cnt_now > 0) {
+        if (!wait(B_OFULL + qi, on & 1u)) { ok = false; break; }
         ++on;
         tc_fence_after();
         if (__any_sync(0xffffffffu, *hidden_flag))
-          add_hidden_values<D>(p, slots[qn].it, slots[qn].rq, tk, slots[qn].it.head * p.G + hr, dst != 0, m, tOr);
+          add_hidden_values<D>(p, ii, qi * p.tpt + tr, hr, dst_now != 0, m, tOr);
       }
       const float inv = l > 0.f || l != l ? __fdividef(1.f, l) : 0.f;   // no key in this range: O = 0, LSE = -inf
       const float lse2 = m + __log2f(l);
-      if (lse_dst) *reinterpret_cast<float*>(lse_dst) = part_row ? lse2 : lse2 * kLn2;
-      if (cnt > 0) {
+      if (lse_now) *reinterpret_cast<float*>(lse_now) = part_now ? lse2 : lse2 * kLn2;
+      if (cnt_now > 0) {
         // the staging element (its stage's earlier tiles were used by this Q tile, or by an earlier
         // item: the wait cannot be a phase behind)
         if (!wait(B_RFULL + ring.st, ring.ph)) { ok = false; break; }
-        // kRow bytes of each of the warp's 32 rows at a time, 16-byte chunks swizzled so that
-        // neither a thread's row nor a quarter warp's chunks meet in a bank
-        constexpr int kRow = D, kChunks = kRow / 16;
-        const uint32_t stage = sR + (uint32_t)ring.st * Lay::kTile + (uint32_t)(qi * 4 + (warp & 3)) * (32 * kRow);
-        auto chunk = [&](int r, int c) { return stage + r * kRow + ((c ^ (kChunks == 8 ? r & 7 : (r >> 1) & 3)) << 4); };
-        auto send = [&](int offset) {              // the staged bytes to their rows, at this byte of each
-          __syncwarp();
-          uint4 v[kChunks];
-          uint64_t to[kChunks];
-#pragma unroll
-          for (int k = 0; k < kChunks; ++k) {      // all on their way before the first is used
-            const int r = (k * 32 + lane) / kChunks;
-            v[k] = lds128(chunk(r, lane % kChunks));
-            to[k] = __shfl_sync(0xffffffffu, dst, r);
-          }
-#pragma unroll
-          for (int k = 0; k < kChunks; ++k) stg128_if(to[k] != 0, to[k] + offset + (lane % kChunks) * 16, v[k]);
-          __syncwarp();
-        };
-        if (part_row) {
+        const uint32_t stage = sR + (uint32_t)ring.st * Lay::kTile;
+        if (part_now) {
+          // fp32 rows, kRow bytes of each of the warp's 32 at a time
+          constexpr int kRow = D, kChunks = kRow / 16;
+          const uint32_t mine = stage + (uint32_t)(warp & 3) * (32 * kRow);
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
             float o[32];
@@ -884,35 +971,45 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             for (int h = 0; h < 32; h += kRow / 4) {
 #pragma unroll
               for (int e = 0; e < kRow / 4; e += 4)
-                sts128(chunk(lane, e / 4),
+                sts128(mine + staged<kRow>(lane, e / 4),
                        make_uint4(__float_as_uint(o[h + e] * inv), __float_as_uint(o[h + e + 1] * inv),
                                   __float_as_uint(o[h + e + 2] * inv), __float_as_uint(o[h + e + 3] * inv)));
-              send((c + h) * 4);
+              __syncwarp();
+              uint4 v[kChunks];
+              uint64_t to[kChunks];
+#pragma unroll
+              for (int k = 0; k < kChunks; ++k) {      // all on their way before the first is used
+                const int r = (k * 32 + lane) / kChunks;
+                v[k] = lds128(mine + staged<kRow>(r, lane % kChunks));
+                to[k] = __shfl_sync(0xffffffffu, dst_now, r);
+              }
+#pragma unroll
+              for (int k = 0; k < kChunks; ++k) stg128_if(to[k] != 0, to[k] + (c + h) * 4 + (lane % kChunks) * 16, v[k]);
+              __syncwarp();
             }
           }
+          if (lane == 0) mbar_arrive_n(bar(B_REMPTY + ring.st), 2);
         } else {
 #pragma unroll 1
-          for (int c = 0; c < D; c += kRow / 2) {
-            float o[kRow / 2];
-#pragma unroll
-            for (int h = 0; h < kRow / 2; h += 32) tmem_ld32(tOr + c + h, o + h);
+          for (int c = 0; c < D; c += 64) {
+            float o[64];
+            tmem_ld32(tOr + c, o);
+            tmem_ld32(tOr + c + 32, o + 32);
             tc_wait_ld();
+            tie32(o);
+            tie32(o + 32);
 #pragma unroll
-            for (int h = 0; h < kRow / 2; h += 32) tie32(o + h);
-#pragma unroll
-            for (int e = 0; e < kRow / 2; e += 8)
-              sts128(chunk(lane, e / 8),
+            for (int e = 0; e < 64; e += 8)
+              sts128(stage + staged_out(row, (c + e) / 8),
                      make_uint4(pack_bf16x2(o[e] * inv, o[e + 1] * inv), pack_bf16x2(o[e + 2] * inv, o[e + 3] * inv),
                                 pack_bf16x2(o[e + 4] * inv, o[e + 5] * inv),
                                 pack_bf16x2(o[e + 6] * inv, o[e + 7] * inv)));
-            send(c * 2);
           }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(B_ROUT + ring.st));   // to the output warp
         }
-        // eight arrivals give it back: a Q tile without tiles stays out of it altogether, as nothing
-        // would keep its warps from arriving for a stage that is still another element's
-        if (lane == 0) mbar_arrive_n(bar(B_REMPTY + ring.st), tile_count(it, rq, p.tpt, qi ^ 1) > 0 ? 1 : 2);
       }
-      ring.next();
+      ring.skip(rest_now);
     }
     tc_fence_before();
   }
@@ -1078,6 +1175,7 @@ int launch_prompt(const LaunchCommon& lc, void* stream, int32_t layer, const gk_
   int e = encode_packed(&pp.tq, b->d_q, D, pp.Hq, pl->tokens, pp.q_stride, G, pp.tpt);
   if (!e) e = encode_packed(&pp.tk, b->d_k, D, pp.Hkv, pl->tokens, pp.k_stride, 1, kPrefixTileN);
   if (!e) e = encode_packed(&pp.tv, b->d_v, D, pp.Hkv, pl->tokens, pp.v_stride, 1, kPrefixTileN);
+  if (!e) e = encode_packed(&pp.tout, b->d_out, D, pp.Hq, pl->tokens, pp.out_stride, G, pp.tpt);
   if (e) return (int)cudaErrorInvalidValue;
   std::memcpy(&pp.thk, pl->hot_maps, sizeof(CUtensorMap));
   std::memcpy(&pp.thv, pl->hot_maps + sizeof(CUtensorMap), sizeof(CUtensorMap));
