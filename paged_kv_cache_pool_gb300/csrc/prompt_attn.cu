@@ -31,21 +31,25 @@
 // CTAs are persistent (one per SM: 512 tensor-memory columns and 224 KB of
 // shared memory) and run the lists of items that the plan balanced.  K and V tiles
 // share one ring of stages, and the loads of the next item start while the
-// softmax of the last one ends.  The ring's element after an item's last V tile
-// stages its output, so that rows go out in whole 128-byte lines.
+// softmax of the last one ends.  The elements after an item's last V tile, one for each
+// Q tile, stage its output: a warp of its own stores them (whole Q tiles by TMA), so
+// that the softmax warps are at the next item 1300 cycles after the last product.
 //
 // What it measured (GB300, one layer, CUDA graph replays): 16384 tokens on 40/8 heads of
-// 128 in 1700 us, 1.62 PFLOP/s, 83 % of the measured bf16 peak; 8192 tokens on 32/8 heads
-// 343 us.  A key tile of two Q tiles takes 1.54 us, about 3100 cycles, where its four
-// products alone are 2048: what bounds it is the chain S -> softmax -> PV and next S ->
-// softmax through four hand-overs, of which the two Q tiles overlap only part.  An item
-// costs 4.5 us besides (first Q, first reference, output), which is what bounds short
-// prompts: 64 prompts of 256 tokens on 32/8 heads take 94 us.  Tried and slower, in ns
-// a key tile: an issuing warp per Q tile (24 % more), two threads a row (2516, spilling),
-// probabilities stored as they come (1643 -> 1876), handed over in two halves (1542 ->
-// 1674: the issuing warp's waits queue behind its own products), the first reference
-// from registers already loaded (1542 -> 1677, spilling), and at d = 64 P in columns of
-// its own with S issued a tile ahead (6 %).
+// 128 in 1660-1710 us, 1.61-1.65 PFLOP/s, 83-85 % of the measured bf16 peak; 8192 tokens
+// on 32/8 heads 331 us.  A key tile of two Q tiles takes 1.48 us, about 3050 cycles, where
+// its four products alone are 2048: what bounds it is the chain S -> softmax (1400) -> PV
+// and next S (1400) -> softmax with its hand-overs (250), of which the two Q tiles overlap
+// all but the products.  An item costs about 3.5 us besides (first Q and S, first
+// reference, output), which is what bounds short prompts: 64 prompts of 256 tokens on 32/8
+// heads take 84 us.  There a fifth of the stalls wait for instructions: the roles' code is
+// 110 KB, so variants of the softmax share one copy of it.  Tried and slower, in ns a key
+// tile: an issuing warp per Q tile (24 % more), its loop over the Q tiles not unrolled
+// (1526 -> 1683: descriptors leave the uniform registers), two threads a row (2516,
+// spilling), probabilities stored as they come (1643 -> 1876), handed over in two halves
+// (1542 -> 1674: the issuing warp's waits queue behind its own products), the first
+// reference from registers already loaded (1542 -> 1677, spilling), and at d = 64 P in
+// columns of its own with S issued a tile ahead (6 %).
 //
 // Masked keys.  Scores are masked by selection, so whatever K holds in a masked
 // place does no harm; the product P V, though, would turn a masked 0 times an
@@ -57,7 +61,7 @@
 // for finite values).
 //
 // Warp roles (512 threads): 0 TMA, 1 MMA and tensor memory, 2-3 and 13-14 gather
-// and scan, 4-7 and 8-11 softmax of Q tiles 0 and 1, 12 operand relay, 15 idle.  The
+// and scan, 4-7 and 8-11 softmax of Q tiles 0 and 1, 12 operand relay, 15 output.  The
 // block starts with 128 registers a thread; the softmax warpgroups take 152 and the
 // other two keep 104 (spills in the softmax loop were measured to halve the kernel's
 // speed, spills in the other roles to cost 6 %).
@@ -118,32 +122,23 @@ struct Layout {
 };
 
 enum : int {
-  B_QFULL = 0,
-  B_QEMPTY = 1,
-  B_SFULL = 2,                    // one per Q tile, also the next two
-  B_PFULL = 4,
-  B_OFULL = 6,
-  B_FINAL = 8,
-  B_RFULL = 9,                    // 8 each
-  B_REMPTY = 17,
-  B_RSCAN = 25,
-  B_ROUT = 33,
-  B_COUNT = 41
+  B_QFULL = 0,                    // one per Q tile, also the next four
+  B_QEMPTY = 2,
+  B_SFULL = 4,
+  B_PFULL = 6,
+  B_OFULL = 8,
+  B_FINAL = 10,
+  B_RFULL = 11,                   // 8 each
+  B_REMPTY = 19,
+  B_RSCAN = 27,
+  B_ROUT = 35,
+  B_COUNT = 43
 };
 constexpr uint32_t kCtlTmemSlot = B_COUNT * 8;
 constexpr uint32_t kCtlAbort = kCtlTmemSlot + 4;
 constexpr uint32_t kCtlHidden = kCtlAbort + 4;   // an infinity or NaN was hidden in this CTA's V tiles
-// the records of the item whose Q tiles are in shared memory, and of the next: the TMA
-// thread passes them on, since every role's own two dependent reads would stand between
-// one item and the next
-struct Slot {
-  PromptItemDev it;
-  PromptReqDev rq;
-};
-constexpr uint32_t kCtlSlots = 352;
 constexpr uint32_t kCtlBytes = 512;
-static_assert(kCtlHidden + 4 <= kCtlSlots && kCtlSlots + 2 * sizeof(Slot) <= kCtlBytes, "prompt control block");
-constexpr int kSlotReaders = 2;           // MMA and relay warps
+static_assert(kCtlHidden + 4 <= kCtlBytes, "prompt control block");
 // dynamic shared memory starts 1024-byte aligned (checked by the kernel)
 static_assert(Layout<128>::kData + kCtlBytes <= 232448 && Layout<64>::kData + kCtlBytes <= 232448, "shared memory");
 
@@ -156,10 +151,6 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* tmap, int 
           dst),
       "l"(tmap), "r"(x), "r"(y), "r"(bar)
       : "memory");
-}
-__device__ __forceinline__ void tma_prefetch_3d(const void* tmap, int x, int y, int z) {
-  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(tmap), "r"(x), "r"(y), "r"(z)
-               : "memory");
 }
 // a whole tile from shared memory to global memory, in the thread's current bulk group
 __device__ __forceinline__ void tma_store_3d(const void* tmap, int x, int y, int z, uint32_t src) {
@@ -253,17 +244,19 @@ __device__ __forceinline__ bool scanned(const PromptItemDev& it, const PromptReq
 // rows were zeroed in shared memory because other rows of the item must not see
 // them.  p_j v_j is added to O (tensor memory) for the rows that do.
 template <int D>
-__device__ __noinline__ void add_hidden_values(const Params& p, int item, int token, int hr, bool valid, float m, uint32_t tO) {
+__device__ __forceinline__ void add_hidden_values(const Params& p, int item, int token, int hr, bool valid, float m, uint32_t tO) {
   const PromptItemDev it = p.items[item];
   const PromptReqDev rq = p.reqs[it.req];
   const int tk = it.tok0 + token, qh = it.head * p.G + hr;
   const int hi = valid ? tk : -1;
   const int top = __reduce_max_sync(0xffffffffu, hi);
+#pragma unroll 1
   for (int j = it.tok0 + 1; j <= top; ++j) {
     const int tile = j / BN + rq.nt_hot + rq.nt_cold;
     if (tile < it.tile0 || tile >= it.tile0 + it.ntile) continue;
     const uint16_t* vr = p.v + (int64_t)(rq.t0 + j) * p.v_stride + it.head * D;
     bool bad = false;
+#pragma unroll 1
     for (int c = 0; c < D; ++c) bad |= (vr[c] & 0x7F80) == 0x7F80;
     if (!bad) continue;   // warp-uniform: every lane read the same row
     float w = 0.f;
@@ -271,14 +264,17 @@ __device__ __noinline__ void add_hidden_values(const Params& p, int item, int to
       const uint16_t* qr = p.q + (int64_t)(rq.t0 + tk) * p.q_stride + qh * D;
       const uint16_t* kr = p.k + (int64_t)(rq.t0 + j) * p.k_stride + it.head * D;
       float s = 0.f;
+#pragma unroll 1
       for (int c = 0; c < D; ++c) s = fmaf(bf_lo(qr[c]), bf_lo(kr[c]), s);
       w = ex2(s * p.scale_log2 - m);
     }
+#pragma unroll 1
     for (int c0 = 0; c0 < D; c0 += 32) {
       float o[32];
       tmem_ld32(tO + c0, o);
       tc_wait_ld();
       if (j <= hi)
+#pragma unroll
         for (int e = 0; e < 32; ++e) o[e] = fmaf(w, bf_lo(vr[c0 + e]), o[e]);
       __syncwarp();
       tmem_st32(tO + c0, o);
@@ -352,7 +348,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   volatile int* abort_flag = reinterpret_cast<volatile int*>(ctl_ptr + kCtlAbort);
   volatile int* hidden_flag = reinterpret_cast<volatile int*>(ctl_ptr + kCtlHidden);
   auto bar = [&](int i) { return ctl + 8u * (uint32_t)i; };
-  Slot* slots = reinterpret_cast<Slot*>(ctl_ptr + kCtlSlots);
   const uint32_t sQ = base, sR = base + Lay::kRing;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -360,16 +355,17 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   if (threadIdx.x == 0) {
     *abort_flag = 0;
     *hidden_flag = 0;
-    mbar_init(bar(B_QFULL), 1);
-    mbar_init(bar(B_QEMPTY), kSlotReaders);   // the last S is done and everyone has read the slot
     mbar_init(bar(B_FINAL), 1);
     for (int s = 0; s < NST; ++s) {
-      mbar_init(bar(B_REMPTY + s), 8);  // one arrival of the MMAs' end and seven of the relay, or the softmax warps'
+      mbar_init(bar(B_REMPTY + s), 8);  // one arrival of the MMAs' end and seven of the relay; for a staging element,
+                                        // eight of the output warp or two of each softmax warp
       mbar_init(bar(B_RFULL + s), 4);   // the TMA thread arrives four times, or each gather warp once
       mbar_init(bar(B_RSCAN + s), 1);
       mbar_init(bar(B_ROUT + s), 4);    // a Q tile's softmax warps: its output is staged
     }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(B_QFULL + i), 1);
+      mbar_init(bar(B_QEMPTY + i), 1);    // a softmax warp has seen the Q tile's last S
       mbar_init(bar(B_SFULL + i), 1);
       mbar_init(bar(B_PFULL + i), 129);   // the softmax threads and the relay
       mbar_init(bar(B_OFULL + i), 1);
@@ -411,39 +407,39 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       uint32_t scan_ph = 0;                        // bit s: parity of RSCAN[s]'s current phase
       uint32_t in_ring = 0, in_scan = 0, full_ph = 0;  // the last load of each stage, for the drain below
       uint32_t staged = 0;                         // stages that an epilogue wrote to last
-      uint32_t qn = 0;
+      uint32_t qn[2] = {0, 0};
       bool ok = true;
-      Slot next = {};
+      PromptItemDev next_it = {};
+      PromptReqDev next_rq = {};
       if (i0 < i1) {
-        next.it = p.items[i0];
-        next.rq = p.reqs[next.it.req];
+        next_it = p.items[i0];
+        next_rq = p.reqs[next_it.req];
       }
       for (const CUtensorMap* tm : {&p.tq, &p.tk, &p.tv, &p.tout})
         asm volatile("prefetch.tensormap [%0];" ::"l"(tm) : "memory");
       griddep_wait();
       for (int ii = i0; ok && ii < i1; ++ii) {
-        const PromptItemDev it = next.it;
-        const PromptReqDev rq = next.rq;
+        const PromptItemDev it = next_it;
+        const PromptReqDev rq = next_rq;
         if (ii + 1 < i1) {
-          next.it = p.items[ii + 1];
-          next.rq = p.reqs[next.it.req];
+          next_it = p.items[ii + 1];
+          next_rq = p.reqs[next_it.req];
         }
         const int nctx = rq.nt_hot + rq.nt_cold;
         const int n_el = 2 * it.ntile + staging_count(it, rq, p.tpt);
         for (int j = 0; j < n_el; ++j) {
           if (j == 1) {
-            // the Q tiles, once the last product with the item before has read its own
-            if (!wait_or_abort(bar(B_QEMPTY), (qn & 1u) ^ 1u, p.err, abort_flag)) { ok = false; break; }
-            slots[qn & 1u].it = it;
-            slots[qn & 1u].rq = rq;
-            ++qn;
-            const bool two = it.tok0 + p.tpt < rq.n;
-            const uint32_t q_bytes = (uint32_t)(p.tpt * p.G) * 128u * (D / 64);
-            mbar_arrive_expect_tx(bar(B_QFULL), two ? 2 * q_bytes : q_bytes);
-            for (int i = 0; i < (two ? 2 : 1); ++i)
+            // each Q tile, once the last product with the one before has read it
+            for (int i = 0; i < 2; ++i) {
+              if (tile_count(it, rq, p.tpt, i) == 0) continue;
+              if (!wait_or_abort(bar(B_QEMPTY + i), (qn[i] & 1u) ^ 1u, p.err, abort_flag)) { ok = false; break; }
+              ++qn[i];
+              mbar_arrive_expect_tx(bar(B_QFULL + i), (uint32_t)(p.tpt * p.G) * 128u * (D / 64));
               for (int h = 0; h < D / 64; ++h)
                 tma_load_3d(sQ + i * Lay::kQTile + h * kRegionQ, &p.tq, h * 64, it.head * p.G,
-                            rq.t0 + it.tok0 + i * p.tpt, bar(B_QFULL));
+                            rq.t0 + it.tok0 + i * p.tpt, bar(B_QFULL + i));
+            }
+            if (!ok) break;
           }
           const int t = it.tile0 + (j >> 1);
           const bool is_v = j & 1;
@@ -490,12 +486,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             full_ph = (full_ph & ~bit) | (ph << st);
             if (scan) scan_ph ^= bit;
           }
-          if (j == 1 && ii + 1 < i1) {
-            // the next item's Q tiles to L2: they are waited for at each item's start
-            for (int i = 0; i < (next.it.tok0 + p.tpt < next.rq.n ? 2 : 1); ++i)
-              for (int h = 0; h < D / 64; ++h)
-                tma_prefetch_3d(&p.tq, h * 64, next.it.head * p.G, next.rq.t0 + next.it.tok0 + i * p.tpt);
-          }
         }
       }
       if (!ok) {
@@ -504,7 +494,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           if (in_ring >> s & 1u) mbar_wait(bar(B_RFULL + s), full_ph >> s & 1u, nullptr);
           if (in_scan >> s & 1u) mbar_wait(bar(B_RSCAN + s), (scan_ph >> s & 1u) ^ 1u, nullptr);
         }
-        if (qn) mbar_wait(bar(B_QFULL), (qn - 1) & 1u, nullptr);
+        for (int i = 0; i < 2; ++i)
+          if (qn[i]) mbar_wait(bar(B_QFULL + i), (qn[i] - 1) & 1u, nullptr);
       }
     }
   } else if (warp == 1) {
@@ -532,25 +523,26 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         tc_mma_ts(tO(i), tS(i) + kk * 8, b0 + ((kk * 2048) >> 4), kIdPV, (!first || kk > 0) ? 1u : 0u);
     };
     Ring<NST> k;                   // the next element: K0 V0 K1 V1 ...
-    uint32_t qn = 0, pn[2] = {0, 0};
+    uint32_t qn[2] = {0, 0}, pn[2] = {0, 0};
     bool ok = true;
     const int u0 = uniform(i0), u1 = uniform(i1);
     for (int ii = u0; ok && ii < u1; ++ii) {
-      if (!wait(B_QFULL, qn & 1u)) { ok = false; break; }
-      const PromptItemDev it = slots[qn & 1u].it;
-      const PromptReqDev rq = slots[qn & 1u].rq;
+      const PromptItemDev it = p.items[ii];
+      const PromptReqDev rq = p.reqs[it.req];
       const int ntile = uniform(it.ntile);
       const int cnt[2] = {uniform(tile_count(it, rq, p.tpt, 0)), uniform(tile_count(it, rq, p.tpt, 1))};
       if (!wait(B_RFULL + k.st, k.ph)) { ok = false; break; }
-      ++qn;
-      tc_fence_after();
-      if (elect_one()) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          if (cnt[i] > 0) issue_s(i, k.st);
-        tc_commit(bar(B_REMPTY + k.st));
-        if (ntile == 1) tc_commit(bar(B_QEMPTY));
+      for (int i = 0; i < 2; ++i) {
+        if (cnt[i] == 0) continue;
+        if (!wait(B_QFULL + i, qn[i] & 1u)) { ok = false; break; }
+        ++qn[i];
+        tc_fence_after();
+        if (elect_one()) issue_s(i, k.st);
+        __syncwarp();
       }
+      if (!ok) break;
+      if (elect_one()) tc_commit(bar(B_REMPTY + k.st));
       __syncwarp();
       for (int j = 0; ok && j < ntile; ++j) {
         Ring<NST> v = k;
@@ -577,7 +569,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         if (elect_one()) {
           tc_commit(bar(B_REMPTY + v.st));
           if (!last) tc_commit(bar(B_REMPTY + k.st));
-          if (j + 2 == ntile) tc_commit(bar(B_QEMPTY));
         }
         __syncwarp();
       }
@@ -708,11 +699,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         return true;
       };
       for (int ii = i0; ok && ii < i1; ++ii) {
-        const uint32_t qn = (uint32_t)(ii - i0) & 1u;
-        if (!wait_or_abort(bar(B_QFULL), qn, p.err, abort_flag)) break;
-        const PromptItemDev it = slots[qn].it;
-        const PromptReqDev rq = slots[qn].rq;
-        mbar_arrive(bar(B_QEMPTY));
+        const PromptItemDev it = p.items[ii];
+        const PromptReqDev rq = p.reqs[it.req];
         const int cnt[2] = {tile_count(it, rq, p.tpt, 0), tile_count(it, rq, p.tpt, 1)};
         ok = full();                   // K_0: the MMA warp waits for it too
         for (int j = 0; ok && j < it.ntile; ++j) {
@@ -732,8 +720,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   } else {
     // ------------------------------- output rows --------------------------------
     // Staged bf16 rows to global memory while the softmax warps are at the next item (they
-    // took 2300 cycles an item to write them themselves): whole Q tiles by TMA, the last
-    // rows of a request, whose tile holds another's behind them, 512 bytes an instruction.
+    // took 2300 cycles an item to write them themselves): whole Q tiles by TMA (1400 cycles a
+    // tile, 3000 by this warp's own stores), the last rows of a request, whose tile holds
+    // another's behind them, 512 bytes an instruction.
     constexpr int kChunks = D / 8, kRows = 32 / kChunks;
     const int ch = lane % kChunks, sub = lane / kChunks;
     const uint32_t inv_g = 65536u / (uint32_t)p.G + 1u;   // r * inv_g >> 16 = r / G for r < 128
@@ -857,6 +846,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         if (!wait(B_SFULL + qi, sn & 1u)) { ok = false; break; }
         ++sn;
         tc_fence_after();
+        if (j + 1 == cnt && (warp & 3) == 0 && lane == 0) mbar_arrive(bar(B_QEMPTY + qi));   // Q was read for the last time
         if (j == j_hot || j == j_cold || j >= j_new) {
           // minus infinity over the hidden scores, in tensor memory: one copy of the code below then
           // serves every tile (with two, the second one's instructions were fetched anew each item)

@@ -58,7 +58,7 @@ class Model:
             scan = [k == "n" or k == "h" and r.random() < 0.3 for k in kinds]
             self.items.append((kinds, n, cnt, scan, r.random() < 0.3))     # the last: a partial state
         self.bars = {}
-        for name, count in [("QFULL", 1), ("QEMPTY", 2), *(("S%d" % i, 1) for i in (0, 1)), *(("P%d" % i, 5) for i in (0, 1)),
+        for name, count in [*(("%s%d" % (k, i), 1) for i in (0, 1) for k in ("QFULL", "QEMPTY", "S")), *(("P%d" % i, 5) for i in (0, 1)),
                             *(("O%d" % i, 1) for i in (0, 1)),
                             *(("%s%d" % (k, s), c) for s in range(stages) for k, c in (("F", 4), ("E", 8), ("C", 1), ("W", 4)))]:
             self.bars[name] = Bar(count, name)
@@ -66,7 +66,7 @@ class Model:
         self.score, self.prob, self.pv = [None, None], [None, None], [None, None]
         self.read = [set(), set()]
         self.mma, self.tma = [], []
-        self.slots = [None, None]
+        self.q = [None, None]
 
     def arrive(self, name, k=1):
         self.bars[name].arrive(k)
@@ -79,14 +79,19 @@ class Model:
         return (cnt[0] > 0) + (cnt[1] > 0)
 
     def producer(self):
-        ring, qn = Ring(self.N), 0
+        ring, qn = Ring(self.N), [0, 0]
         for n, (kinds, nt, cnt, scan, part) in enumerate(self.items):
             for j in range(2 * nt + self.staging(cnt)):
                 if j == 1:
-                    yield from self.wait("QEMPTY", (qn & 1) ^ 1)
-                    self.slots[qn & 1] = n
-                    qn += 1
-                    self.tma.append(lambda: self.arrive("QFULL"))
+                    for i in (0, 1):
+                        if cnt[i] > 0:
+                            yield from self.wait("QEMPTY%d" % i, (qn[i] & 1) ^ 1)
+                            qn[i] += 1
+
+                            def loaded(i=i, n=n):
+                                self.q[i] = n
+                                self.arrive("QFULL%d" % i)
+                            self.tma.append(loaded)
                 st, ph = ring.st, ring.ph
                 ring.next()
                 yield from self.wait("E%d" % st, ph ^ 1)
@@ -138,6 +143,7 @@ class Model:
     def issue_s(self, i, st, n, j):
         def run():
             assert self.stage[st] == (n, 2 * j), ("S reads", self.stage[st], (n, 2 * j))
+            assert self.q[i] == n, ("S reads the Q tile of", self.q[i], n)
             if self.score[i] is not None:
                 assert all((*self.score[i], w) in self.read[i] for w in range(4)), ("S overwritten", self.score[i])
             self.score[i] = (n, j)
@@ -151,19 +157,15 @@ class Model:
         self.mma.append(run)
 
     def issuer(self):
-        k, qn, pn = Ring(self.N), 0, [0, 0]
-        for _ in self.items:
-            yield from self.wait("QFULL", qn & 1)
-            n = self.slots[qn & 1]
-            kinds, nt, cnt, scan, part = self.items[n]
+        k, qn, pn = Ring(self.N), [0, 0], [0, 0]
+        for n, (kinds, nt, cnt, scan, part) in enumerate(self.items):
             yield from self.wait("F%d" % k.st, k.ph)
-            qn += 1
             for i in (0, 1):
                 if cnt[i] > 0:
+                    yield from self.wait("QFULL%d" % i, qn[i] & 1)
+                    qn[i] += 1
                     self.issue_s(i, k.st, n, 0)
             self.mma.append(lambda st=k.st: self.arrive("E%d" % st))
-            if nt == 1:
-                self.mma.append(lambda: self.arrive("QEMPTY"))
             for j in range(nt):
                 v, k = k.ahead(1), k.ahead(2)
                 for i in (0, 1):
@@ -180,8 +182,6 @@ class Model:
                 self.mma.append(lambda st=v.st: self.arrive("E%d" % st))
                 if j + 1 < nt:
                     self.mma.append(lambda st=k.st: self.arrive("E%d" % st))
-                if j + 2 == nt:
-                    self.mma.append(lambda: self.arrive("QEMPTY"))
             k.next(self.staging(cnt))
 
     def relay(self):
@@ -192,12 +192,7 @@ class Model:
             assert self.stage[ring.st] == el
             self.arrive("E%d" % ring.st, 7)
             ring.next()
-        for q in range(len(self.items)):
-            yield from self.wait("QFULL", q & 1)
-            n = self.slots[q & 1]
-            assert n == q, "slot of another item"
-            kinds, nt, cnt, scan, part = self.items[n]
-            self.arrive("QEMPTY")
+        for n, (kinds, nt, cnt, scan, part) in enumerate(self.items):
             yield from full((n, 0))
             for j in range(nt):
                 yield from full((n, 2 * j + 1))
@@ -213,15 +208,15 @@ class Model:
 
     def softmax(self, i, w):
         ring, sn, on = Ring(self.N), 0, 0
-        for q in range(len(self.items)):
-            n = q
-            kinds, nt, cnt, scan, part = self.items[n]
+        for n, (kinds, nt, cnt, scan, part) in enumerate(self.items):
             yield None
             mine = int(i == 1 and cnt[0] > 0)
             ring.next(2 * nt + mine)
             for j in range(cnt[i]):
                 yield from self.wait("S%d" % i, sn & 1)
                 sn += 1
+                if j + 1 == cnt[i] and w == 0:
+                    self.arrive("QEMPTY%d" % i)
                 assert self.score[i] == (n, j), ("softmax reads S", self.score[i], (n, j))
                 yield None
                 assert self.score[i] == (n, j)
