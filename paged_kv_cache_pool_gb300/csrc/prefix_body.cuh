@@ -535,13 +535,6 @@ __device__ __forceinline__ bool prefix_item(const PrefixParams& p, const PrefixI
 
 }  // namespace prefix
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// the driver's tensor-map encoder; null when the driver has none
-EncodeTiledFn encode_fn();
-
 // kernel arguments of the prefix contraction for one layer of a planned batch
 int fill_prefix_params(const LaunchCommon& lc, int32_t layer, const gk_batch* b, const Plan* pl,
                        prefix::PrefixParams* out);

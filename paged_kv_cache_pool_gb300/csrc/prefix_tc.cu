@@ -53,17 +53,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const PrefixParams 
   }
 }
 
-template <int D>
-int launch_prefix_t(const PrefixParams& pp, int n_items, int ctas, cudaStream_t st) {
-  auto kern = prefix_kernel<D>;
-  const size_t smem = kernel_smem<D>();
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return (int)e;
-  e = launch_pdl(kern, dim3(ctas), dim3(kThreads), smem, st, pp, n_items);
-  return (int)e;
-}
-
-}  // namespace
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 EncodeTiledFn encode_fn() {
   static EncodeTiledFn fn = nullptr;
@@ -77,6 +69,18 @@ EncodeTiledFn encode_fn() {
   }
   return fn;
 }
+
+template <int D>
+int launch_prefix_t(const PrefixParams& pp, int n_items, int ctas, cudaStream_t st) {
+  auto kern = prefix_kernel<D>;
+  const size_t smem = kernel_smem<D>();
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return (int)e;
+  e = launch_pdl(kern, dim3(ctas), dim3(kThreads), smem, st, pp, n_items);
+  return (int)e;
+}
+
+}  // namespace
 
 size_t tmap_bytes() { return sizeof(CUtensorMap); }
 

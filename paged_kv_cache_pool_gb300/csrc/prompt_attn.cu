@@ -1105,9 +1105,28 @@ int launch_t(const Params& pp, const PromptPlan* pl, const uint8_t* base, cudaSt
 }  // namespace
 }  // namespace prompt
 
+namespace {
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// the driver's tensor-map encoder; null when the driver has none
+EncodeTiledFn encode_fn() {
+  static EncodeTiledFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    return cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+                   q == cudaDriverEntryPointSuccess
+               ? (EncodeTiledFn)p
+               : nullptr;
+  }();
+  return fn;
+}
+
 // 3D map over a packed tensor [tokens][heads][d] with a token stride, 128-byte
 // swizzle; tokens past the end read as zeros
-static int encode_packed(CUtensorMap* tm, const void* ptr, int d, int heads, int64_t tokens, int64_t stride,
+int encode_packed(CUtensorMap* tm, const void* ptr, int d, int heads, int64_t tokens, int64_t stride,
                          int box_heads, int box_tokens) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return 1;
@@ -1123,7 +1142,7 @@ static int encode_packed(CUtensorMap* tm, const void* ptr, int d, int heads, int
 }
 
 // 2D map over a whole HOT pool as rows of d elements
-static int encode_hot(CUtensorMap* tm, const void* ptr, int d, int64_t rows) {
+int encode_hot(CUtensorMap* tm, const void* ptr, int d, int64_t rows) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return 1;
   cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)rows};
@@ -1136,6 +1155,8 @@ static int encode_hot(CUtensorMap* tm, const void* ptr, int d, int64_t rows) {
              ? 0
              : 2;
 }
+
+}  // namespace
 
 int encode_hot_maps(const gk_pool_config* cfg, uint8_t* out) {
   const int64_t rows = cfg->hot_tokens * cfg->num_layers * cfg->num_kv_heads;
