@@ -206,7 +206,8 @@ typedef struct gk_tables {
  * the stack outside the pool gives slots of -1; a count outside [0, capacity], or
  * releases past it, counts as an empty stack or releases nothing: each is reported
  * as GK_ERR_DEVICE_BOUNDS by gk_device_error().  Nothing happens when R = 0.  Calls
- * that share any of the arrays must be ordered. */
+ * that share any of the arrays must be ordered.  The pool's device must be the
+ * current one (else GK_ERR_INVALID). */
 gk_status gk_tables_step(gk_pool* pool, void* stream, const gk_tables* t, const int32_t* d_release,
                          const int32_t* d_add, int64_t n_slots, int64_t* d_slot_mapping, int32_t* d_done);
 
@@ -422,7 +423,8 @@ typedef struct gk_prompt_plan_summary {
  * prefix that is not live with that length, a context longer than its
  * block-table row, or more than 2^31 - 1 tokens.  Allocates device memory and
  * uploads from a buffer that the next plan rewrites: on a stream that is capturing
- * it does nothing and returns GK_ERR_UNSUPPORTED. */
+ * it does nothing and returns GK_ERR_UNSUPPORTED.  The pool's device must be the
+ * current one, here and in gk_prompt_attn (else GK_ERR_INVALID). */
 gk_status gk_prompt_plan_build(gk_pool* pool, const gk_prompt_batch* batch, void* stream, gk_prompt_plan** out);
 /* Re-plan for the next step, reusing the buffers; on the stream of the plan's earlier
  * work.  A graph captured with the plan holds the launch of the step planned then:

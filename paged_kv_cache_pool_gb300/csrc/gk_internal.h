@@ -229,6 +229,8 @@ int launch_scatter(const LaunchCommon& lc, void* stream, int32_t layer, int32_t 
 int launch_write_prefix(const LaunchCommon& lc, void* stream, int32_t layer, int64_t base,
                         int64_t lp, int64_t t0, int64_t n, const void* d_k, const void* d_v);
 
+// GK_ERR_INVALID unless the pool's device is the current one (after ensure_device)
+gk_status device_is_current(Pool* p);
 int launch_tables_step(const LaunchCommon& lc, void* stream, const gk_tables* t, const int32_t* d_release,
                        const int32_t* d_add, int64_t n_slots, int64_t* d_slots, int32_t* d_done);
 

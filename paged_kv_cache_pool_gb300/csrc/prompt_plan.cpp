@@ -406,6 +406,7 @@ gk_status plan_for(Pool* p, PromptPlan* pl, const gk_prompt_batch* b, void* stre
   pl->uploaded = false;
   if (p->has_device) {
     gk_status st = ensure_device(p);
+    if (st == GK_OK) st = device_is_current(p);
     if (st != GK_OK) return st;
   }
   gk_status st = GK_ERR_INVALID;
@@ -427,6 +428,14 @@ void free_buffers(PromptPlan* pl) {
 }
 
 }  // namespace
+
+gk_status device_is_current(Pool* p) {
+  int dev = -1;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(p, e, "cudaGetDevice");
+  return dev == p->dev.device ? GK_OK : fail(p, GK_ERR_INVALID, "the pool's device is not the current device");
+}
+
 }  // namespace gk
 
 extern "C" {
@@ -514,6 +523,7 @@ gk_status gk_prompt_attn(gk_pool* pool, void* stream, int32_t layer, const gk_pr
   if (!pl->uploaded) return gk::fail(p, GK_ERR_INVALID, "plan has no device tables");
   if (!rows) return GK_OK;
   gk_status st = gk::ensure_device(p);
+  if (st == GK_OK) st = gk::device_is_current(p);
   if (st != GK_OK) return st;
   gk::LaunchCommon lc{&p->cfg, p->d_error, p->dev.num_sms};
   int e = gk::launch_prompt(lc, stream, layer, b, pl);

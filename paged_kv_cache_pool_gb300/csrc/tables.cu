@@ -440,6 +440,7 @@ extern "C" gk_status gk_tables_step(gk_pool* pool, void* stream, const gk_tables
     if ((uintptr_t)t->d_work % 16 != 0) return gk::fail(p, GK_ERR_INVALID, "d_work must be 16-byte aligned");
   }
   gk_status st = gk::ensure_device(p);
+  if (st == GK_OK) st = gk::device_is_current(p);
   if (st != GK_OK) return st;
   if (t->num_rows == 0) return GK_OK;
   gk::LaunchCommon lc{&p->cfg, p->d_error, p->dev.num_sms};
