@@ -167,10 +167,9 @@ __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src
   const uint32_t n = valid ? 16u : 0u;
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait_group() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+// one arrival of this thread at the barrier once its copies so far have landed
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 // Bounded wait; the clock and the CTA's abort flag are looked at every 256 tries only,
@@ -359,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     for (int s = 0; s < NST; ++s) {
       mbar_init(bar(B_REMPTY + s), 8);  // one arrival of the MMAs' end and seven of the relay; for a staging element,
                                         // eight of the output warp or two of each softmax warp
-      mbar_init(bar(B_RFULL + s), 4);   // the TMA thread arrives four times, or each gather warp once
+      mbar_init(bar(B_RFULL + s), 128); // the TMA thread arrives 128 times, or each gather thread once
       mbar_init(bar(B_RSCAN + s), 1);
       mbar_init(bar(B_ROUT + s), 4);    // a Q tile's softmax warps: its output is staged
     }
@@ -454,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             in_ring &= ~(1u << st);
             in_scan &= ~(1u << st);
             if (it.entry >= 0) staged |= 1u << st;   // written and read by the softmax warps only
-            mbar_arrive_n(bar(B_RFULL + st), 4);
+            mbar_arrive_n(bar(B_RFULL + st), 128);
           } else if (t >= rq.nt_hot && t < nctx) { // COLD: to the gather warps
             in_ring &= ~(1u << st);
             in_scan &= ~(1u << st);
@@ -470,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
               fence_async_shared();
               staged &= ~(1u << st);
             }
-            if (!scan) mbar_arrive_n(b, 3);
+            if (!scan) mbar_arrive_n(b, 127);
             mbar_arrive_expect_tx(b, Lay::kTile);
             if (t < rq.nt_hot) {
               const int row = (int)(rq.hot_row + ((int64_t)p.layer * p.Hkv + it.head) * rq.lp + t * BN);
@@ -532,6 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       const int ntile = uniform(it.ntile);
       const int cnt[2] = {uniform(tile_count(it, rq, p.tpt, 0)), uniform(tile_count(it, rq, p.tpt, 1))};
       if (!wait(B_RFULL + k.st, k.ph)) { ok = false; break; }
+      fence_async_shared();        // K_0 may have been gathered
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         if (cnt[i] == 0) continue;
@@ -586,20 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     griddep_wait();
     Ring<NST> ring;
     uint32_t scan_ph = 0;
-    int pending = -1;                            // stage this warp copied to but has not announced
     bool ok = true;
-    auto announce = [&](int st) {                // this warp's rows of stage st are written
-      fence_async_shared();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(B_RFULL + st));
-    };
-    auto flush = [&]() {
-      if (pending >= 0) {
-        cp_async_wait_group<0>();
-        announce(pending);
-        pending = -1;
-      }
-    };
     for (int ii = i0; ok && ii < i1; ++ii) {
       const PromptItemDev it = p.items[ii];
       const PromptReqDev rq = p.reqs[it.req];
@@ -619,7 +606,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         const int st = ring.st;
         ring.next();
         const bool cold = t >= rq.nt_hot && t < nctx;
-        if (!cold) flush();    // before anything that could wait for the copied tile to be used
         if (!cold && !(is_v && scanned(it, rq, t))) continue;
         // the stage is free (COLD), or TMA has filled it
         if (!wait(B_RSCAN + st, scan_ph >> st & 1u)) { ok = false; break; }
@@ -642,12 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             cp_async16_or_zero(dst0 + row * 128 + (((ch & 7) ^ (row & 7)) << 4),
                                src0 + (int64_t)max(s, 0) * p.Hkv * D, s >= 0);
           }
-          cp_async_commit();
-          if (pending >= 0) {
-            cp_async_wait_group<1>();
-            announce(pending);
-          }
-          pending = st;
+          cp_async_arrive(bar(B_RFULL + st));
         } else {
           const bool hot = t < rq.nt_hot;
           const int key0 = (hot ? t : t - nctx) * BN;
@@ -674,15 +655,15 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             for (int c = 0; c < kChunks; ++c)
               sts128(src + (c >> 3) * kRegionKV + (((c & 7) ^ (row & 7)) << 4), make_uint4(0, 0, 0, 0));
           }
-          announce(st);
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_n(bar(B_RFULL + st), 32);
         }
       }
       if (!ok) break;
-      flush();
       ring.skip(staging_count(it, rq, p.tpt));
     }
-    if (ok) flush();
-    else cp_async_wait_all();
+    cp_async_wait_all();
   } else if (warp == 12) {
     // ------------------------------ operand relay -------------------------------
     // Waits for V_j and K_(j+1) and arrives for them on the barriers of P(j): the MMA
@@ -692,8 +673,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       Ring<NST> ring;
       uint32_t pn[2] = {0, 0};
       bool ok = true;
-      auto full = [&]() {
+      auto full = [&](bool cold) {
         if (!wait_or_abort(bar(B_RFULL + ring.st), ring.ph, p.err, abort_flag)) return false;
+        if (cold) fence_async_shared();            // the gathered rows before the products' reads
         mbar_arrive_n(bar(B_REMPTY + ring.st), 7);
         ring.next();
         return true;
@@ -702,9 +684,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         const PromptItemDev it = p.items[ii];
         const PromptReqDev rq = p.reqs[it.req];
         const int cnt[2] = {tile_count(it, rq, p.tpt, 0), tile_count(it, rq, p.tpt, 1)};
-        ok = full();                   // K_0: the MMA warp waits for it too
+        auto cold = [&](int j) { return it.tile0 + j >= rq.nt_hot && it.tile0 + j < rq.nt_hot + rq.nt_cold; };
+        ok = full(cold(0));            // K_0: the MMA warp waits for it too
         for (int j = 0; ok && j < it.ntile; ++j) {
-          ok = full() && (j + 1 == it.ntile || full());
+          ok = full(cold(j)) && (j + 1 == it.ntile || full(cold(j + 1)));
 #pragma unroll
           for (int i = 0; i < 2; ++i)
             if (ok && j < cnt[i]) {

@@ -112,32 +112,26 @@ class Model:
                 yield None
 
     def gather(self):
-        ring, ph, pending = Ring(self.N), [0] * self.N, None
+        ring, ph = Ring(self.N), [0] * self.N
         for n, (kinds, nt, cnt, scan, part) in enumerate(self.items):
             for j in range(2 * nt):
                 st = ring.st
                 ring.next()
                 cold = kinds[j // 2] == "c"
-                if not cold and pending is not None:
-                    self.arrive("F%d" % pending)
-                    pending = None
                 if not cold and not (j & 1 and scan[j // 2]):
                     continue
                 yield from self.wait("C%d" % st, ph[st])
                 ph[st] ^= 1
                 if cold:
-                    self.stage[st] = (n, j)
-                    if pending is not None:
-                        yield None
-                        self.arrive("F%d" % pending)
-                    pending = st
+
+                    def landed(st=st, n=n, j=j):
+                        self.stage[st] = (n, j)
+                        self.arrive("F%d" % st)
+                    self.tma.append(landed)
                 else:
                     assert self.stage[st] == (n, j)
                     self.arrive("F%d" % st)
                 yield None
-            if pending is not None:
-                self.arrive("F%d" % pending)
-                pending = None
             ring.next(self.staging(cnt))
 
     def issue_s(self, i, st, n, j):
