@@ -163,7 +163,7 @@ __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.comm
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 // 16-byte copy, or 16 zero bytes when !valid (the source is then not read)
-__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool valid) {
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, uint64_t src, bool valid) {
   const uint32_t n = valid ? 16u : 0u;
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
@@ -583,6 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     constexpr int kRowsPerCopy = 32 / kChunks;   // rows per warp instruction
     const int row0 = (warp < 4 ? warp - 2 : warp - 11) * 32;   // this warp's rows of a tile
     const int ch = lane % kChunks, sub = lane / kChunks;
+    const uint32_t slot_bytes = (uint32_t)(p.Hkv * D) * 2u;
     griddep_wait();
     Ring<NST> ring;
     uint32_t scan_ph = 0;
@@ -619,14 +620,24 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             if (in && slot < 0) report_error(p.err, kErrBounds);
             fetch_ids(t + 1);
           }
-          const uint16_t* src0 = (is_v ? p.cold_v : p.cold_k) + ((int64_t)p.layer * p.cold_slots * p.Hkv + it.head) * D + ch * 8;
-          const uint32_t dst0 = tile + (uint32_t)(ch >> 3) * kRegionKV;
-#pragma unroll 8
-          for (int r = 0; r < 32; r += kRowsPerCopy) {
-            const int row = row0 + r + sub;
-            const int s = __shfl_sync(0xffffffffu, slot, r + sub);
-            cp_async16_or_zero(dst0 + row * 128 + (((ch & 7) ^ (row & 7)) << 4),
-                               src0 + (int64_t)max(s, 0) * p.Hkv * D, s >= 0);
+          // four instructions a copy where every row exists: the gather warps share their schedulers
+          // with the softmax warps (a tile of COLD keys took 1837 ns with a dozen, 1603 so)
+          const uint64_t src0 = (uint64_t)((is_v ? p.cold_v : p.cold_k) +
+                                           ((int64_t)p.layer * p.cold_slots * p.Hkv + it.head) * D + ch * 8);
+          const uint32_t dst0 = tile + (uint32_t)(ch >> 3) * kRegionKV + (uint32_t)(row0 + sub) * 128;
+          const bool all = __all_sync(0xffffffffu, slot >= 0);
+          if (all) {
+#pragma unroll
+            for (int r = 0; r < 32; r += kRowsPerCopy)     // row0 is a multiple of 8
+              cp_async16(dst0 + r * 128 + (((ch ^ (r + sub)) & 7) << 4),
+                         (const void*)(src0 + (uint64_t)(uint32_t)__shfl_sync(0xffffffffu, slot, r + sub) * slot_bytes));
+          } else {
+#pragma unroll 1
+            for (int r = 0; r < 32; r += kRowsPerCopy) {
+              const int s = __shfl_sync(0xffffffffu, slot, r + sub);
+              cp_async16_or_zero(dst0 + r * 128 + (((ch ^ (r + sub)) & 7) << 4),
+                                 src0 + (uint64_t)(uint32_t)max(s, 0) * slot_bytes, s >= 0);
+            }
           }
           cp_async_arrive(bar(B_RFULL + st));
         } else {
