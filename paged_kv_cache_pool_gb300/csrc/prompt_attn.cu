@@ -12,7 +12,8 @@
 // floor(128 / g); the g query heads of a token are g consecutive rows, so an item
 // is two 128-row Q tiles) x a range of 128-key tiles.  Keys come in tiles of one
 // source each: HOT tiles (2D tensor map over the whole HOT pool), COLD tiles
-// (rows gathered through the block table by four warps with 16-byte cp.async),
+// (rows gathered through the block table by four warps with 16-byte cp.async, whose
+// completion arrives at the tile's barrier),
 // then tiles of new tokens (3D tensor maps over the caller's packed tensors).
 // S_i = Q_i K^T and O_i += P_i V accumulate in tensor memory (512 columns: S_0
 // S_1 O_0 O_1; P_i overwrites S_i as bf16).  Softmax warpgroup i owns Q tile i, one
@@ -42,7 +43,9 @@
 // and next S (1400) -> softmax with its hand-overs (250), of which the two Q tiles overlap
 // all but the products.  An item costs about 3.5 us besides (first Q and S, first
 // reference, output), which is what bounds short prompts: 64 prompts of 256 tokens on 32/8
-// heads take 84 us.  There a fifth of the stalls wait for instructions: the roles' code is
+// heads take 82 us.  COLD tiles cost 1.60 us: their copies share the schedulers with the
+// softmax (two chunks of 2048 tokens over 6000-12000 in pages of 16: 465 us, 1.40 PFLOP/s).
+// In short prompts a fifth of the stalls wait for instructions: the roles' code is
 // 110 KB, so variants of the softmax share one copy of it.  Tried and slower, in ns a key
 // tile: an issuing warp per Q tile (24 % more), its loop over the Q tiles not unrolled
 // (1526 -> 1683: descriptors leave the uniform registers), two threads a row (2516,
@@ -167,11 +170,6 @@ __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, uint64_t src, b
   const uint32_t n = valid ? 16u : 0u;
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
-// one arrival of this thread at the barrier once its copies so far have landed
-__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
-
 // Bounded wait; the clock and the CTA's abort flag are looked at every 256 tries only,
 // as reading the timer at each try delays what follows the barrier by 100 cycles and more.
 __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, int32_t* err, volatile int* abort_flag) {
@@ -639,7 +637,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                                  src0 + (uint64_t)(uint32_t)max(s, 0) * slot_bytes, s >= 0);
             }
           }
-          cp_async_arrive(bar(B_RFULL + st));
+          cp_async_mbar_arrive(bar(B_RFULL + st));
         } else {
           const bool hot = t < rq.nt_hot;
           const int key0 = (hot ? t : t - nctx) * BN;
