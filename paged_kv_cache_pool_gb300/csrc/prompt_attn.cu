@@ -37,8 +37,8 @@
 // that the softmax warps are at the next item 1300 cycles after the last product.
 //
 // What it measured (GB300, one layer, CUDA graph replays): 16384 tokens on 40/8 heads of
-// 128 in 1660-1710 us, 1.61-1.65 PFLOP/s, 83-85 % of the measured bf16 peak; 8192 tokens
-// on 32/8 heads 331 us.  A key tile of two Q tiles takes 1.48 us, about 3050 cycles, where
+// 128 in 1630-1770 us as the power cap sets the clock, 1.55-1.68 PFLOP/s; 8192 tokens on
+// 32/8 heads 331 us, 1.66 PFLOP/s, 85 % of the measured bf16 peak.  A key tile of two Q tiles takes 1.48 us, about 3050 cycles, where
 // its four products alone are 2048: what bounds it is the chain S -> softmax (1400) -> PV
 // and next S (1400) -> softmax with its hand-overs (250), of which the two Q tiles overlap
 // all but the products.  An item costs about 3.5 us besides (first Q and S, first
