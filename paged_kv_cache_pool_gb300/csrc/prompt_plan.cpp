@@ -218,6 +218,7 @@ gk_status build_host(Pool* p, const gk_prompt_batch* b, PromptPlan* pl) {
   }
   int32_t best = longest;
   double best_t = 1e300;
+  // (with two dozen items per SM whole ranges balance by themselves)
   if (shapes.size() * (size_t)Hkv < 24 * (size_t)num_sms) {
     for (int k = 0; k <= 8; ++k) {
       const int32_t most = k == 0 ? longest : std::max(1, (int32_t)(work / num_sms / kTile2Us / k));
@@ -237,6 +238,7 @@ gk_status build_host(Pool* p, const gk_prompt_batch* b, PromptPlan* pl) {
         best_t = t;
         best = most;
       }
+      if (best_t <= work / num_sms + kJoinLaunchUs) break;   // pieces add a join to at least this much
     }
   }
 
