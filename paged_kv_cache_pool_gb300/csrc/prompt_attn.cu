@@ -1005,9 +1005,17 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   }
 }
 
+// the larger of two numbers; NaN where one of them is (fmaxf drops it)
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+  return m;
+}
+
 // Joins the partial states of rows whose keys several items covered: with l_e the
 // states' LSE (log2), m = max l_e, w_e = 2^(l_e - m): O = sum w_e O_e / sum w_e,
-// LSE = (m + log2 sum w_e) ln 2.  One warp per row, 32 rows per CTA, at most 32
+// LSE = (m + log2 sum w_e) ln 2.  A state whose LSE is NaN makes its row NaN, as
+// it is where one item covers the keys.  One warp per row, 32 rows per CTA, at most 32
 // states per row (lane e holds state e's weight); bound by the read of the states
 // (4 d bytes each), four in flight per warp.
 template <int D>
@@ -1039,7 +1047,7 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const PromptJoinDev* _
     const float le = lane < n ? __ldcg(part_l + entry_row(lane)) : -INFINITY;
     float mx = le;
 #pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+    for (int off = 16; off >= 1; off >>= 1) mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, off));
     float w = mx == -INFINITY ? 0.f : ex2(le - mx);
     if (lane >= n) w = 0.f;
     float z = w;
