@@ -169,21 +169,15 @@ def lib():
 
 def _ptr(x):
     """Device address of a torch tensor, an int, or None."""
-    try:
-        return x.data_ptr()
-    except AttributeError:
-        if x is None or isinstance(x, int):
-            return x
-        raise
+    if x is None or isinstance(x, int):    # first: a failed attribute look-up costs 0.4 us a call
+        return x
+    return x.data_ptr()
 
 
 def _stream(s):
-    try:
-        return s.cuda_stream
-    except AttributeError:
-        if s is None or isinstance(s, int):
-            return s
-        raise
+    if s is None or isinstance(s, int):
+        return s
+    return s.cuda_stream
 
 
 def _check(st, pool=None):
