@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sys
 
 import numpy as np
 
@@ -196,6 +197,10 @@ def _i32p(a):
     return a.ctypes.data_as(P(c_i32))
 
 
+# what the checks of tensors need to know: heads and channels by pool, tokens by prompt plan
+_geometry, _prompt_tokens = {}, {}
+
+
 # ---- pool ----------------------------------------------------------------------
 def gk_pool_create(num_layers, num_q_heads, num_kv_heads, head_dim, hot_tokens, cold_slots, cold_page_size,
                    seed=0, hot_k=None, hot_v=None, cold_k=None, cold_v=None):
@@ -203,10 +208,12 @@ def gk_pool_create(num_layers, num_q_heads, num_kv_heads, head_dim, hot_tokens, 
                          seed, _ptr(hot_k), _ptr(hot_v), _ptr(cold_k), _ptr(cold_v))
     out = c_vp()
     _check(lib().gk_pool_create(ctypes.byref(cfg), ctypes.byref(out)))
+    _geometry[out.value] = (num_q_heads, num_kv_heads, head_dim)
     return out.value
 
 
 def gk_pool_destroy(pool):
+    _geometry.pop(pool, None)
     lib().gk_pool_destroy(pool)
 
 
@@ -476,15 +483,18 @@ def gk_cascade_merge(pool, stream, layer, batch, plan):
 
 
 # ---- prompt step ---------------------------------------------------------------------
-def _token_stride(x, tokens, what):
-    """Elements from one token of x (bf16 [tokens, heads, d]) to the next; 0 (packed) for an address or one token."""
+def _token_rows(x, tokens, what, torch):
+    """heads, d, elements from one token to the next (0: packed) and address of x, a bf16 CUDA tensor [tokens, heads, d];
+    no heads and no d for the address of packed rows."""
     if x is None or isinstance(x, int):
-        return 0
+        return None, None, 0, x
     n, heads, d = x.shape
     row, head, channel = x.stride()
-    if n != tokens or x.element_size() != 2 or (n and (channel != 1 or (heads > 1 and head != d))):
-        raise ValueError(f"{what} must be bf16 [{tokens}, heads, d] with a token's heads and channels contiguous")
-    return row if n > 1 else 0
+    if n != tokens or x.dtype is not torch.bfloat16 or not x.is_cuda or n and (channel != 1 or heads > 1 and head != d):
+        raise ValueError(f"{what} must be bf16 [{tokens}, heads, d] on the GPU, with a token's heads and channels contiguous")
+    if n > 1 and row < heads * d:
+        raise ValueError(f"{what}'s tokens overlap: a row of a token's own is read for each of {n}, which expand() does not give")
+    return heads, d, row if n > 1 else 0, x.data_ptr()
 
 
 class PromptBatch:
@@ -509,36 +519,68 @@ class PromptBatch:
                                  None if self.prefix_hot_base is None else _i64p(self.prefix_hot_base),
                                  None if self.prefix_len is None else _i32p(self.prefix_len),
                                  None if self.context_len is None else _i32p(self.context_len))
+        self._check_table(d_block_table, max_blocks)
         self._table = d_block_table
         self.c.d_block_table = _ptr(d_block_table)
+        self.heads = None, None, None          # query heads, KV heads and channels of the tensors set last
         self.ref = ctypes.byref(self.c)
 
     def set_device(self, d_q, d_k, d_v, d_out, d_lse=None, d_block_table=None, max_blocks=None):
-        """bf16 [T, Hq, d] q and out, [T, Hkv, d] k and v, fp32 [T, Hq] lse: torch tensors
-        (tokens may be strided, as views of a fused projection are) or addresses of packed rows."""
-        c, T = self.c, self.tokens
-        c.q_stride, c.out_stride = _token_stride(d_q, T, "q"), _token_stride(d_out, T, "out")
-        c.k_stride, c.v_stride = _token_stride(d_k, T, "k"), _token_stride(d_v, T, "v")
-        c.d_q, c.d_k, c.d_v, c.d_out, c.d_lse = _ptr(d_q), _ptr(d_k), _ptr(d_v), _ptr(d_out), _ptr(d_lse)
-        if d_block_table is not None:
-            c.d_block_table = _ptr(d_block_table)
-            self._table = d_block_table
-        if max_blocks is not None:
-            c.max_blocks = max_blocks
+        """bf16 [T, Hq, d] q and out, [T, Hkv, d] k and v, fp32 [T, Hq] lse, int32 [B, max_blocks] table: torch tensors
+        (tokens may be strided, as views of a fused projection are; lse and table are contiguous) or addresses of packed
+        rows.  ValueError, with the batch as it was, for tensors of another type or shape."""
+        c, T, torch = self.c, self.tokens, sys.modules.get("torch")    # who passes tensors has imported it
+        hq, d, q_stride, q = _token_rows(d_q, T, "q", torch)
+        ho, do, out_stride, out = _token_rows(d_out, T, "out", torch)
+        hkv, dk, k_stride, k = _token_rows(d_k, T, "k", torch)
+        hv, dv, v_stride, v = _token_rows(d_v, T, "v", torch)
+        if hq != ho or hkv != hv or not d == do == dk == dv:       # or some of them are addresses
+            hq, hkv, d = (hq, ho), (hkv, hv), (d, do, dk, dv)
+            hq, hkv, d = (next((x for x in same if x is not None), None) for same in (hq, hkv, d))
+            if any(x not in (None, y) for x, y in zip((ho, hv, do, dk, dv), (hq, hkv, d, d, d))):
+                raise ValueError("out has the heads of q, v those of k, and all four the same channels")
+        if d_lse is not None and not isinstance(d_lse, int):
+            if d_lse.shape != (T, hq) and (hq is not None or d_lse.dim() != 2 or d_lse.shape[0] != T) or \
+                    d_lse.dtype is not torch.float32 or not d_lse.is_contiguous() or not d_lse.is_cuda:
+                raise ValueError(f"lse must be contiguous fp32 [{T}, query heads] on the GPU")
+        if d_block_table is not None or max_blocks is not None:
+            table = self._table if d_block_table is None else d_block_table
+            width = c.max_blocks if max_blocks is None else max_blocks
+            self._check_table(table, width)
+            c.d_block_table, c.max_blocks, self._table = _ptr(table), width, table
+        c.q_stride, c.out_stride, c.k_stride, c.v_stride = q_stride, out_stride, k_stride, v_stride
+        c.d_q, c.d_k, c.d_v, c.d_out, c.d_lse = q, k, v, out, _ptr(d_lse)
+        self.heads = hq, hkv, d
         return self
+
+    def _check_table(self, table, width):
+        if table is None or isinstance(table, int):
+            return
+        if table.dtype is not sys.modules["torch"].int32 or table.numel() < len(self.new_len) * width or not table.is_contiguous() or \
+                not table.is_cuda:
+            raise ValueError(f"the block table must be contiguous int32 [{len(self.new_len)}, {width}] on the GPU")
+
+    def _check_pool(self, pool):
+        """The tensors set last have the pool's heads (None: an address, of whose heads nothing is known)."""
+        have = _geometry.get(pool, self.heads)
+        if any(a not in (None, b) for a, b in zip(self.heads, have)):
+            raise ValueError("the pool has %d query heads and %d KV heads of %d" % have)
 
 
 def gk_prompt_plan_build(pool, batch, stream=None):
     out = c_vp()
     _check(lib().gk_prompt_plan_build(pool, ctypes.byref(batch.c), _stream(stream), ctypes.byref(out)), pool)
+    _prompt_tokens[out.value] = batch.tokens
     return out.value
 
 
 def gk_prompt_plan_update(pool, plan, batch, stream=None):
     _check(lib().gk_prompt_plan_update(plan, ctypes.byref(batch.c), _stream(stream)), pool)
+    _prompt_tokens[plan] = batch.tokens
 
 
 def gk_prompt_plan_destroy(plan):
+    _prompt_tokens.pop(plan, None)
     lib().gk_prompt_plan_destroy(plan)
 
 
@@ -560,6 +602,10 @@ def gk_prompt_plan_items(plan):
 
 
 def gk_prompt_attn(pool, stream, layer, batch, plan):
+    if _geometry.get(pool) != batch.heads:
+        batch._check_pool(pool)
+    if _prompt_tokens.get(plan, batch.tokens) != batch.tokens:
+        raise ValueError("the plan is of another number of tokens than the batch")
     st = lib().gk_prompt_attn(pool, _stream(stream), layer, batch.ref, plan)
     if st:
         _check(st, pool)
