@@ -362,9 +362,10 @@ class Tables:
         self.num_free_out = num_free if num_free_out is None else num_free_out
         self.table, self.free, self.length, self.num_free = table, free, length, num_free
         rows, width = table.shape
+        self.rows, self.i32, self.i64 = rows, sys.modules["torch"].int32, sys.modules["torch"].int64
         for x, n in ((table, rows * width), (free, free.numel()), (length, rows), (num_free, 1), (self.length_out, rows),
                      (self.num_free_out, 1)):
-            if x.numel() != n or x.element_size() != 4 or x.is_floating_point() or not x.is_contiguous():
+            if x.numel() != n or x.dtype is not self.i32 or not x.is_contiguous():
                 raise ValueError("tables are contiguous int32 tensors: table [rows, max_blocks], free, length [rows], num_free [1]")
         # int32 words: allocations are at least 16-byte aligned
         self.work = table.new_empty((rows + 1) * (GK_TABLES_WORK_PER_ROW // 4))
@@ -373,9 +374,21 @@ class Tables:
         self.ref = ctypes.byref(self.c)
 
 
+def _row_of(x, n, dtype, what):
+    """Address of x, a contiguous tensor of at least n elements, or an address."""
+    if x is None or isinstance(x, int):
+        return x
+    if x.dtype is not dtype or x.numel() < n or not x.is_contiguous():
+        raise ValueError(f"{what} must be contiguous {dtype} with {n} elements or more")
+    return x.data_ptr()
+
+
 def gk_tables_step(pool, stream, tables, d_add, d_slot_mapping, d_done, d_release=None, n_slots=None):
-    st = lib().gk_tables_step(pool, _stream(stream), tables.ref, None if d_release is None else _ptr(d_release), _ptr(d_add),
-                              d_slot_mapping.numel() if n_slots is None else n_slots, _ptr(d_slot_mapping), _ptr(d_done))
+    """int32 [rows] add, done and release (flags), int64 [n_slots] slot mapping: torch tensors or addresses."""
+    rows, n, i32, i64 = tables.rows, d_slot_mapping.numel() if n_slots is None else n_slots, tables.i32, tables.i64
+    st = lib().gk_tables_step(pool, _stream(stream), tables.ref, _row_of(d_release, rows, i32, "release"),
+                              _row_of(d_add, rows, i32, "add"), n, _row_of(d_slot_mapping, n, i64, "the slot mapping"),
+                              _row_of(d_done, rows, i32, "done"))
     if st:
         _check(st, pool)
 
