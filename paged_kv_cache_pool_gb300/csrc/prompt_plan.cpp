@@ -210,18 +210,23 @@ gk_status build_host(Pool* p, const gk_prompt_batch* b, PromptPlan* pl) {
   // gains more than the join costs (steps with few rows and many keys): the same 64 turns take
   // 158 us in pieces and 219 us whole; one question of 77 tokens, with one tile, stays whole.
   const int num_sms = p->dev.num_sms;
-  double work = 0;
+  double work = 0, longest_us = 0;
   int32_t longest = 1;
   for (const Shape& s : shapes) {
     work += Hkv * cost(s, s.ntile);
     longest = std::max(longest, s.ntile);
+    longest_us = std::max(longest_us, cost(s, s.ntile));
   }
+  const double mean = work / num_sms;
   int32_t best = longest;
   double best_t = 1e300;
-  // (with two dozen items per SM whole ranges balance by themselves)
-  if (shapes.size() * (size_t)Hkv < 24 * (size_t)num_sms) {
-    for (int k = 0; k <= 8; ++k) {
-      const int32_t most = k == 0 ? longest : std::max(1, (int32_t)(work / num_sms / kTile2Us / k));
+  // Two dozen items per SM, none of which stands out, balance by themselves.  With one that does
+  // (a single context of 131072 tokens among 456 of 16) whole ranges leave an SM with 1025 tiles where
+  // the others have 48: two sizes are tried then, as each takes some 100 ns of host time an item.
+  const bool many = shapes.size() * (size_t)Hkv >= 24 * (size_t)num_sms;
+  if (!many || longest_us > mean / 8) {
+    for (int k = 0; k <= (many ? 2 : 8); ++k) {
+      const int32_t most = k == 0 ? longest : std::max(1, (int32_t)(mean / kTile2Us / k));
       if (k > 0 && most >= longest) continue;
       std::vector<double> costs;
       double joined = 0;
@@ -238,7 +243,7 @@ gk_status build_host(Pool* p, const gk_prompt_batch* b, PromptPlan* pl) {
         best_t = t;
         best = most;
       }
-      if (best_t <= work / num_sms + kJoinLaunchUs) break;   // pieces add a join to at least this much
+      if (best_t <= mean + kJoinLaunchUs) break;   // pieces add a join to at least this much
     }
   }
 
