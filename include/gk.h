@@ -411,6 +411,7 @@ typedef struct gk_prompt_plan_summary {
   int32_t partials;               /* partial states the join combines (0: no join launch) */
   int32_t max_pieces;             /* most items over one block of rows' keys */
   int32_t max_cta_tiles;          /* 128-key tiles of the CTA with the most */
+  int64_t scratch_bytes;          /* of the partial states: 4 * (d + 1) for each row of each, at most 32 states a row */
 } gk_prompt_plan_summary;
 
 /* Plan a prompt step: cut the rows into items, balance them over the SMs by their
@@ -421,7 +422,9 @@ typedef struct gk_prompt_plan_summary {
  * graph.  Tables and partial states are owned by the plan; calls that use a plan
  * must be ordered on one stream.  GK_ERR_INVALID for a negative length, a HOT
  * prefix that is not live with that length, a context longer than its
- * block-table row, or more than 2^31 - 1 tokens.  Allocates device memory and
+ * block-table row, or more than 2^31 - 1 tokens.  Allocates device memory (the
+ * tables, some hundred bytes an item, and scratch_bytes; a plan that grows takes up
+ * to half as much again, and keeps it until it is destroyed) and
  * uploads from a buffer that the next plan rewrites: on a stream that is capturing
  * it does nothing and returns GK_ERR_UNSUPPORTED.  The pool's device must be the
  * current one, here and in gk_prompt_attn (else GK_ERR_INVALID). */

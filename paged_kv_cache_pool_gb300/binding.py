@@ -89,7 +89,8 @@ class gk_prompt_batch(ctypes.Structure):
 
 class gk_prompt_plan_summary(ctypes.Structure):
     _fields_ = [("tokens", c_i64), ("flops", c_i64), ("bytes", c_i64), ("items", c_i32), ("ctas", c_i32),
-                ("stacked_requests", c_i32), ("partials", c_i32), ("max_pieces", c_i32), ("max_cta_tiles", c_i32)]
+                ("stacked_requests", c_i32), ("partials", c_i32), ("max_pieces", c_i32), ("max_cta_tiles", c_i32),
+                ("scratch_bytes", c_i64)]
 
 
 P = ctypes.POINTER

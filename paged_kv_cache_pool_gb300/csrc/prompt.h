@@ -25,6 +25,8 @@ struct PromptItemDev {
   int32_t tile0;       // key tiles [tile0, tile0 + ntile) of the request: HOT, COLD, new
   int32_t ntile;
   int32_t entry;       // partial state, -1 = the item covers every key and writes the output
+  int32_t part_row;    // its first row: a state has one for each row of the item's tokens, token by token
+  int32_t pad0;
 };
 
 struct PromptJoinDev { // 32 rows of a block whose keys several items cover
@@ -32,9 +34,10 @@ struct PromptJoinDev { // 32 rows of a block whose keys several items cover
   int32_t head;
   int32_t tok0;        // first token of the block
   int32_t row0;        // first of the 32 rows, counted from the block's first
-  int32_t own0, own_n; // partial states of the block's own items
-  int32_t hot0, hot_n; // partial states of the stacked prefix items of this head (hot_n per block), 0 = none
+  int32_t own0, own_n; // first row of the partial states of the block's own items, and how many states
+  int32_t hot0, hot_n; // the same of the stacked prefix items of this head (hot_n states per block), 0 = none
   int32_t hot_tok;     // the block's first token, counted from the first token of the stacked requests
+  int32_t hot_len;     // tokens of the stacked requests
 };
 
 struct PromptPlan {
@@ -49,6 +52,7 @@ struct PromptPlan {
   std::vector<int32_t> cta_begin;        // [CTAs + 1]
   std::vector<PromptJoinDev> joins;
   int32_t n_entries = 0;
+  int64_t part_rows = 0;                 // rows of all partial states
   uint8_t hot_maps[256] = {};            // tensor maps of the HOT pool's K and V (any_hot)
   void* d_buf = nullptr;
   void* h_stage = nullptr;
@@ -56,9 +60,9 @@ struct PromptPlan {
   bool staged = false;
   size_t d_bytes = 0;
   size_t off_reqs = 0, off_items = 0, off_begin = 0, off_joins = 0;
-  float* d_part_o = nullptr;             // [entries][256][d]
-  float* d_part_l = nullptr;             // [entries][256] (log2)
-  size_t part_entries = 0;
+  float* d_part_o = nullptr;             // [rows][d]
+  float* d_part_l = nullptr;             // [rows] (log2)
+  size_t part_cap = 0;                   // rows that both hold
   bool uploaded = false;
 };
 

@@ -104,8 +104,8 @@ struct Params {
   const uint16_t *q, *k, *v;      // add_hidden_values only
   uint16_t* out;
   float* lse;
-  float* part_o;                  // [entries][256][D]
-  float* part_l;                  // [entries][256], log2
+  float* part_o;                  // [rows of the partial states][D]
+  float* part_l;                  // [rows], log2
   int64_t q_stride, k_stride, v_stride, out_stride;
   int64_t cold_slots;
   int64_t cold_blocks;
@@ -797,7 +797,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       dst = lse_dst = 0;
       if (tr < p.tpt && tk < rq.n) {
         const int qh = it.head * p.G + hr;
-        const int64_t prow = (int64_t)it.entry * 256 + qi * BM + row, orow = rq.t0 + tk;
+        const int64_t prow = it.part_row + qi * p.tpt * p.G + row, orow = rq.t0 + tk;
         dst = part_row ? (uint64_t)(p.part_o + prow * D) : 1;
         lse_dst = part_row ? (uint64_t)(p.part_l + prow) : p.lse ? (uint64_t)(p.lse + orow * p.Hq + qh) : 0;
       }
@@ -1030,19 +1030,20 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const PromptJoinDev* _
   const PromptJoinDev jn = joins[blockIdx.x];
   const PromptReqDev rq = reqs[jn.req];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int own_ld = jn.own0, n = jn.own_n + jn.hot_n;
+  const int n = jn.own_n + jn.hot_n;
+  const int own_rows = min(2 * tpt, rq.n - jn.tok0) * G;   // of each of the block's own states
 #pragma unroll 1
   for (int u = 0; u < 4; ++u) {
     const int r = jn.row0 + u * 8 + warp;          // row of the block, counted token by token
     const int local = r / G, h = r % G;            // token of the block, head of the group
     const int tk = jn.tok0 + local;
     if (local >= 2 * tpt || tk >= rq.n) break;     // warp-uniform
-    const int64_t own_row = (local / tpt) * 128 + (local % tpt) * G + h;
+    // the stacked prefix: whole blocks before the token's, hot_n states each, then its own block's states
     const int ht = jn.hot_tok + local, hb = ht / (2 * tpt), hl = ht % (2 * tpt);
-    const int64_t hot_row = (hl / tpt) * 128 + (hl % tpt) * G + h;
+    const int hot_rows = min(2 * tpt, jn.hot_len - hb * 2 * tpt) * G;
+    const int64_t hot_row = jn.hot0 + (int64_t)hb * 2 * tpt * G * jn.hot_n + hl * G + h;
     auto entry_row = [&](int e) {
-      return e < jn.own_n ? (int64_t)(own_ld + e) * 256 + own_row
-                          : (int64_t)(jn.hot0 + hb * jn.hot_n + (e - jn.own_n)) * 256 + hot_row;
+      return e < jn.own_n ? jn.own0 + (int64_t)e * own_rows + r : hot_row + (int64_t)(e - jn.own_n) * hot_rows;
     };
     const float le = lane < n ? __ldcg(part_l + entry_row(lane)) : -INFINITY;
     float mx = le;

@@ -27,6 +27,7 @@ struct Run {              // neighbouring requests whose rows are stacked over o
   int32_t rec;            // its record in reqs
   int32_t n;              // tokens
   int32_t entry0 = 0;     // partial states: entry0 + (head * blocks + block) * pieces + piece
+  int64_t row0 = 0;       // the first one's first row
   int32_t pieces = 1;
   int32_t blocks = 0;
 };
@@ -80,6 +81,7 @@ gk_status build_host(Pool* p, const gk_prompt_batch* b, PromptPlan* pl) {
   pl->cta_begin.assign(1, 0);
   pl->joins.clear();
   pl->n_entries = 0;
+  pl->part_rows = 0;
   pl->any_hot = pl->any_cold = false;
   pl->max_blocks = 0;
   gk_prompt_plan_summary sum{};
@@ -250,46 +252,54 @@ gk_status build_host(Pool* p, const gk_prompt_batch* b, PromptPlan* pl) {
   // ---- items, partial states, joins --------------------------------------------------
   std::vector<PromptItemDev> items;
   std::vector<double> costs;
-  int64_t entries = 0;
+  int64_t entries = 0, part_rows = 0;             // a state has as many rows as its block
   for (const Shape& s : shapes) {                 // the runs come first: their entries are known to the joins
     const int32_t np = pieces_of(s.ntile, best);
     sum.max_pieces = std::max(sum.max_pieces, np);
     const bool parts = np > 1 || s.joined;
+    const int32_t rows = std::min(bt, pl->reqs[(size_t)s.req].n - s.tok0) * G;
     for (int32_t h = 0; h < Hkv; ++h) {
-      int64_t entry = -1;
+      int64_t entry = -1, part_row = -1;
       if (s.run >= 0) {
         Run& run = runs[(size_t)s.run];
         if (s.run_block == 0 && h == 0) {
           run.entry0 = (int32_t)entries;
+          run.row0 = part_rows;
           run.pieces = np;
           entries += (int64_t)Hkv * run.blocks * np;
+          part_rows += (int64_t)Hkv * run.n * G * np;
         }
         entry = run.entry0 + ((int64_t)h * run.blocks + s.run_block) * np;
+        part_row = run.row0 + ((int64_t)h * run.n + s.tok0) * G * np;    // the blocks before are whole
       } else if (parts) {
         entry = entries;
+        part_row = part_rows;
         entries += np;
-        const int32_t rows = std::min(bt, pl->reqs[(size_t)s.req].n - s.tok0) * G;
+        part_rows += (int64_t)np * rows;
         for (int32_t row = 0; row < rows; row += 32) {
-          PromptJoinDev jn{s.req, h, s.tok0, row, (int32_t)entry, np, 0, 0, s.hot_tok};
+          PromptJoinDev jn{s.req, h, s.tok0, row, (int32_t)part_row, np, 0, 0, s.hot_tok, 0};
           if (s.hot_run >= 0) {
             const Run& run = runs[(size_t)s.hot_run];
-            jn.hot0 = run.entry0 + h * run.blocks * run.pieces;
+            jn.hot0 = (int32_t)(run.row0 + (int64_t)h * run.n * G * run.pieces);
             jn.hot_n = run.pieces;
+            jn.hot_len = run.n;
           }
           pl->joins.push_back(jn);
         }
       }
-      if (entries > INT32_MAX / 256) return fail(p, GK_ERR_INVALID, "too many partial states");
+      if (part_rows > INT32_MAX) return fail(p, GK_ERR_INVALID, "too many partial states");
       int32_t tile = s.tile0;
       for (int32_t x = 0; x < np; ++x) {
         const int32_t nt = s.ntile / np + (x < s.ntile % np);
-        items.push_back({s.req, h, s.tok0, tile, nt, parts ? (int32_t)entry + x : -1});
+        items.push_back({s.req, h, s.tok0, tile, nt, parts ? (int32_t)entry + x : -1,
+                         parts ? (int32_t)(part_row + (int64_t)x * rows) : -1, 0});
         costs.push_back(cost(s, nt));
         tile += nt;
       }
     }
   }
   pl->n_entries = (int32_t)entries;
+  pl->part_rows = part_rows;
 
   // ---- CTA lists ---------------------------------------------------------------------
   const int ctas = (int)std::min<size_t>((size_t)num_sms, items.size());
@@ -318,6 +328,7 @@ gk_status build_host(Pool* p, const gk_prompt_batch* b, PromptPlan* pl) {
   sum.items = (int32_t)items.size();
   sum.ctas = ctas;
   sum.partials = pl->n_entries;
+  sum.scratch_bytes = part_rows * (d + 1) * (int64_t)sizeof(float);
   pl->summary = sum;
   return GK_OK;
 }
@@ -377,25 +388,25 @@ gk_status upload(Pool* p, PromptPlan* pl, void* stream) {
   e = cudaEventRecord(pl->upload_done, st);
   if (e != cudaSuccess) return cuda_fail(p, e, "cudaEventRecord");
   pl->staged = true;
-  if ((size_t)pl->n_entries > pl->part_entries) {
+  if ((size_t)pl->part_rows > pl->part_cap) {
     if (pl->d_part_o) {
       e = cudaStreamSynchronize(st);
       if (e != cudaSuccess) return cuda_fail(p, e, "cudaStreamSynchronize");
       cudaFree(pl->d_part_o);
       cudaFree(pl->d_part_l);
       pl->d_part_o = pl->d_part_l = nullptr;
-      pl->part_entries = 0;
+      pl->part_cap = 0;
     }
-    const size_t cap = (size_t)pl->n_entries + (size_t)pl->n_entries / 4;
-    e = cudaMalloc(&pl->d_part_o, cap * 256 * (size_t)p->cfg.head_dim * sizeof(float));
+    const size_t cap = (size_t)pl->part_rows + (size_t)pl->part_rows / 4;
+    e = cudaMalloc(&pl->d_part_o, cap * (size_t)p->cfg.head_dim * sizeof(float));
     if (e != cudaSuccess) return cuda_fail(p, e, "cudaMalloc(prompt partial outputs)");
-    e = cudaMalloc(&pl->d_part_l, cap * 256 * sizeof(float));
+    e = cudaMalloc(&pl->d_part_l, cap * sizeof(float));
     if (e != cudaSuccess) {
       cudaFree(pl->d_part_o);
       pl->d_part_o = nullptr;
       return cuda_fail(p, e, "cudaMalloc(prompt partial lse)");
     }
-    pl->part_entries = cap;
+    pl->part_cap = cap;
   }
   pl->uploaded = true;
   return GK_OK;
