@@ -198,8 +198,8 @@ def _i32p(a):
     return a.ctypes.data_as(P(c_i32))
 
 
-# what the checks of tensors need to know: heads and channels by pool, tokens by prompt plan
-_geometry, _prompt_tokens = {}, {}
+# what the checks of tensors need to know: (query heads, KV heads, channels) by pool, and behind the tokens by prompt plan
+_geometry, _prompt_shape = {}, {}
 
 
 # ---- pool ----------------------------------------------------------------------
@@ -536,7 +536,7 @@ class PromptBatch:
         self._check_table(d_block_table, max_blocks)
         self._table = d_block_table
         self.c.d_block_table = _ptr(d_block_table)
-        self.heads = None, None, None          # query heads, KV heads and channels of the tensors set last
+        self.shape = self.tokens, None, None, None   # and query heads, KV heads and channels of the tensors set last
         self.ref = ctypes.byref(self.c)
 
     def set_device(self, d_q, d_k, d_v, d_out, d_lse=None, d_block_table=None, max_blocks=None):
@@ -564,7 +564,7 @@ class PromptBatch:
             c.d_block_table, c.max_blocks, self._table = _ptr(table), width, table
         c.q_stride, c.out_stride, c.k_stride, c.v_stride = q_stride, out_stride, k_stride, v_stride
         c.d_q, c.d_k, c.d_v, c.d_out, c.d_lse = q, k, v, out, _ptr(d_lse)
-        self.heads = hq, hkv, d
+        self.shape = T, hq, hkv, d
         return self
 
     def _check_table(self, table, width):
@@ -574,27 +574,29 @@ class PromptBatch:
                 not table.is_cuda:
             raise ValueError(f"the block table must be contiguous int32 [{len(self.new_len)}, {width}] on the GPU")
 
-    def _check_pool(self, pool):
-        """The tensors set last have the pool's heads (None: an address, of whose heads nothing is known)."""
-        have = _geometry.get(pool, self.heads)
-        if any(a not in (None, b) for a, b in zip(self.heads, have)):
-            raise ValueError("the pool has %d query heads and %d KV heads of %d" % have)
+    def check_plan(self, plan):
+        """The plan is of as many tokens, and its pool has the tensors' heads (None: an address's are not known)."""
+        want = _prompt_shape.get(plan, self.shape)
+        if want[0] != self.tokens:
+            raise ValueError("the plan is of another number of tokens than the batch")
+        if any(None is not a != b is not None for a, b in zip(self.shape, want)):
+            raise ValueError("the pool has %s query heads and %s KV heads of %s" % want[1:])
 
 
 def gk_prompt_plan_build(pool, batch, stream=None):
     out = c_vp()
     _check(lib().gk_prompt_plan_build(pool, ctypes.byref(batch.c), _stream(stream), ctypes.byref(out)), pool)
-    _prompt_tokens[out.value] = batch.tokens
+    _prompt_shape[out.value] = (batch.tokens, *_geometry.get(pool, (None, None, None)))
     return out.value
 
 
 def gk_prompt_plan_update(pool, plan, batch, stream=None):
     _check(lib().gk_prompt_plan_update(plan, ctypes.byref(batch.c), _stream(stream)), pool)
-    _prompt_tokens[plan] = batch.tokens
+    _prompt_shape[plan] = (batch.tokens, *_geometry.get(pool, (None, None, None)))
 
 
 def gk_prompt_plan_destroy(plan):
-    _prompt_tokens.pop(plan, None)
+    _prompt_shape.pop(plan, None)
     lib().gk_prompt_plan_destroy(plan)
 
 
@@ -616,10 +618,8 @@ def gk_prompt_plan_items(plan):
 
 
 def gk_prompt_attn(pool, stream, layer, batch, plan):
-    if _geometry.get(pool) != batch.heads:
-        batch._check_pool(pool)
-    if _prompt_tokens.get(plan, batch.tokens) != batch.tokens:
-        raise ValueError("the plan is of another number of tokens than the batch")
+    if _prompt_shape.get(plan) != batch.shape:
+        batch.check_plan(plan)
     st = lib().gk_prompt_attn(pool, _stream(stream), layer, batch.ref, plan)
     if st:
         _check(st, pool)
