@@ -6,6 +6,7 @@
 
 #include "device_common.cuh"
 #include "gk_internal.h"
+#include "max_nan.cuh"
 
 namespace gk {
 namespace {
@@ -13,6 +14,7 @@ namespace {
 // LSE merge (GraniKV Eq. 1, applied to any number of partial states): for each
 // request and query head, O = sum_e 2^(l_e - m) O_e / sum_e 2^(l_e - m),
 // LSE = (m + log2 sum_e 2^(l_e - m)) * ln 2, with m = max_e l_e (log2 domain).
+// A state whose LSE is NaN makes its row NaN.
 // One warp per (request, query head): entries [e0, e0 + ne).  Lane e holds
 // entry e's LSE and weight (entries beyond 32 are folded in a second round);
 // the d-wide rows are read ROWS entries per round trip, every load of a round
@@ -42,9 +44,9 @@ __device__ __forceinline__ void merge_head(const float* part_o, const float* par
   float4 v0[ROWS];
   load_rows(v0, 0, 0, min(32, ne));
   float mx = l0;
-  for (int e = lane + 32; e < ne; e += 32) mx = fmaxf(mx, __ldcg(part_l + (int64_t)(e0 + e) * Hq + qh));
+  for (int e = lane + 32; e < ne; e += 32) mx = max_nan(mx, __ldcg(part_l + (int64_t)(e0 + e) * Hq + qh));
 #pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+  for (int off = 16; off >= 1; off >>= 1) mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, off));
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   float z = 0.f;
   if (mx != -INFINITY) {

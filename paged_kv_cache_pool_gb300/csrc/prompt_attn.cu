@@ -74,6 +74,7 @@
 #include <cstring>
 #include <type_traits>
 
+#include "max_nan.cuh"
 #include "prefix_body.cuh"
 #include "prompt.h"
 
@@ -1003,13 +1004,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
-}
-
-// the larger of two numbers; NaN where one of them is (fmaxf drops it)
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float m;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
-  return m;
 }
 
 // Joins the partial states of rows whose keys several items covered: with l_e the
