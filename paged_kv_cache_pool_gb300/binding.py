@@ -592,7 +592,7 @@ def gk_prompt_plan_build(pool, batch, stream=None):
 
 def gk_prompt_plan_update(pool, plan, batch, stream=None):
     _check(lib().gk_prompt_plan_update(plan, ctypes.byref(batch.c), _stream(stream)), pool)
-    _prompt_shape[plan] = (batch.tokens, *_geometry.get(pool, (None, None, None)))
+    _prompt_shape[plan] = (batch.tokens, *_prompt_shape.get(plan, (0, None, None, None))[1:])
 
 
 def gk_prompt_plan_destroy(plan):
