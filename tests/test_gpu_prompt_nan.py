@@ -91,3 +91,31 @@ def test_pieces_of_keys_that_score_minus_infinity_weigh_nothing():
     with np.errstate(invalid="ignore"):
         _verify(p, np.zeros((p.T, p.hq), bool), "minus infinity")
     p.close()
+
+
+@pytest.mark.parametrize("name", sorted(STEPS))
+def test_rows_whose_every_score_is_minus_infinity(name):
+    """out = 0 and lse = -inf, whole, in pieces and stacked."""
+    new, prefixes, which, cold, parts = STEPS[name]
+    p = Prompts(128, 4, 2, new, prefixes=prefixes, which=which, cold=cold, spare_nan=False)
+    p.q[:, :, 0] = p.q[:, :, 0].abs() + 0.5
+    p.q[:, 1, 0] = -p.q[:, 1, 0]        # ... but of head 1 plus infinity, which has no softmax
+    for x in (p.hot[0].view(-1, p.d), p.cold[0], p.k):
+        x[..., 0] = float("-inf")
+    p.run()
+    torch.cuda.synchronize()
+    assert (p.info()["partials"] > 0) == parts
+    out, lse = p.host(p.out), p.host(p.lse)
+    assert np.isnan(out[:, 1]).all() and np.isnan(lse[:, 1]).all()
+    rest = [h for h in range(p.hq) if h != 1]
+    assert (out[:, rest] == 0).all() and (lse[:, rest] == -np.inf).all()
+    p.close()
+
+
+@pytest.mark.parametrize("scale", [1.0, 8.0, 64.0])
+def test_large_finite_values(scale):
+    """V up to 2^62, over scores that rise far above a row's first keys: nothing overflows before the division by Z."""
+    p = Prompts(128, 4, 2, [300, 20], cold=[0, 2000], scale=scale)
+    p.v.mul_(2.0 ** 60).clamp_(-2.0 ** 62, 2.0 ** 62)
+    p.run().verify(f"large values, queries by {scale}")
+    p.close()
