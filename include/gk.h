@@ -414,20 +414,22 @@ typedef struct gk_prompt_plan_summary {
   int64_t scratch_bytes;          /* of the partial states: 4 * (d + 1) for each row of each, at most 32 states a row */
 } gk_prompt_plan_summary;
 
-/* Plan a prompt step: cut the rows into items, balance them over the SMs by their
- * key tiles (long key ranges of steps with few rows are split and joined by
- * log-sum-exp, GraniKV Eq. 1; neighbouring requests with the same HOT prefix and
- * few rows each are stacked over it, Section 2.3).  Depends only on the host
- * arrays, so one plan serves every layer and may be replayed from a captured
- * graph.  Tables and partial states are owned by the plan; calls that use a plan
- * must be ordered on one stream.  GK_ERR_INVALID for a negative length, a HOT
- * prefix that is not live with that length, a context longer than its
- * block-table row, or more than 2^31 - 1 tokens.  Allocates device memory (the
- * tables, some hundred bytes an item, and scratch_bytes; a plan that grows takes up
- * to half as much again, and keeps it until it is destroyed) and
- * uploads from a buffer that the next plan rewrites: on a stream that is capturing
- * it does nothing and returns GK_ERR_UNSUPPORTED.  The pool's device must be the
- * current one, here and in gk_prompt_attn (else GK_ERR_INVALID). */
+/* Plan a prompt step: cut the rows into items, balance them over the SMs by their key
+ * tiles (long key ranges of steps with few rows are split and joined by log-sum-exp,
+ * GraniKV Eq. 1; neighbouring requests with the same HOT prefix and few rows each are
+ * stacked over it, Section 2.3; requests of one prefix that others stand between are
+ * not, and each reads it by itself: 64 requests of 1 to 16 tokens over four prefixes
+ * of 16384 take five times the key tiles in round robin that they take sorted by
+ * prefix).  Depends only on the host arrays, so one plan serves every layer and may
+ * be replayed from a captured graph.  Tables and partial states are owned by the
+ * plan; calls that use a plan must be ordered on one stream.  GK_ERR_INVALID for a
+ * negative length, a HOT prefix that is not live with that length, a context longer
+ * than its block-table row, or more than 2^31 - 1 tokens.  Allocates device memory
+ * (the tables, some hundred bytes an item, and scratch_bytes; a plan that grows takes
+ * up to half as much again, and keeps it until it is destroyed) and uploads from a
+ * buffer that the next plan rewrites: on a stream that is capturing it does nothing
+ * and returns GK_ERR_UNSUPPORTED.  The pool's device must be the current one, here
+ * and in gk_prompt_attn (else GK_ERR_INVALID). */
 gk_status gk_prompt_plan_build(gk_pool* pool, const gk_prompt_batch* batch, void* stream, gk_prompt_plan** out);
 /* Re-plan for the next step, reusing the buffers; on the stream of the plan's earlier
  * work.  A graph captured with the plan holds the launch of the step planned then:
@@ -449,15 +451,18 @@ gk_status gk_prompt_plan_items(const gk_prompt_plan* plan, int32_t* n_ctas, int3
 /* Attention of one layer of a planned prompt step: with s_j = q.k_j / sqrt(d) over
  * the keys the row attends, out = sum_j e^(s_j) v_j / Z and lse = ln Z, Z = sum_j
  * e^(s_j).  Products and sums are held in fp32; the weights are rounded to bf16
- * before the product with V, the output to bf16 at the end; scores of magnitude
- * 2^28 and more, which fp32 holds to whole tens only, are out of range.  Keys a row does not
- * attend contribute nothing, whatever their K and V hold (infinities and NaN
- * included).  Reads COLD through the block table (an out-of-range block id
- * counts as zero K and V and is reported as GK_ERR_DEVICE_BOUNDS by
- * gk_device_error()) and does not write the pool: gk_append_kv (or
- * gk_write_prefix_kv) stores the new tokens, before or after.  The batch's
- * lengths and HOT bases are the plan's; only its device pointers and strides are
- * read.  May be captured. */
+ * before the product with V, the output to bf16 at the end.  Out of range are scores
+ * of magnitude 2^28 and more, which fp32 holds to whole tens only, and finite values
+ * of V of magnitude 2^63 and more, whose products with weights of up to 2^64 before
+ * the division by Z could overflow.  A row that attends a score of NaN (or of plus
+ * infinity) comes out NaN, lse too; where every score is minus infinity out is 0 and
+ * lse minus infinity.  Keys a row does not attend contribute nothing, whatever their
+ * K and V hold (infinities and NaN included).  Reads COLD through the block table (an
+ * out-of-range block id counts as zero K and V and is reported as
+ * GK_ERR_DEVICE_BOUNDS by gk_device_error()) and does not write the pool:
+ * gk_append_kv (or gk_write_prefix_kv) stores the new tokens, before or after.  The
+ * batch's lengths and HOT bases are the plan's; only its device pointers and strides
+ * are read.  May be captured. */
 gk_status gk_prompt_attn(gk_pool* pool, void* stream, int32_t layer, const gk_prompt_batch* batch,
                          const gk_prompt_plan* plan);
 

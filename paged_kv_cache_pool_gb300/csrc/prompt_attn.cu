@@ -5,8 +5,11 @@
 // (KV head h / g), over the keys HOT 0..Lp-1, COLD 0..c-1, new 0..i:
 //   s_j = q.k_j / sqrt(d),  m = max_j s_j,  Z = sum_j e^(s_j - m),
 //   O = sum_j e^(s_j - m) v_j / Z,  LSE = m + ln Z.
-// 4 d flop per (row, key) against 4 d / g bytes per key and 256 rows, so any
-// prompt of more than a few tokens is bound by the tensor cores, not by HBM.
+// A key of one KV head is 4 d bytes and 4 d flop for each of the n g rows of the
+// request's n tokens: n g flop per byte where the keys are its own, so that it is
+// bound by the tensor cores above some 292 / g tokens (73 at g = 4; 1950 TFLOP/s
+// against 6.69 TB/s), and by HBM or a chain of latencies below.  New tokens and
+// shared prefixes are read again from L2 by each 256 rows.
 //
 // One work item = one KV head x 2 * tpt consecutive tokens of one request (tpt =
 // floor(128 / g); the g query heads of a token are g consecutive rows, so an item
@@ -43,7 +46,7 @@
 // and next S (1400) -> softmax with its hand-overs (250), of which the two Q tiles overlap
 // all but the products.  An item costs about 3.5 us besides (first Q and S, first
 // reference, output), which is what bounds short prompts: 64 prompts of 256 tokens on 32/8
-// heads take 82 us.  COLD tiles cost 1.60 us: their copies share the schedulers with the
+// heads take 82-87 us.  COLD tiles cost 1.60 us: their copies share the schedulers with the
 // softmax (two chunks of 2048 tokens over 6000-12000 in pages of 16: 465 us, 1.40 PFLOP/s).
 // In short prompts a fifth of the stalls wait for instructions: the roles' code is
 // 110 KB, so variants of the softmax share one copy of it.  Tried and slower, in ns a key

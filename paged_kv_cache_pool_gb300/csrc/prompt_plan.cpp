@@ -144,8 +144,9 @@ gk_status build_host(Pool* p, const gk_prompt_batch* b, PromptPlan* pl) {
 
   // ---- neighbouring requests stacked over their HOT prefix ------------------------
   // Worth it where the tiles saved cost more than joining every row of the run: 64 turns of
-  // 1-16 tokens behind one prefix of 16384 take 158 us stacked and 691 us apart; turns of 64-600
-  // tokens, which fill their own items, stay apart.
+  // 1-16 tokens behind one prefix of 16384 take 137 us stacked and 647 us apart; turns of 64-600
+  // tokens, which fill their own items, stay apart.  Only neighbours: an item's rows are loaded as
+  // one box of the packed tokens.
   std::vector<Run> runs;
   std::vector<int32_t> run_of((size_t)B, -1), run_tok((size_t)B, 0);
   for (int32_t r = 0; r < B;) {
@@ -210,7 +211,7 @@ gk_status build_host(Pool* p, const gk_prompt_batch* b, PromptPlan* pl) {
   // ---- how many key tiles one item takes -------------------------------------------
   // Whole ranges, or pieces of at most `most` tiles where the balance over the SMs
   // gains more than the join costs (steps with few rows and many keys): the same 64 turns take
-  // 158 us in pieces and 219 us whole; one question of 77 tokens, with one tile, stays whole.
+  // 137 us in pieces and 195 us whole; one question of 77 tokens, with one tile, stays whole.
   const int num_sms = p->dev.num_sms;
   double work = 0, longest_us = 0;
   int32_t longest = 1;
