@@ -541,8 +541,8 @@ class PromptBatch:
 
     def set_device(self, d_q, d_k, d_v, d_out, d_lse=None, d_block_table=None, max_blocks=None):
         """bf16 [T, Hq, d] q and out, [T, Hkv, d] k and v, fp32 [T, Hq] lse, int32 [B, max_blocks] table: torch tensors
-        (tokens may be strided, as views of a fused projection are; lse and table are contiguous) or addresses of packed
-        rows.  ValueError, with the batch as it was, for tensors of another type or shape."""
+        (tokens may be strided, as views of a fused projection are; lse is contiguous, and the table's rows max_blocks
+        apart) or addresses of packed rows.  ValueError, with the batch as it was, for tensors of another type or shape."""
         c, T, torch = self.c, self.tokens, sys.modules.get("torch")    # who passes tensors has imported it
         hq, d, q_stride, q = _token_rows(d_q, T, "q", torch)
         ho, do, out_stride, out = _token_rows(d_out, T, "out", torch)
@@ -570,9 +570,11 @@ class PromptBatch:
     def _check_table(self, table, width):
         if table is None or isinstance(table, int):
             return
-        if table.dtype is not sys.modules["torch"].int32 or table.numel() < len(self.new_len) * width or not table.is_contiguous() or \
-                not table.is_cuda:
-            raise ValueError(f"the block table must be contiguous int32 [{len(self.new_len)}, {width}] on the GPU")
+        n = len(self.new_len)
+        rows = table.is_contiguous() and table.numel() >= n * width or \
+            table.dim() == 2 and table.shape[0] >= n and table.stride() == (width, 1)    # the first columns of a wider table
+        if table.dtype is not sys.modules["torch"].int32 or not rows or not table.is_cuda:
+            raise ValueError(f"the block table must be int32 [{n}, {width}] on the GPU, or columns of one with rows of {width}")
 
     def check_plan(self, plan):
         """The plan is of as many tokens, and its pool has the tensors' heads (None: an address's are not known)."""

@@ -93,6 +93,11 @@ def test_block_table(gk):
             gk.PromptBatch([3, 4], None, None, [0, 20], OnGpu(y), 5)
         with pytest.raises(ValueError, match="table"):
             gk.PromptBatch([3, 4]).set_device(**tensors(), d_block_table=OnGpu(y), max_blocks=5)
+    # more rows than requests, and the first columns of a table whose rows are as far apart as said
+    for y, width in ((ints(9, 5), 5), (ints(4, 64)[:, :3], 64), (ints(1, 64)[:, :3], 64)):
+        gk.PromptBatch([3, 4][:len(y)], None, None, None, OnGpu(y), width)
+    with pytest.raises(ValueError, match="table"):
+        gk.PromptBatch([3, 4], None, None, None, OnGpu(ints(4, 64)[:, :3]), 3)
     batch = gk.PromptBatch([3, 4], None, None, [0, 20], OnGpu(ints(2, 5)), 5)
     with pytest.raises(ValueError, match="table"):
         batch.set_device(**tensors(), max_blocks=6)                         # wider rows than the table has
