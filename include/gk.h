@@ -28,6 +28,8 @@
  *  - COLD K and V: [L][cold_slots][Hkv][d] bf16 each; the slot of token t of a
  *    sequence is table[t / P] * P + t % P with P = cold_page_size
  *    ("Paged KV cache", How it works).
+ *  - COLD in 4 bits (gk_pool_create_kv4): [L][cold_slots][gk_kv4_row_bytes], one row
+ *    of codes and scales for a token's K and V together (the call gives the layout).
  *  - Queries [B][Hq][d] bf16, outputs [B][Hq][d] fp32, LSE [B][Hq] fp32
  *    (natural log).  Query head qh reads KV head qh / (Hq / Hkv).
  */
@@ -81,6 +83,27 @@ typedef struct gk_pool_config {
 /* Create a pool over caller-allocated storage.  Does not touch the device
  * contents.  *out is owned by the caller and freed with gk_pool_destroy. */
 gk_status gk_pool_create(const gk_pool_config* cfg, gk_pool** out);
+
+/* A pool whose COLD side holds K and V in 4 bits, 4.5 bits an element (5 where a row is
+ * padded) instead of 16; HOT stays bf16.  cfg->cold_k is the store of every layer's rows,
+ * [num_layers][cold_slots][gk_kv4_row_bytes(Hkv, d)], cold_v NULL; the rest is gk_pool_create's.
+ * Each 64 channels of a token's K and of its V, per KV head, are one group: with lo its least
+ * value (a bf16 value of the group itself) and span = bf16(greatest - lo),
+ *   code = min(15, round((x - lo) * 15 / span)), ties to even,   x is held as lo + code * (span / 15).
+ * A span under 2^-100 counts as 0 (every code 0).  A group that holds an infinity or NaN, or whose span
+ * reaches 2^120, is held as NaN throughout (lo NaN, span 0).
+ * A row: per KV head K's codes then V's (d / 2 bytes each: 32-bit words of eight channels, the first in
+ * the lowest four bits; word w has channels 8 w .. 8 w + 7 at d = 64 and 8 (w / 2) + 64 (w % 2) .. + 7 at
+ * d = 128, so that a thread's loads hold what its tensor-core fragments take), then per KV head the bf16
+ * pairs (lo, span) of K's groups, then of V's; padded to 16 bytes.
+ * The block manager, gk_tables_step, the HOT calls and plans work as on any pool.  Written by
+ * gk_append_kv and gk_append_qkv, read by gk_read_kv and gk_decode_kv4; the other calls that read or
+ * write COLD (gk_decode_dense, gk_decode_dense_static, gk_decode_cascade and its stages,
+ * gk_sm_speeds_measure, gk_calibrate, gk_dispatch, prompt plans with a COLD context) return
+ * GK_ERR_UNSUPPORTED. */
+gk_status gk_pool_create_kv4(const gk_pool_config* cfg, gk_pool** out);
+/* Bytes of one 4-bit row; 0 for a geometry that no pool takes. */
+int64_t gk_kv4_row_bytes(int32_t num_kv_heads, int32_t head_dim);
 void gk_pool_destroy(gk_pool* pool);
 /* Text of the pool's last error ("" if none); valid until the next call on the pool. */
 const char* gk_last_error(const gk_pool* pool);
@@ -219,7 +242,7 @@ gk_status gk_tables_step(gk_pool* pool, void* stream, const gk_tables* t, const 
  * d_slot_mapping: device int64 [n]; d_k, d_v: device bf16 [n][Hkv][d];
  * d_cow_pairs: device int32 [n_cow][2] (src, dst) or NULL when n_cow = 0.
  * Out-of-range slots or blocks are skipped and reported as GK_ERR_DEVICE_BOUNDS
- * by gk_device_error(). */
+ * by gk_device_error().  On a 4-bit pool the rows are encoded (gk_pool_create_kv4). */
 gk_status gk_append_kv(gk_pool* pool, void* stream, int32_t layer, int32_t n, const int64_t* d_slot_mapping,
                        const void* d_k, const void* d_v, int32_t n_cow, const int32_t* d_cow_pairs);
 /* Write prefix tokens [t0, t0+n) of one layer into the HOT slab at hot_base
@@ -227,6 +250,62 @@ gk_status gk_append_kv(gk_pool* pool, void* stream, int32_t layer, int32_t n, co
  * [n][Hkv][d] (token-major, the same input layout as gk_append_kv). */
 gk_status gk_write_prefix_kv(gk_pool* pool, void* stream, int32_t layer, int64_t hot_base,
                              int64_t prefix_len, int64_t t0, int64_t n, const void* d_k, const void* d_v);
+
+/* ---- from a layer's projections to its cache and attention (device) ------------ */
+
+/* The rows of n tokens between the q, k, v projection of a layer and its attention: each head of q and k
+ * is normed, then rotated by its token's position.  The pages' caches hold keys after the rotation
+ * (queries and keys reach them post-RoPE) and leave both to the engine.
+ *   norm (weight not NULL):  x <- x / sqrt(mean_i x_i^2 + eps) * weight
+ *   rotation of the first rot_dim channels, with (c, s) the cosine and sine of pair i at the position:
+ *     (x_a, x_b) <- (x_a c - x_b s, x_b c + x_a s),  (a, b) = (i, i + rot_dim / 2), or (2 i, 2 i + 1)
+ *     where interleaved; the channels from rot_dim on pass.
+ * Everything is computed in fp32 and rounded to bf16 once.  Where a token's position is outside
+ * [0, num_positions), nothing of the token is written, and it is reported as GK_ERR_DEVICE_BOUNDS by
+ * gk_device_error(). */
+typedef struct gk_qkv {
+  int32_t num_tokens;         /* n, at most 2^27 */
+  int32_t rot_dim;            /* 0 (no rotation) to head_dim, a multiple of 16 */
+  int32_t interleaved;        /* 0 or 1 */
+  float eps;                  /* of the norms, >= 0 */
+  int64_t num_positions;      /* rows of d_cos_sin */
+  const float* d_cos_sin;     /* device fp32 [num_positions][rot_dim], 16-byte aligned: rot_dim / 2 cosines,
+                                 then as many sines; NULL when rot_dim is 0 */
+  const int32_t* d_positions; /* device [n]; NULL when rot_dim is 0 */
+  const void* d_q_weight;     /* device bf16 [d], 16-byte aligned, or NULL: no norm of queries */
+  const void* d_k_weight;     /* ... of keys */
+  const void* d_q;            /* device bf16 [n][Hq][d], 16-byte aligned like all rows here; NULL: no queries */
+  const void* d_k;            /* device bf16 [n][Hkv][d] */
+  const void* d_v;            /* device bf16 [n][Hkv][d] (gk_append_qkv) */
+  void* d_q_out;              /* device bf16 [n][Hq][d], may be d_q with its stride; NULL when d_q is */
+  void* d_k_out;              /* device bf16 [n][Hkv][d], may be d_k with its stride; gk_append_qkv: may be NULL */
+  int64_t q_stride;           /* elements from one token's row to the next (views of a fused projection): */
+  int64_t k_stride;           /* a multiple of 8, at least heads * d; 0 = packed rows */
+  int64_t v_stride;
+  int64_t q_out_stride;
+  int64_t k_out_stride;
+} gk_qkv;                     /* outputs overlap no input but their own, row for row */
+
+/* q and k of n tokens, normed and rotated, to d_q_out and d_k_out (d_v is not read).  d_q or d_k may be
+ * NULL with its output.  GK_ERR_INVALID for missing or misaligned pointers, a stride or count that does not
+ * fit, a negative eps; GK_ERR_UNSUPPORTED for a rot_dim that is no multiple of 16 or above head_dim.  May
+ * be captured.  The pool gives the geometry; its device must be the current one (else GK_ERR_INVALID). */
+gk_status gk_qk_norm_rope(gk_pool* pool, void* stream, const gk_qkv* x);
+/* The same, and the tokens' K (normed and rotated) and V into the slots of one layer's COLD cache,
+ * in place of gk_qk_norm_rope and gk_append_kv: one pass over the projection's output.  d_k and d_v are
+ * required, queries and d_k_out optional.  Copy-on-write pairs are copied first.  Slots are distinct.
+ * Out-of-range slots or blocks are skipped and reported as by gk_append_kv (the token's q and k rows are
+ * still written).  On a 4-bit pool the stored keys are the codes of the bf16 keys that d_k_out gets. */
+gk_status gk_append_qkv(gk_pool* pool, void* stream, int32_t layer, const gk_qkv* x, const int64_t* d_slot_mapping,
+                        int32_t n_cow, const int32_t* d_cow_pairs);
+/* K and V of n COLD slots of one layer, as bf16 rows: a context that moves to a HOT prefix
+ * (gk_write_prefix_kv), or a 4-bit context that the next chunk of its prompt attends there.  d_slot_mapping:
+ * device int64 [n], n at most 2^27, any order, slots may repeat.  d_k, d_v: device bf16 [n][Hkv][d], 16-byte aligned, with
+ * token strides as in gk_qkv.  4-bit rows give bf16(lo + code * (span / 15)), the bracket and the sum rounded to
+ * fp32.  An out-of-range slot gives zeros and is reported as GK_ERR_DEVICE_BOUNDS by gk_device_error().
+ * May be captured.  The pool's device must be the current one (else GK_ERR_INVALID). */
+gk_status gk_read_kv(gk_pool* pool, void* stream, int32_t layer, int64_t n, const int64_t* d_slot_mapping, void* d_k,
+                     void* d_v, int64_t k_stride, int64_t v_stride);
 
 /* ---- one decode step ------------------------------------------------------- */
 
@@ -367,6 +446,23 @@ gk_status gk_cascade_suffix(gk_pool* pool, void* stream, int32_t layer, const gk
                             const gk_plan* plan);
 gk_status gk_cascade_merge(gk_pool* pool, void* stream, int32_t layer, const gk_batch* batch,
                            const gk_plan* plan);
+
+/* One layer of a planned decode step over a 4-bit pool: each request's query attends its HOT prefix (bf16)
+ * and its COLD tokens as the codes hold them, with s_j = q.k_j / sqrt(d):
+ *   out = sum_j e^(s_j) v_j / Z,   lse = ln Z,   Z = sum_j e^(s_j).
+ * The plan is gk_plan_build's on the 4-bit pool: prefix items, the COLD gather and the log-sum-exp join one
+ * after the other (a join is launched only where a request has several partial states or no token).
+ * d_out: device bf16 [B][Hq][d], 16-byte aligned, like the batch's d_q; the batch's d_out is not used, d_lse
+ * may be NULL, d_new_k and d_new_v must be (GK_ERR_UNSUPPORTED: append first, gk_append_qkv).  Products and sums
+ * are held in fp32; the weights are rounded to bf16 over the prefix and to fp16 (times the group's span, scaled by a
+ * power of two per request) over COLD, the output to bf16 at the end.  Queries of magnitude up to 2^100 are in
+ * range; a row that has a query of infinity or NaN, or attends a key that is held as NaN, comes out NaN, lse
+ * too; channels whose attended values include NaN come out NaN.  A request without a token gives 0 and
+ * minus infinity.  An out-of-range block id counts as zero K and V and is reported as GK_ERR_DEVICE_BOUNDS
+ * by gk_device_error().  The batch's lengths and HOT bases are the plan's; only its device pointers and
+ * max_blocks are read.  May be captured.  The pool's device must be the current one (else GK_ERR_INVALID). */
+gk_status gk_decode_kv4(gk_pool* pool, void* stream, int32_t layer, const gk_batch* batch, const gk_plan* plan,
+                        void* d_out);
 
 /* ---- one prompt step ------------------------------------------------------- */
 

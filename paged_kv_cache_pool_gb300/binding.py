@@ -93,9 +93,18 @@ class gk_prompt_plan_summary(ctypes.Structure):
                 ("scratch_bytes", c_i64)]
 
 
+class gk_qkv(ctypes.Structure):
+    _fields_ = [("num_tokens", c_i32), ("rot_dim", c_i32), ("interleaved", c_i32), ("eps", ctypes.c_float), ("num_positions", c_i64),
+                ("d_cos_sin", c_vp), ("d_positions", c_vp), ("d_q_weight", c_vp), ("d_k_weight", c_vp), ("d_q", c_vp), ("d_k", c_vp),
+                ("d_v", c_vp), ("d_q_out", c_vp), ("d_k_out", c_vp), ("q_stride", c_i64), ("k_stride", c_i64), ("v_stride", c_i64),
+                ("q_out_stride", c_i64), ("k_out_stride", c_i64)]
+
+
 P = ctypes.POINTER
 _SIGS = {
     "gk_pool_create": (c_i32, [P(gk_pool_config), P(c_vp)]),
+    "gk_pool_create_kv4": (c_i32, [P(gk_pool_config), P(c_vp)]),
+    "gk_kv4_row_bytes": (c_i64, [c_i32, c_i32]),
     "gk_pool_destroy": (None, [c_vp]),
     "gk_last_error": (ctypes.c_char_p, [c_vp]),
     "gk_status_string": (ctypes.c_char_p, [c_i32]),
@@ -118,6 +127,10 @@ _SIGS = {
     "gk_block_refcount": (c_i32, [c_vp, c_i32, P(c_i32)]),
     "gk_append_kv": (c_i32, [c_vp, c_vp, c_i32, c_i32, c_vp, c_vp, c_vp, c_i32, c_vp]),
     "gk_write_prefix_kv": (c_i32, [c_vp, c_vp, c_i32, c_i64, c_i64, c_i64, c_i64, c_vp, c_vp]),
+    "gk_qk_norm_rope": (c_i32, [c_vp, c_vp, P(gk_qkv)]),
+    "gk_append_qkv": (c_i32, [c_vp, c_vp, c_i32, P(gk_qkv), c_vp, c_i32, c_vp]),
+    "gk_read_kv": (c_i32, [c_vp, c_vp, c_i32, c_i64, c_vp, c_vp, c_vp, c_i64, c_i64]),
+    "gk_decode_kv4": (c_i32, [c_vp, c_vp, c_i32, P(gk_batch), c_vp, c_vp]),
     "gk_plan_build": (c_i32, [c_vp, P(gk_batch), c_vp, P(c_vp)]),
     "gk_plan_update": (c_i32, [c_vp, P(gk_batch), c_vp]),
     "gk_plan_destroy": (None, [c_vp]),
@@ -211,6 +224,26 @@ def gk_pool_create(num_layers, num_q_heads, num_kv_heads, head_dim, hot_tokens, 
     _check(lib().gk_pool_create(ctypes.byref(cfg), ctypes.byref(out)))
     _geometry[out.value] = (num_q_heads, num_kv_heads, head_dim)
     return out.value
+
+
+def gk_pool_create_kv4(num_layers, num_q_heads, num_kv_heads, head_dim, hot_tokens, cold_slots, cold_page_size, seed=0, hot_k=None,
+                       hot_v=None, cold=None):
+    """cold: uint8 [num_layers, cold_slots, gk_kv4_row_bytes(num_kv_heads, head_dim)] or its address."""
+    cfg = gk_pool_config(num_layers, num_q_heads, num_kv_heads, head_dim, hot_tokens, cold_slots, cold_page_size, 0, seed,
+                         _ptr(hot_k), _ptr(hot_v), _ptr(cold), None)
+    if cold is not None and not isinstance(cold, int):
+        row = gk_kv4_row_bytes(num_kv_heads, head_dim)
+        if cold.numel() * cold.element_size() < num_layers * cold_slots * row or not cold.is_contiguous():
+            raise ValueError(f"cold must be contiguous and hold {num_layers} layers of {cold_slots} rows of {row} bytes")
+    out = c_vp()
+    _check(lib().gk_pool_create_kv4(ctypes.byref(cfg), ctypes.byref(out)))
+    _geometry[out.value] = (num_q_heads, num_kv_heads, head_dim)
+    return out.value
+
+
+def gk_kv4_row_bytes(num_kv_heads, head_dim):
+    """Bytes of a 4-bit row of K and V (0: no pool has this geometry)."""
+    return lib().gk_kv4_row_bytes(num_kv_heads, head_dim)
 
 
 def gk_pool_destroy(pool):
@@ -408,6 +441,104 @@ def gk_write_prefix_kv(pool, stream, layer, hot_base, prefix_len, t0, d_k, d_v, 
            pool)
 
 
+# ---- from a layer's projections to its cache and attention -----------------------------
+def _gpu_row(x, n, dtype, what):
+    """As _row_of, of a tensor that is on the GPU."""
+    if x is not None and not isinstance(x, int) and not x.is_cuda:
+        raise ValueError(f"{what} must be on the GPU")
+    return _row_of(x, n, dtype, what)
+
+
+class Rope:
+    """How the queries and keys of a layer are normed and rotated: cos_sin fp32 [positions, rot_dim] (cosines, then sines),
+    bf16 weights [head_dim] or None (no norm).  Kept by the caller; the tensors stay alive with it."""
+
+    def __init__(self, cos_sin=None, rot_dim=None, interleaved=False, q_weight=None, k_weight=None, eps=1e-6):
+        import torch
+        self.torch = torch
+        if cos_sin is not None:
+            if cos_sin.dim() != 2 or cos_sin.dtype is not torch.float32 or not cos_sin.is_contiguous() or not cos_sin.is_cuda:
+                raise ValueError("cos_sin must be contiguous fp32 [positions, rot_dim] on the GPU")
+            if rot_dim is not None and rot_dim != cos_sin.shape[1]:
+                raise ValueError(f"cos_sin has rows of {cos_sin.shape[1]}, not of rot_dim {rot_dim}")
+            rot_dim = cos_sin.shape[1]
+        elif rot_dim:
+            raise ValueError("a rotation needs cos_sin")
+        self.dims = set()
+        for w in (q_weight, k_weight):
+            if w is None:
+                continue
+            if w.dim() != 1 or w.dtype is not torch.bfloat16 or not w.is_contiguous() or not w.is_cuda:
+                raise ValueError("a norm's weight must be contiguous bf16 [head_dim] on the GPU")
+            self.dims.add(w.shape[0])
+        self.tensors = cos_sin, q_weight, k_weight
+        self.rotates = bool(rot_dim)
+        self.c = gk_qkv(0, rot_dim or 0, int(bool(interleaved)), eps, 0 if cos_sin is None else cos_sin.shape[0], _ptr(cos_sin), None,
+                        _ptr(q_weight), _ptr(k_weight))
+        self.ref = ctypes.byref(self.c)
+
+    def set(self, pool, positions, q, k, v, q_out, k_out, n):
+        """Fill the call's rows in: bf16 [n, heads, d] tensors (tokens may be strided) or addresses of packed rows."""
+        c, torch = self.c, self.torch
+        hq, hkv, dim = _geometry.get(pool, (None, None, None))
+        if dim is not None and any(d != dim for d in self.dims):
+            raise ValueError(f"the norms' weights are of {self.dims} channels, the pool's heads of {dim}")
+        rows = []
+        for x, heads, what in ((q, hq, "q"), (q_out, hq, "q_out"), (k, hkv, "k"), (k_out, hkv, "k_out"), (v, hkv, "v")):
+            h, d, stride, at = _token_rows(x, n, what, torch)
+            if h is not None and heads is not None and (h != heads or d != dim):
+                raise ValueError(f"{what} must have the pool's {heads} heads of {dim}")
+            rows += [at, stride]
+        if self.rotates and positions is None and n:
+            raise ValueError("a rotation needs positions")
+        c.d_positions = _gpu_row(positions, n, torch.int32, "positions") if self.rotates else None
+        c.num_tokens = n
+        c.d_q, c.q_stride, c.d_q_out, c.q_out_stride, c.d_k, c.k_stride, c.d_k_out, c.k_out_stride, c.d_v, c.v_stride = rows
+        return self.ref
+
+
+def _tokens(*xs):
+    """The tokens of the first tensor."""
+    return next(x.shape[0] for x in xs if x is not None and not isinstance(x, int))
+
+
+def gk_qk_norm_rope(pool, stream, rope, positions, q, k, q_out=None, k_out=None, n=None):
+    """q [n, Hq, d] and k [n, Hkv, d] (either may be None), normed and rotated, to q_out and k_out (default: in place)."""
+    q_out, k_out = q if q_out is None else q_out, k if k_out is None else k_out
+    ref = rope.set(pool, positions, q, k, None, q_out, k_out, _tokens(q, k) if n is None else n)
+    st = lib().gk_qk_norm_rope(pool, _stream(stream), ref)
+    if st:
+        _check(st, pool)
+
+
+def gk_append_qkv(pool, stream, layer, rope, positions, d_slot_mapping, q, k, v, q_out=None, k_out=None, d_cow_pairs=None, n=None):
+    """As gk_qk_norm_rope, and K and V into the cache; q may be None, q_out defaults to in place, k_out to none."""
+    n = _tokens(k, d_slot_mapping) if n is None else n
+    ref = rope.set(pool, positions, q, k, v, q if q_out is None else q_out, k_out, n)
+    n_cow = 0 if d_cow_pairs is None else d_cow_pairs.numel() // 2
+    st = lib().gk_append_qkv(pool, _stream(stream), layer, ref, _gpu_row(d_slot_mapping, n, rope.torch.int64, "the slot mapping"), n_cow,
+                             _gpu_row(d_cow_pairs, 2 * n_cow, rope.torch.int32, "copy-on-write pairs") if n_cow else None)
+    if st:
+        _check(st, pool)
+
+
+def gk_read_kv(pool, stream, layer, d_slot_mapping, d_k, d_v, n=None):
+    """K and V of the slots as bf16 [n, Hkv, d] (tokens may be strided)."""
+    n = d_slot_mapping.numel() if n is None else n
+    torch = sys.modules.get("torch")
+    heads, dim = _geometry.get(pool, (None, None, None))[1:]
+    rows = []
+    for x, what in ((d_k, "k"), (d_v, "v")):
+        h, d, stride, at = _token_rows(x, n, what, torch)
+        if h is not None and heads is not None and (h != heads or d != dim):
+            raise ValueError(f"{what} must have the pool's {heads} heads of {dim}")
+        rows.append((at, stride))
+    slots = d_slot_mapping if isinstance(d_slot_mapping, int) else _gpu_row(d_slot_mapping, n, torch.int64, "the slot mapping")
+    st = lib().gk_read_kv(pool, _stream(stream), layer, n, slots, rows[0][0], rows[1][0], rows[0][1], rows[1][1])
+    if st:
+        _check(st, pool)
+
+
 class Batch:
     """Keeps the host arrays of a gk_batch alive; .set_layer() swaps the per-layer device pointers."""
 
@@ -474,6 +605,19 @@ def gk_decode_dense(pool, stream, layer, batch, plan):
 
 def gk_decode_cascade(pool, stream, layer, batch, plan):
     _check(lib().gk_decode_cascade(pool, _stream(stream), layer, ctypes.byref(batch.c), plan), pool)
+
+
+def gk_decode_kv4(pool, stream, layer, batch, plan, d_out):
+    """bf16 out [B, Hq, d] of a decode step over a 4-bit pool (the batch's q, lse and block table; its d_out is not used)."""
+    if not isinstance(d_out, int):
+        hq, _, d = _geometry.get(pool, (None, None, None))
+        shape = (batch.c.num_requests, d_out.shape[1] if hq is None else hq, d_out.shape[2] if d is None else d)
+        if d_out.shape != shape or d_out.dtype is not sys.modules["torch"].bfloat16 or not d_out.is_contiguous() or not d_out.is_cuda:
+            raise ValueError("out must be contiguous bf16 [%d, %d, %d] on the GPU" % shape)
+        d_out = d_out.data_ptr()
+    st = lib().gk_decode_kv4(pool, _stream(stream), layer, ctypes.byref(batch.c), plan, d_out)
+    if st:
+        _check(st, pool)
 
 
 def gk_decode_dense_static(pool, stream, layer, batch):

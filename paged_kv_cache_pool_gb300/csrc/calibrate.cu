@@ -286,6 +286,7 @@ using gk::Case;
 extern "C" gk_status gk_calibrate(gk_pool* pool, void* stream, const char* json_out) {
   if (!pool) return GK_ERR_INVALID;
   gk::Pool* p = &pool->impl;
+  if (p->kv4) return gk::fail(p, GK_ERR_UNSUPPORTED, "the cost model is of bf16 pools");
   if (!p->has_device) return gk::fail(p, GK_ERR_INVALID, "gk_calibrate needs a pool with device storage");
   gk_status st = gk::ensure_device(p);
   if (st != GK_OK) return st;
@@ -715,6 +716,7 @@ extern "C" gk_status gk_sm_speeds_measure(gk_pool* pool, void* stream, int32_t l
                                           const gk_plan* plan, int32_t reps, float* speeds) {
   if (!pool || !batch || !plan) return GK_ERR_INVALID;
   gk::Pool* p = &pool->impl;
+  if (p->kv4) return gk::fail(p, GK_ERR_UNSUPPORTED, "SM speeds are of the bf16 gather");
   if (reps < 1 || reps > 64) return gk::fail(p, GK_ERR_INVALID, "reps must be in 1 .. 64");
   gk_status st = gk::ensure_device(p);
   if (st != GK_OK) return st;

@@ -91,6 +91,7 @@ struct DeviceInfo {
 struct Pool {
   gk_pool_config cfg{};
   bool has_device = false;
+  bool kv4 = false;                  // COLD in 4-bit rows (cfg.cold_k; cfg.cold_v is null)
   HotAllocator hot;
   HotCache hot_cache;
   BlockManager cold;
@@ -186,6 +187,11 @@ struct Plan {
   // item and gather slot) planned for SM s; empty: CTA b takes slot b
   std::vector<int32_t> slot_of_sm;
   size_t off_slot_of_sm = 0;
+  // 4-bit pools: the longest suffix in blocks, whether any request needs the join,
+  // and the most partial states of one that does
+  int32_t suffix_blocks = 0;
+  bool kv4_join = false;
+  int32_t kv4_most_states = 0;
 };
 
 // host half of gk_plan_build: grouping, work lists and partial-state layout (no device work)
@@ -248,6 +254,18 @@ int launch_prefix_warp(const LaunchCommon& lc, void* stream, int32_t layer, cons
 // launch, on disjoint SMs (the merge follows as its own launch)
 int launch_cascade_split(const LaunchCommon& lc, void* stream, int32_t layer, const gk_batch* b,
                          const Plan* plan);
+// 4-bit rows: bytes of one, the copy of copy-on-write blocks, and the suffix gather's
+// CTAs per SM (no device query)
+int64_t kv4_row_bytes(int32_t hkv, int32_t d);
+int launch_kv4_cow_copy(const LaunchCommon& lc, void* stream, int32_t layer, int32_t n_cow, const int32_t* d_pairs);
+int kv4_ctas_per_sm(const gk_pool_config* cfg);
+int launch_kv4_gather(const LaunchCommon& lc, void* stream, int32_t layer, const gk_batch* b, const Plan* plan,
+                      void* d_out);
+int launch_kv4_join(const LaunchCommon& lc, void* stream, const gk_batch* b, const Plan* plan, void* d_out);
+// norms, rotation and cache writes of a layer's new tokens (slots null: no cache)
+int launch_qkv(const LaunchCommon& lc, void* stream, bool kv4, int32_t layer, const gk_qkv* x, const int64_t* d_slots);
+int launch_read_kv(const LaunchCommon& lc, void* stream, bool kv4, int32_t layer, int64_t n, const int64_t* d_slots,
+                   void* d_k, void* d_v, int64_t k_stride, int64_t v_stride);
 // resident gather CTAs per SM for the pool's geometry (no device query, so
 // host-only pools plan identically)
 int gather_ctas_per_sm(const gk_pool_config* cfg);

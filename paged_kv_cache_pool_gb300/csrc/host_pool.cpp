@@ -226,7 +226,7 @@ const char* gk_status_string(gk_status s) {
   return "unknown status";
 }
 
-gk_status gk_pool_create(const gk_pool_config* cfg, gk_pool** out) {
+static gk_status create_pool(const gk_pool_config* cfg, bool kv4, gk_pool** out) {
   if (!cfg || !out) return GK_ERR_INVALID;
   *out = nullptr;
   const gk_pool_config& c = *cfg;
@@ -241,10 +241,10 @@ gk_status gk_pool_create(const gk_pool_config* cfg, gk_pool** out) {
       c.cold_slots % c.cold_page_size != 0 || c.cold_slots > INT32_MAX)
     return GK_ERR_INVALID;
   bool any = c.hot_k || c.hot_v || c.cold_k || c.cold_v;
-  bool all = c.hot_k && c.hot_v && c.cold_k && c.cold_v;
+  bool all = c.hot_k && c.hot_v && c.cold_k && (kv4 ? !c.cold_v : c.cold_v != nullptr);
   if (any && !all) return GK_ERR_INVALID;
   if (all) {
-    for (void* ptr : {c.hot_k, c.hot_v, c.cold_k, c.cold_v})
+    for (void* ptr : {c.hot_k, c.hot_v, c.cold_k, c.cold_v})   // a 4-bit pool's cold_v is null
       if (((uintptr_t)ptr) % 256 != 0) return GK_ERR_INVALID;   // 16 B is the TMA floor; ask for 256
   }
   gk_pool* p = new (std::nothrow) gk_pool;
@@ -252,6 +252,7 @@ gk_status gk_pool_create(const gk_pool_config* cfg, gk_pool** out) {
   Pool& P = p->impl;
   P.cfg = c;
   P.has_device = all;
+  P.kv4 = kv4;
   P.hot.capacity = c.hot_tokens;
   P.cold.init(c.cold_slots / c.cold_page_size, c.cold_page_size, c.seed);
   // default cost model: nominal GB300 figures until a measured one is loaded
@@ -283,6 +284,15 @@ gk_status gk_pool_create(const gk_pool_config* cfg, gk_pool** out) {
   cm.split_tensor_us = 0.0;
   *out = p;
   return GK_OK;
+}
+
+gk_status gk_pool_create(const gk_pool_config* cfg, gk_pool** out) { return create_pool(cfg, false, out); }
+
+gk_status gk_pool_create_kv4(const gk_pool_config* cfg, gk_pool** out) { return create_pool(cfg, true, out); }
+
+int64_t gk_kv4_row_bytes(int32_t num_kv_heads, int32_t head_dim) {
+  if (num_kv_heads <= 0 || num_kv_heads > gk::kMaxKvHeads || (head_dim != 64 && head_dim != 128)) return 0;
+  return gk::kv4_row_bytes(num_kv_heads, head_dim);
 }
 
 void gk_pool_destroy(gk_pool* pool) {
@@ -566,10 +576,18 @@ gk_status gk_append_kv(gk_pool* pool, void* stream, int32_t layer, int32_t n, co
   if (st != GK_OK) return st;
   gk::LaunchCommon lc{&p->cfg, p->d_error, p->dev.num_sms};
   if (n_cow > 0) {
-    int e = gk::launch_cow_copy(lc, stream, layer, n_cow, d_cow_pairs);
+    int e = p->kv4 ? gk::launch_kv4_cow_copy(lc, stream, layer, n_cow, d_cow_pairs)
+                   : gk::launch_cow_copy(lc, stream, layer, n_cow, d_cow_pairs);
     if (e) return gk::cuda_fail(p, e, "copy-on-write kernel");
   }
-  if (n > 0) {
+  if (n > 0 && p->kv4) {
+    gk_qkv x{};
+    x.num_tokens = n;
+    x.d_k = d_k;
+    x.d_v = d_v;
+    int e = gk::launch_qkv(lc, stream, true, layer, &x, d_slot_mapping);
+    if (e) return gk::cuda_fail(p, e, "4-bit append kernel");
+  } else if (n > 0) {
     int e = gk::launch_scatter(lc, stream, layer, n, d_slot_mapping, d_k, d_v);
     if (e) return gk::cuda_fail(p, e, "reshape_and_cache kernel");
   }

@@ -405,7 +405,8 @@ gk_status build_host_plan_kind(Pool* p, const gk_batch* b, Plan* pl, gk_prefix_k
     };
     int32_t c_split = 0;
     double t_split = 1e300;
-    const bool can_split = G > 0 && suffix_tokens > 0 && p->cascade_mode != GK_CASCADE_SEQUENTIAL;
+    // (a 4-bit gather has a launch of its own)
+    const bool can_split = G > 0 && suffix_tokens > 0 && p->cascade_mode != GK_CASCADE_SEQUENTIAL && !p->kv4;
     if (can_split && p->cascade_mode == GK_CASCADE_SPLIT && p->cascade_tiles > 0) {
       const int32_t C = std::min(p->cascade_tiles, max_ntiles);
       if (n_split_items(C) <= num_sms) {
@@ -549,7 +550,7 @@ gk_status build_host_plan_kind(Pool* p, const gk_batch* b, Plan* pl, gk_prefix_k
     if (p->gather_partition == GK_PARTITION_PER_REQUEST)
       partition_per_request(n_suf, num_sms, &pl->suf_seg_begin, &pl->suf_segs);
     else
-      partition_tokens(n_suf, num_sms, &pl->suf_seg_begin, &pl->suf_segs);
+      partition_tokens(n_suf, (int64_t)num_sms * (p->kv4 ? kv4_ctas_per_sm(&c) : 1), &pl->suf_seg_begin, &pl->suf_segs);
   }
   if (p->gather_partition == GK_PARTITION_PER_REQUEST)
     partition_per_request(n_dense, max_ctas, &pl->dense_seg_begin, &pl->dense_segs);
@@ -570,12 +571,23 @@ gk_status build_host_plan_kind(Pool* p, const gk_batch* b, Plan* pl, gk_prefix_k
     RequestDev& rq = pl->reqs[(size_t)r];
     rq.entry_cas = e;
     rq.n_entry_cas = prefix_splits[(size_t)r] + nseg_suf[(size_t)r];
-    e += rq.n_entry_cas;
+    // 4-bit pools: a request that one segment covers writes its output directly
+    if (p->kv4 && prefix_splits[(size_t)r] == 0 && nseg_suf[(size_t)r] == 1) rq.n_entry_cas = -1;
+    e += std::max(0, rq.n_entry_cas);
   }
   pl->n_entries_cas = e;
   std::vector<int32_t> next((size_t)B);
   for (int32_t r = 0; r < B; ++r) next[(size_t)r] = pl->reqs[(size_t)r].entry_cas + prefix_splits[(size_t)r];
-  for (auto& sgm : pl->suf_segs) sgm.entry = next[(size_t)sgm.req]++;
+  for (auto& sgm : pl->suf_segs)
+    sgm.entry = pl->reqs[(size_t)sgm.req].n_entry_cas < 0 ? -1 : next[(size_t)sgm.req]++;
+  pl->suffix_blocks = 0;
+  pl->kv4_join = false;
+  pl->kv4_most_states = 0;
+  for (const RequestDev& rq : pl->reqs) {
+    pl->suffix_blocks = std::max(pl->suffix_blocks, (int32_t)((rq.slen + P - 1) / P));
+    if (p->kv4 && rq.n_entry_cas >= 0) pl->kv4_join = true;
+    pl->kv4_most_states = std::max(pl->kv4_most_states, rq.n_entry_cas);
+  }
   // dense: a request covered by one segment writes its output directly
   e = 0;
   pl->dense_needs_merge = false;
@@ -607,8 +619,10 @@ gk_status build_host_plan_kind(Pool* p, const gk_batch* b, Plan* pl, gk_prefix_k
   sm.dense_merge = pl->dense_needs_merge ? 1 : 0;
   sm.prefix_bytes = pre_bytes;
   sm.prefix_flops = pre_flops;
-  sm.suffix_bytes = suf_tokens * 2 * Hkv * d * 2;
-  sm.dense_bytes = dense_tokens * 2 * Hkv * d * 2;
+  // 4-bit rows: 4.5 bits an element
+  const int64_t cold_token = p->kv4 ? (int64_t)Hkv * (d + d / 8) : 2LL * Hkv * d * 2;
+  sm.suffix_bytes = suf_tokens * cold_token;
+  sm.dense_bytes = (dense_tokens - suf_tokens) * 2 * Hkv * d * 2 + suf_tokens * cold_token;
   sm.cascade_split = pl->split ? 1 : 0;
   sm.prefix_tiles_per_item = 0;
   for (int32_t gi = 0; gi < G; ++gi) sm.prefix_tiles_per_item = std::max(sm.prefix_tiles_per_item, std::min(best_c, ntiles[(size_t)gi]));
@@ -660,6 +674,9 @@ gk_status build_host_plan(Pool* p, const gk_batch* b, Plan* pl) {
     pl->split = w.split;
     pl->prefix_kind = w.prefix_kind;
     pl->slot_of_sm.swap(w.slot_of_sm);
+    pl->suffix_blocks = w.suffix_blocks;
+    pl->kv4_join = w.kv4_join;
+    pl->kv4_most_states = w.kv4_most_states;
   }
   return GK_OK;
 }
@@ -938,6 +955,8 @@ gk_status gk_plan_segments(const gk_plan* plan, int32_t dense, int32_t* n_ctas, 
 gk_status gk_dispatch(const gk_pool* pool, const gk_plan* plan, gk_backend* choice, double* t_dense_us,
                       double* t_cascade_us) {
   if (!pool || !plan || !choice) return GK_ERR_INVALID;
+  if (pool->impl.kv4)
+    return gk::fail(const_cast<Pool*>(&pool->impl), GK_ERR_UNSUPPORTED, "a 4-bit pool has one backend (gk_decode_kv4)");
   double t_flat, t_cas;
   gk::predict_plan(pool->impl.cost, pool->impl.dev.num_sms, pool->impl.cfg.num_q_heads, plan->impl, &t_flat, &t_cas);
   *choice = t_flat < t_cas ? GK_BACKEND_DENSE : GK_BACKEND_CASCADE;
@@ -1074,6 +1093,7 @@ gk_status gk_cost_model_load(gk_pool* pool, const char* json) {
 }
 
 static gk_status check_decode(Pool* p, int32_t layer, const gk_batch* b, const Plan* pl) {
+  if (p->kv4) return gk::fail(p, GK_ERR_UNSUPPORTED, "a 4-bit pool decodes by gk_decode_kv4");
   if (layer < 0 || layer >= p->cfg.num_layers) return gk::fail(p, GK_ERR_INVALID, "layer out of range");
   if (pl->pool != p) return gk::fail(p, GK_ERR_INVALID, "plan belongs to another pool");
   if (!pl->uploaded) return gk::fail(p, GK_ERR_INVALID, "plan has no device tables");

@@ -97,6 +97,8 @@ gk_status build_host(Pool* p, const gk_prompt_batch* b, PromptPlan* pl) {
     rq.n = b->new_len[r];
     rq.ctx = b->context_len ? b->context_len[r] : 0;
     if (rq.n < 0 || rq.ctx < 0) return fail(p, GK_ERR_INVALID, "negative length");
+    if (p->kv4 && rq.ctx > 0)
+      return fail(p, GK_ERR_UNSUPPORTED, "prompts do not attend 4-bit COLD tokens: read them into a HOT prefix (gk_read_kv)");
     if ((int64_t)rq.ctx > (int64_t)b->max_blocks * c.cold_page_size)
       return fail(p, GK_ERR_INVALID, "context longer than the block-table row");
     if (base < 0) {

@@ -62,6 +62,7 @@ using gk::Pool;
 extern "C" gk_status gk_decode_dense_static(gk_pool* pool, void* stream, int32_t layer, const gk_batch* batch) {
   if (!pool || !batch) return GK_ERR_INVALID;
   Pool* p = &pool->impl;
+  if (p->kv4) return gk::fail(p, GK_ERR_UNSUPPORTED, "a 4-bit pool decodes by gk_decode_kv4");
   if (!p->has_device) return gk::fail(p, GK_ERR_INVALID, "pool has no device storage");
   if (layer < 0 || layer >= p->cfg.num_layers) return gk::fail(p, GK_ERR_INVALID, "layer out of range");
   if (batch->num_requests > 0 && (!batch->d_q || !batch->d_out || !batch->d_block_table))

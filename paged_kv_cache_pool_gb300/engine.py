@@ -16,6 +16,11 @@ and of a prompt step (the new tokens of prompts, turns or chunks):
   -> prompt_batch, prompt_plan (gk_prompt_plan_build / _update)
   -> per layer: append_kv, prompt (gk_prompt_attn).
 
+append_qkv stands in append_kv's place where the layer's queries and keys are not
+normed and rotated yet.  With kv_bits=4 the COLD cache holds 4-bit rows; the decode
+step is then append_slots -> append_qkv (or append_kv) -> plan -> decode_kv4, and
+read_kv gives tokens back as bf16, for a HOT prefix or the prompt step behind them.
+
 Every method is one library call; the work is in libgk.
 """
 from __future__ import annotations
@@ -26,7 +31,7 @@ from . import binding as gk
 
 
 class Engine:
-    def __init__(self, L, Hq, Hkv, d, hot_tokens, cold_slots, page_size, seed=0, device="cuda"):
+    def __init__(self, L, Hq, Hkv, d, hot_tokens, cold_slots, page_size, seed=0, device="cuda", kv_bits=16):
         import torch
         self.torch = torch
         self.L, self.Hq, self.Hkv, self.d = L, Hq, Hkv, d
@@ -36,10 +41,17 @@ class Engine:
         bf = torch.bfloat16
         self.hot_k = torch.empty(max(1, hot_tokens) * L * Hkv * d, dtype=bf, device=self.device)
         self.hot_v = torch.empty_like(self.hot_k)
-        self.cold_k = torch.empty((L, cold_slots, Hkv, d), dtype=bf, device=self.device)
-        self.cold_v = torch.empty_like(self.cold_k)
-        self.pool = gk.gk_pool_create(L, Hq, Hkv, d, hot_tokens, cold_slots, page_size, seed,
-                                      self.hot_k, self.hot_v, self.cold_k, self.cold_v)
+        if kv_bits not in (4, 16):
+            raise ValueError("kv_bits must be 16 (bf16) or 4")
+        self.kv_bits = kv_bits
+        if kv_bits == 4:
+            self.cold = torch.empty((L, cold_slots, gk.gk_kv4_row_bytes(Hkv, d)), dtype=torch.uint8, device=self.device)
+            self.pool = gk.gk_pool_create_kv4(L, Hq, Hkv, d, hot_tokens, cold_slots, page_size, seed, self.hot_k, self.hot_v, self.cold)
+        else:
+            self.cold_k = torch.empty((L, cold_slots, Hkv, d), dtype=bf, device=self.device)
+            self.cold_v = torch.empty_like(self.cold_k)
+            self.pool = gk.gk_pool_create(L, Hq, Hkv, d, hot_tokens, cold_slots, page_size, seed,
+                                          self.hot_k, self.hot_v, self.cold_k, self.cold_v)
         self._plans = []
         self._prompt_plans = []
 
@@ -86,6 +98,34 @@ class Engine:
 
     def append_kv(self, layer, d_slots, k, v, d_cow=None, stream=None):
         gk.gk_append_kv(self.pool, stream, layer, d_slots, k, v, d_cow)
+
+    # ---- from a layer's projections to its cache ------------------------------------------
+    def rope_table(self, positions, rot_dim=None, base=10000.0, inv_freq=None):
+        """fp32 [positions, rot_dim] cosines, then sines, of the angles position * inv_freq (default base^(-2 i / rot_dim)); angles
+        in 64 bits, of which a far position needs every one that 32 would drop."""
+        torch, r = self.torch, self.d if rot_dim is None else rot_dim
+        f64 = dict(dtype=torch.float64, device=self.device)
+        if inv_freq is None:
+            inv_freq = base ** (-2 * torch.arange(r // 2, **f64) / r)
+        angle = torch.arange(positions, **f64)[:, None] * torch.as_tensor(inv_freq, **f64)
+        return torch.cat([angle.cos(), angle.sin()], 1).float()
+
+    def rope(self, cos_sin=None, interleaved=False, q_weight=None, k_weight=None, eps=1e-6):
+        return gk.Rope(cos_sin, None, interleaved, q_weight, k_weight, eps)
+
+    def qk_norm_rope(self, rope, positions, q, k, q_out=None, k_out=None, stream=None):
+        """q [n, Hq, d] and k [n, Hkv, d] normed and rotated (in place by default)."""
+        gk.gk_qk_norm_rope(self.pool, stream, rope, positions, q, k, q_out, k_out)
+
+    def append_qkv(self, layer, rope, positions, d_slots, q, k, v, q_out=None, k_out=None, d_cow=None, stream=None):
+        gk.gk_append_qkv(self.pool, stream, layer, rope, positions, d_slots, q, k, v, q_out, k_out, d_cow)
+
+    def read_kv(self, layer, d_slots, k=None, v=None, stream=None):
+        """-> (K, V) bf16 [n, Hkv, d] of the COLD slots."""
+        shape = dict(size=(d_slots.numel(), self.Hkv, self.d), dtype=self.torch.bfloat16, device=self.device)
+        k, v = (self.torch.empty(**shape) if x is None else x for x in (k, v))
+        gk.gk_read_kv(self.pool, stream, layer, d_slots, k, v)
+        return k, v
 
     def block_tables(self, seqs, max_blocks=None, out=None, lens=None):
         if max_blocks is None:
@@ -138,6 +178,10 @@ class Engine:
             gk.gk_decode_dense(self.pool, stream, layer, batch, plan)
         else:
             gk.gk_decode_cascade(self.pool, stream, layer, batch, plan)
+
+    def decode_kv4(self, layer, batch, plan, out, stream=None):
+        """out bf16 [B, Hq, d] of the batch's queries over a 4-bit COLD cache (and the HOT prefixes)."""
+        gk.gk_decode_kv4(self.pool, stream, layer, batch, plan, out)
 
     # ---- prompt step --------------------------------------------------------------------
     def prompt_batch(self, new_lens, prefix_bases=None, prefix_lens=None, context_lens=None, d_table=None, max_blocks=0):
