@@ -3,7 +3,15 @@
 //
 // With k_c = lo + code_c * (span / 15) in each group of 64 channels,
 //   q . k = sum_groups span / 15 * (q_g . code_g) + lo * sum(q_g)
-//   sum_j p_j v_j = sum_j (p_j span_j / 15) code_j + sum_j p_j lo_j   in each group's channels.
+//   sum_j p_j v_j = sum_j (p_j span_j / 15) code_j + sum_j p_j lo_j   in each group's channels,
+// so the two products run on codes alone and a token's scales meet its score and its weight.
+//
+// What bounds it: 4.5 bits an element, (d + d / 8) bytes a token and KV head, from HBM; 4 g d operations
+// for them on the warp-level tensor cores.  At HBM speed an SM has about 800 instruction slots for 32 tokens of
+// one head (d = 128), so the instructions a token costs decide how near the gather comes.  Codes become
+// operands by one logic instruction a pair: the pair (code & 0x000f000f) read as fp16 is the subnormal pair
+// code * 2^-24, and (code & 0x00f000f0) is 16 * code * 2^-24, both exact, and the tensor core multiplies
+// subnormals exactly.  The factor 16 goes into the query's fragment, and into the output for V.
 #include <cmath>
 
 #include "device_common.cuh"
@@ -14,10 +22,14 @@
 namespace gk {
 namespace {
 
+constexpr int kTok = 32;       // tokens of a stage
+constexpr int kSmWarps = 16;   // warps of an SM: 128 registers a thread
+constexpr size_t kSmSmem = 228 * 1024;  // shared memory of an SM, 1 KB of it taken by each resident CTA
+
 struct Kv4Params {
   const uint8_t* rows;        // the layer's
   int64_t num_blocks;
-  int32_t page;
+  int32_t page, page_shift;   // log2(page), or -1
   int32_t Hkv, Hq;
   const int32_t* table;
   int32_t max_blocks;
@@ -32,132 +44,514 @@ struct Kv4Params {
   int32_t* err;
 };
 
-// Warp h of a CTA is KV head h; it takes the CTA's segments one by one, each query
-// head over the segment's tokens, 32 at a time: a thread scores a token, then the
-// warp adds the tokens' values, D / 32 channels a thread.
-template <int D>
-__global__ void __launch_bounds__(32 * kMaxKvHeads) kv4_gather_kernel(const Kv4Params p) {
-  constexpr int C = D / 32, W = D / 8;
-  __shared__ float qs[kMaxKvHeads][D];
+// a stage of one warp: K codes, V codes, scales of kTok tokens
+__host__ __device__ constexpr int stage_bytes(int d) { return kTok * (d + d / 8); }
+__host__ __device__ constexpr int stages(int d) { return d == 128 ? 3 : 4; }
+
+// D (16x8, fp32) += A (16x16, row) . B (16x8, col), fp16
+__device__ __forceinline__ void mma_f16(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+// BYTES from global to shared memory, zeros where !live
+template <int BYTES>
+__device__ __forceinline__ void copy_or_zero(uint32_t dst, const void* src, bool live) {
+  const int n = live ? BYTES : 0;
+  if (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+// 2^e as fp32, -126 <= e <= 127
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+// floor(log2 x) of a normal x >= 0; -127 for 0
+__device__ __forceinline__ int exponent(float x) { return (int)(__float_as_uint(x) >> 23) - 127; }
+
+constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
+
+// Warp h of a CTA is KV head h and its G query heads, and moves its own data: it copies its head's codes and
+// scales of 32 tokens a stage with cp.async into a private ring, stages(D) - 1 ahead of its compute, so no
+// warp waits for another; 16 warps share an SM.  Block ids are loaded a stage before its copies.
+//
+// A stage is two tiles of 16 tokens.  S^T[16 tok x 8] = K . Q^T: a thread's 16 bytes of a token's K row are the
+// A fragments of all eight k16 steps (the row's order, kv4.cuh, is made for that).  Rows r = 0 .. 7 of a
+// tile are tokens (r >> 1) + 4 (r & 1) of its half, which lets the V loads below go without bank conflicts.
+// O^T[d x 8] += V^T . P^T: a thread's 8 bytes of each of four tokens, paired by two byte permutes, are the A fragments
+// of all m16 tiles; P^T is the weights of both heads a thread scored, times the token's span, through movmatrix.
+template <int D, int G>
+__global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_gather_kernel(const Kv4Params p) {
+  constexpr int NG = D / 64;         // groups
+  constexpr int KW = D / 32;         // words of K a thread takes of a token
+  constexpr int MT = D / 16;         // m16 tiles of O^T
+  constexpr int NST = stages(D);
+  constexpr int CPT = D / 16;        // 16-byte chunks of a token's codes (K and V)
+  constexpr int TPI = 32 / CPT;      // tokens a copy instruction of the warp covers
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int lane = threadIdx.x & 31, h = threadIdx.x >> 5;
+  const int gq = lane >> 2, tq = lane & 3;
+  const int sg1 = p.seg_begin[blockIdx.x + 1];
+  int sg = p.seg_begin[blockIdx.x];
   griddep_launch_dependents();
   griddep_wait();
-  const int lane = threadIdx.x & 31, h = threadIdx.x >> 5, g = p.Hq / p.Hkv;
-  const int64_t row_bytes = kv4::row_bytes(p.Hkv, D);
-  for (int sg = p.seg_begin[blockIdx.x]; sg < p.seg_begin[blockIdx.x + 1]; ++sg) {
+  const uint32_t ring = smem_u32(smem) + (uint32_t)(h * NST * stage_bytes(D));
+  const int row_bytes = kv4::row_bytes(p.Hkv, D);
+  const uint8_t* const codes = p.rows + kv4::codes_at(h, D) + (lane % CPT) * 16;
+  const uint8_t* const scales = p.rows + kv4::scales_at(p.Hkv, h, D);
+
+  // ---- copies ----
+  // where this thread's chunk of the tokens it copies lands: token T's K row at place T ^ bit 2 of T (d = 128; at d = 64
+  // T ^ 2 * bit 2), its V row at T with the halves swapped by bit 1 (d = 128), for conflict-free loads
+  uint32_t dst0, dst1;
+  {
+    const int t = lane / CPT, c = lane % CPT;
+    if (c < CPT / 2) {
+      if (D == 128) {                // t = 0 .. 3; a step adds 4, which flips bit 2
+        dst0 = t * 64 + c * 16;
+        dst1 = (t ^ 1) * 64 + c * 16;
+      } else {                       // t = 0 .. 7; a step adds 8
+        dst0 = dst1 = (t ^ ((t >> 2 & 1) << 1)) * 32 + c * 16;
+      }
+    } else {
+      const int cv = c - CPT / 2;
+      dst0 = dst1 = kTok * (D / 2) + (D == 128 ? t * 64 + (cv ^ ((t >> 1 & 1) << 1)) * 16 : t * 32 + cv * 16);
+    }
+  }
+  int lsg = sg, lt = 0, lt1 = 0;     // the look-up's segment and tokens
+  const int32_t* ltab = nullptr;
+  auto look_at = [&]() {
+    if (lsg < sg1) {
+      const SegmentDev sd = p.segs[lsg];
+      lt = sd.t0;
+      lt1 = sd.t1;
+      ltab = p.table + (int64_t)sd.req * p.max_blocks;
+    }
+  };
+  int32_t id = 0, in_page = 0;
+  int idn = 0;                       // tokens of the stage looked up
+  auto lookup = [&]() {
+    idn = 0;
+    if (lsg < sg1) {
+      idn = min(kTok, lt1 - lt);
+      const int t = lt + lane;
+      const int b = p.page_shift >= 0 ? t >> p.page_shift : t / p.page;
+      in_page = t - b * p.page;
+      if (lane < idn) id = __ldg(ltab + b);
+      lt += idn;
+      if (lt == lt1) {
+        ++lsg;
+        look_at();
+      }
+    }
+  };
+  int islot = 0;
+  auto issue = [&]() {
+    if (idn > 0) {
+      int32_t slot = -1;
+      if (lane < idn) {
+        if (id >= 0 && id < p.num_blocks)
+          slot = id * p.page + in_page;
+        else
+          report_error(p.err, kErrBounds);
+      }
+      const uint32_t st = ring + (uint32_t)islot * stage_bytes(D);
+#pragma unroll
+      for (int j = 0; j < kTok / TPI; ++j) {
+        const int32_t s = __shfl_sync(0xffffffffu, slot, j * TPI + lane / CPT);
+        copy_or_zero<16>(st + (j & 1 ? dst1 : dst0) + j * TPI * (D / 2), codes + (int64_t)max(s, 0) * row_bytes, s >= 0);
+      }
+      copy_or_zero<D / 8>(st + kTok * D + lane * (D / 8), scales + (int64_t)max(slot, 0) * row_bytes, slot >= 0);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    if (++islot == NST) islot = 0;
+  };
+  look_at();
+  lookup();
+#pragma unroll
+  for (int i = 0; i < NST - 1; ++i) {
+    issue();
+    lookup();
+  }
+
+  // ---- compute ----
+  const int ta = (gq >> 1) + 4 * (gq & 1);                 // this thread's row of a half tile, as a token
+  const uint32_t k_at = D == 128 ? (uint32_t)((ta ^ (gq & 1)) * 64 + tq * 16) : (uint32_t)((ta ^ ((gq & 1) << 1)) * 32 + tq * 8);
+  const uint32_t v_at = kTok * (D / 2) +
+                        (D == 128 ? tq * 64 + ((gq >> 1) ^ ((tq >> 1) << 1)) * 16 + (gq & 1) * 8 : tq * 32 + gq * 4);
+  const uint32_t s_at = kTok * D + ta * (D / 8);
+  int cslot = 0;
+  for (; sg < sg1; ++sg) {
     const SegmentDev seg = p.segs[sg];
-    for (int qi = 0; qi < g; ++qi) {
-      const int qh = h * g + qi;
-      const uint16_t* qrow = p.q + ((int64_t)seg.req * p.Hq + qh) * D;
-      __syncwarp();
-      float sum[D / 64] = {};
-      for (int c = lane; c < D; c += 32) {
-        const float x = __uint_as_float((uint32_t)qrow[c] << 16);
-        qs[h][c] = x;
-        sum[c / 64] += x;
+    // Q as B fragments: word i of a thread's K is channels ch .. ch + 7, paired (c, c + 4); scaled by a power of two
+    // to between 2^13 and 2^14, so that fp16 holds a row's bf16 values to 2^-38 of the largest
+    uint32_t qf[KW][4];
+    float F[2], Z[NG][2];
+    {
+      float x[KW][8], top = 0.f, sum[NG] = {};
+#pragma unroll
+      for (int i = 0; i < KW; ++i) {
+        const int w = KW * tq + i, ch = D == 128 ? 8 * (w >> 1) + 64 * (w & 1) : 8 * w;
+        uint4 r = make_uint4(0, 0, 0, 0);
+        if (gq < G) r = *reinterpret_cast<const uint4*>(p.q + ((int64_t)seg.req * p.Hq + h * G + gq) * D + ch);
+        x[i][0] = bf_lo(r.x); x[i][1] = bf_hi(r.x); x[i][2] = bf_lo(r.y); x[i][3] = bf_hi(r.y);
+        x[i][4] = bf_lo(r.z); x[i][5] = bf_hi(r.z); x[i][6] = bf_lo(r.w); x[i][7] = bf_hi(r.w);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          top = fmaxf(top, fabsf(x[i][c]));
+          sum[D == 128 ? i & 1 : 0] += x[i][c];
+        }
       }
 #pragma unroll
-      for (int gr = 0; gr < D / 64; ++gr)
+      for (int off = 1; off < 4; off <<= 1) {
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
 #pragma unroll
-        for (int off = 16; off >= 1; off >>= 1) sum[gr] += __shfl_xor_sync(0xffffffffu, sum[gr], off);
+        for (int g = 0; g < NG; ++g) sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], off);
+      }
+      const int e = min(120, 13 - exponent(top));
+      const float s = pow2(e), s16 = pow2(e - 4);
+#pragma unroll
+      for (int i = 0; i < KW; ++i) {
+        qf[i][0] = pack_f16x2(x[i][0] * s, x[i][4] * s);
+        qf[i][1] = pack_f16x2(x[i][1] * s16, x[i][5] * s16);
+        qf[i][2] = pack_f16x2(x[i][2] * s, x[i][6] * s);
+        qf[i][3] = pack_f16x2(x[i][3] * s16, x[i][7] * s16);
+      }
+      const float f = p.scale * (16777216.f / 15.f) * pow2(-e);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {    // of query heads 2 tq and 2 tq + 1
+        F[k] = __shfl_sync(0xffffffffu, f, 4 * (2 * tq + k));
+#pragma unroll
+        for (int g = 0; g < NG; ++g) Z[g][k] = __shfl_sync(0xffffffffu, sum[g], 4 * (2 * tq + k)) * p.scale;
+      }
+    }
+    float o[MT][4], R[NG][2] = {}, m[2] = {-INFINITY, -INFINITY}, l[2] = {};
+#pragma unroll
+    for (int i = 0; i < MT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    float vs = 0.f;                    // spans of V are scaled by this power of two (0: not chosen yet)
+
+    for (int t = seg.t0; t < seg.t1; t += kTok) {
+      const int n = min(kTok, seg.t1 - t);
+      issue();
+      lookup();
+      asm volatile("cp.async.wait_group %0;" ::"n"(NST - 1) : "memory");
       __syncwarp();
-      float m = -INFINITY, l = 0.f, o[C] = {};
-      for (int t = seg.t0; t < seg.t1; t += 32) {
-        const bool live = t + lane < seg.t1;
-        int64_t slot = -1;
-        if (live) {
-          const int32_t b = p.table[(int64_t)seg.req * p.max_blocks + (t + lane) / p.page];
-          if (b >= 0 && b < p.num_blocks)
-            slot = (int64_t)b * p.page + (t + lane) % p.page;
-          else
-            report_error(p.err, kErrBounds);
+      const uint32_t st = ring + (uint32_t)cslot * stage_bytes(D);
+      if (++cslot == NST) cslot = 0;
+      // scores
+      float sc[2][4];                  // rows ta and ta + 8 of each tile, heads 2 tq and 2 tq + 1
+      uint32_t vscale[2][2][NG];       // V's (lo, span) of those tokens
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        uint32_t wa[KW], wb[KW], ka[NG], kb[NG];
+        const uint32_t kt = st + k_at + u * 16 * (D / 2);
+        if (D == 128) {
+          const uint4 a = lds128(kt), b = lds128(kt + 8 * (D / 2));
+          wa[0] = a.x; wa[1] = a.y; wa[KW - 2] = a.z; wa[KW - 1] = a.w;
+          wb[0] = b.x; wb[1] = b.y; wb[KW - 2] = b.z; wb[KW - 1] = b.w;
+        } else {
+          const uint2 a = lds64(kt), b = lds64(kt + 8 * (D / 2));
+          wa[0] = a.x; wa[1] = a.y;
+          wb[0] = b.x; wb[1] = b.y;
         }
-        const uint8_t* row = p.rows + slot * row_bytes;
-        float s = live ? 0.f : -INFINITY;
-        if (slot >= 0) {
-          const uint32_t* codes = reinterpret_cast<const uint32_t*>(row + kv4::codes_at(h, D));
-          const uint32_t* sc = reinterpret_cast<const uint32_t*>(row + kv4::scales_at(p.Hkv, h, D));
-          float dot[D / 64] = {};
-          for (int w = 0; w < W; ++w) {
-            const uint32_t x = codes[w];
-            const int gr = D == 64 ? 0 : w & 1, c0 = D == 64 ? 8 * w : 8 * (w >> 1) + 64 * gr;
-            for (int i = 0; i < 8; ++i) dot[gr] = fmaf((float)((x >> (4 * i)) & 15u), qs[h][c0 + i], dot[gr]);
+        const uint32_t at = st + s_at + u * 16 * (D / 8);
+        if (D == 128) {
+          const uint4 a = lds128(at), b = lds128(at + 8 * (D / 8));
+          ka[0] = a.x; ka[NG - 1] = a.y; vscale[u][0][0] = a.z; vscale[u][0][NG - 1] = a.w;
+          kb[0] = b.x; kb[NG - 1] = b.y; vscale[u][1][0] = b.z; vscale[u][1][NG - 1] = b.w;
+        } else {
+          const uint2 a = lds64(at), b = lds64(at + 8 * (D / 8));
+          ka[0] = a.x; vscale[u][0][0] = a.y;
+          kb[0] = b.x; vscale[u][1][0] = b.y;
+        }
+        float acc[NG][4] = {};
+#pragma unroll
+        for (int i = 0; i < KW; ++i) {
+          float* d = acc[D == 128 ? i & 1 : 0];
+          mma_f16(d, wa[i] & kLow, wb[i] & kLow, wa[i] & kHigh, wb[i] & kHigh, qf[i][0], qf[i][1]);
+          const uint32_t xa = wa[i] >> 8, xb = wb[i] >> 8;
+          mma_f16(d, xa & kLow, xb & kLow, xa & kHigh, xb & kHigh, qf[i][2], qf[i][3]);
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float da = 0.f, db = 0.f, za = 0.f, zb = 0.f;
+#pragma unroll
+          for (int g = 0; g < NG; ++g) {
+            da = fmaf(bf_hi(ka[g]), acc[g][k], da);
+            db = fmaf(bf_hi(kb[g]), acc[g][2 + k], db);
+            za = fmaf(bf_lo(ka[g]), Z[g][k], za);
+            zb = fmaf(bf_lo(kb[g]), Z[g][k], zb);
           }
-#pragma unroll
-          for (int gr = 0; gr < D / 64; ++gr)
-            s += fmaf(bf_hi(sc[gr]) * (1.f / 15.f), dot[gr], bf_lo(sc[gr]) * sum[gr]);
-          s *= p.scale;
-        }
-        float mx = s;
-#pragma unroll
-        for (int off = 16; off >= 1; off >>= 1) mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-        const float mn = max_nan(m, mx);
-        const float a = ex2(m - mn), pr = ex2(s - mn);
-        m = mn;
-        float ps = pr;
-#pragma unroll
-        for (int off = 16; off >= 1; off >>= 1) ps += __shfl_xor_sync(0xffffffffu, ps, off);
-        l = l * a + ps;
-#pragma unroll
-        for (int c = 0; c < C; ++c) o[c] *= a;
-        for (int u = 0; u < 32 && t + u < seg.t1; ++u) {
-          const float pu = __shfl_sync(0xffffffffu, pr, u);
-          const int64_t su = __shfl_sync(0xffffffffu, slot, u);
-          if (su < 0) continue;
-          const uint8_t* ru = p.rows + su * row_bytes;
-          const int w = lane * C / 8;
-          const uint32_t x = reinterpret_cast<const uint32_t*>(ru + kv4::codes_at(h, D) + D / 2)[w];
-          const uint32_t sc = reinterpret_cast<const uint32_t*>(ru + kv4::scales_at(p.Hkv, h, D) + D / 16)[D == 64 ? 0 : w & 1];
-#pragma unroll
-          for (int c = 0; c < C; ++c)
-            o[c] = fmaf(pu, fmaf((float)((x >> (4 * (lane * C % 8 + c))) & 15u), bf_hi(sc) * (1.f / 15.f), bf_lo(sc)), o[c]);
+          sc[u][k] = fmaf(da, F[k], za);
+          sc[u][2 + k] = fmaf(db, F[k], zb);
         }
       }
-      const float inv = 1.f / l;
-      const int w = lane * C / 8, ch = (D == 64 ? 8 * w : 8 * (w >> 1) + 64 * (w & 1)) + lane * C % 8;
-      if (seg.entry >= 0) {
-        const int64_t r = (int64_t)seg.entry * p.Hq + qh;
-        for (int c = 0; c < C; ++c) p.part_o[r * D + ch + c] = o[c] * inv;
-        if (lane == 0) p.part_l[r] = m + __log2f(l);
-      } else {
-        const int64_t r = (int64_t)seg.req * p.Hq + qh;
-        for (int c = 0; c < C; c += 2)
-          *reinterpret_cast<uint32_t*>(p.out + r * D + ch + c) = pack_bf16x2(o[c] * inv, o[c + 1] * inv);
-        if (lane == 0 && p.lse) p.lse[r] = (m + __log2f(l)) * kLn2;
+      if (n < kTok) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+            if (16 * u + 8 * r + ta >= n) sc[u][2 * r] = sc[u][2 * r + 1] = -INFINITY;
+      }
+      // running maximum; weights
+      float x0 = fmaxf(fmaxf(sc[0][0], sc[0][2]), fmaxf(sc[1][0], sc[1][2]));
+      float x1 = fmaxf(fmaxf(sc[0][1], sc[0][3]), fmaxf(sc[1][1], sc[1][3]));
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) {
+        x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, off));
+        x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, off));
+      }
+      x0 = fmaxf(m[0], x0);
+      x1 = fmaxf(m[1], x1);
+      // the largest span of V this thread sees, in the current scale
+      float top = 0.f;
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int g = 0; g < NG; ++g) top = fmaxf(top, bf_hi(vscale[u][r][g]));
+      const bool grow = vs == 0.f || top * vs >= 32768.f;
+      if (__any_sync(0xffffffffu, x0 != m[0] || x1 != m[1] || grow)) {
+        float a0 = ex2(m[0] - x0), a1 = ex2(m[1] - x1);
+        if (x0 == m[0]) a0 = 1.f;      // -inf - -inf
+        if (x1 == m[1]) a1 = 1.f;
+        l[0] *= a0;
+        l[1] *= a1;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          R[g][0] *= a0;
+          R[g][1] *= a1;
+        }
+        if (__any_sync(0xffffffffu, grow)) {
+          // a scale that puts the stage's largest span between 2^13 and 2^14
+#pragma unroll
+          for (int off = 1; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+          const float to = pow2(min(113, 13 - exponent(top)));
+          if (vs != 0.f) {
+            a0 *= to / vs;
+            a1 *= to / vs;
+          }
+          vs = to;
+        }
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          o[i][0] *= a0; o[i][1] *= a1; o[i][2] *= a0; o[i][3] *= a1;
+        }
+        m[0] = x0;
+        m[1] = x1;
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        uint32_t b[NG][2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float p0 = ex2(sc[u][2 * r] - m[0]), p1 = ex2(sc[u][2 * r + 1] - m[1]);
+          l[0] += p0;
+          l[1] += p1;
+#pragma unroll
+          for (int g = 0; g < NG; ++g) {
+            const float span = bf_hi(vscale[u][r][g]) * vs, lo = bf_lo(vscale[u][r][g]);
+            R[g][0] = fmaf(p0, lo, R[g][0]);
+            R[g][1] = fmaf(p1, lo, R[g][1]);
+            b[g][r] = transpose8x8(pack_f16x2(p0 * span, p1 * span));
+          }
+        }
+        // tokens tq, tq + 4, tq + 8, tq + 12 of the tile
+        uint32_t w[4][NG];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t at = st + v_at + (u * 16 + 4 * k) * (D / 2);
+          if (D == 128) {
+            const uint2 x = lds64(at);
+            w[k][0] = x.x;
+            w[k][NG - 1] = x.y;
+          } else {
+            w[k][0] = lds32(at);
+          }
+        }
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {      // channels 0 .. 3, then 4 .. 7
+            const uint32_t x = __byte_perm(w[0][g], w[1][g], hf ? 0x7632 : 0x5410);
+            const uint32_t y = __byte_perm(w[2][g], w[3][g], hf ? 0x7632 : 0x5410);
+            mma_f16(o[4 * g + 2 * hf], x & kLow, x & kHigh, y & kLow, y & kHigh, b[g][0], b[g][1]);
+            mma_f16(o[4 * g + 2 * hf + 1], (x >> 8) & kLow, (x >> 8) & kHigh, (y >> 8) & kLow, (y >> 8) & kHigh, b[g][0], b[g][1]);
+          }
+        }
+      }
+      __syncwarp();                    // every lane has read the stage before it is refilled
+    }
+
+    // the sums over tokens live on the eight threads that share tq
+#pragma unroll
+    for (int off = 4; off < 32; off <<= 1)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        l[k] += __shfl_xor_sync(0xffffffffu, l[k], off);
+#pragma unroll
+        for (int g = 0; g < NG; ++g) R[g][k] += __shfl_xor_sync(0xffffffffu, R[g][k], off);
+      }
+    const float back = 1.f / vs;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int hh = 2 * tq + k;
+      if (hh >= G) continue;
+      const float inv = 1.f / l[k], f = inv * (16777216.f / 15.f);
+      const int64_t row = (int64_t)(seg.entry >= 0 ? seg.entry : seg.req) * p.Hq + h * G + hh;
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        float y[8];                    // channels 64 g + 8 gq .. + 7
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          y[2 * i] = fmaf(o[4 * g + i][k] * f, back, R[g][k] * inv);
+          y[2 * i + 1] = fmaf(o[4 * g + i][2 + k] * (f * 0.0625f), back, R[g][k] * inv);
+        }
+        const int64_t at = row * D + 64 * g + 8 * gq;
+        if (seg.entry >= 0) {
+          *reinterpret_cast<float4*>(p.part_o + at) = make_float4(y[0], y[1], y[2], y[3]);
+          *reinterpret_cast<float4*>(p.part_o + at + 4) = make_float4(y[4], y[5], y[6], y[7]);
+        } else {
+          *reinterpret_cast<uint4*>(p.out + at) =
+              make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+        }
+      }
+      if (gq == 0) {
+        const float lse = m[k] + __log2f(l[k]);
+        if (seg.entry >= 0)
+          p.part_l[row] = lse;
+        else if (p.lse)
+          p.lse[row] = lse * kLn2;
       }
     }
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 // O = sum_e 2^(l_e - m) O_e / sum_e 2^(l_e - m), LSE = (m + log2 sum_e 2^(l_e - m)) ln 2 over the partial
-// states of a request, m the largest l_e; a warp for each request and query head.
-__global__ void __launch_bounds__(256) kv4_join_kernel(const float* part_o, const float* part_l, const RequestDev* reqs, int32_t B,
-                                                       int32_t Hq, int32_t D, uint16_t* out, float* lse) {
+// states of a request, m the largest l_e, for each query head.  WARPS warps share a row: each joins the states
+// e = its index + WARPS i, then the first one theirs.  A state of LSE -inf (weight 0) may hold anything.
+// Bound by latency: a warp asks for eight states' rows before it uses any.
+template <int D, int WARPS>
+__global__ void __launch_bounds__(256) kv4_join_kernel(const float* part_o, const float* part_l, const RequestDev* __restrict__ reqs,
+                                                       int32_t B, int32_t Hq, uint16_t* out, float* lse) {
+  constexpr int C = D / 32;            // channels of a thread
+  __shared__ float sm[8], sz[8], so[8][D];
   griddep_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % WARPS;
+  const int64_t w = blockIdx.x * (int64_t)(8 / WARPS) + warp / WARPS;
+  const bool row = w < (int64_t)B * Hq;
+  const int r = row ? (int)(w / Hq) : 0, qh = (int)(w % Hq);
+  const int e0 = reqs[r].entry_cas, ne = row ? reqs[r].n_entry_cas : -1;
   griddep_wait();
-  const int w = (int)((blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5), lane = threadIdx.x & 31;
-  if (w >= B * Hq) return;
-  const int r = w / Hq, qh = w % Hq;
-  const int e0 = reqs[r].entry_cas, ne = reqs[r].n_entry_cas;
-  if (ne < 0) return;  // written by its only segment
-  float m = -INFINITY, z = 0.f, o[4] = {};
-  for (int e = 0; e < ne; ++e) m = max_nan(m, __ldcg(part_l + (int64_t)(e0 + e) * Hq + qh));
-  if (m != -INFINITY)
-    for (int e = 0; e < ne; ++e) {
-      const int64_t row = (int64_t)(e0 + e) * Hq + qh;
-      const float x = ex2(__ldcg(part_l + row) - m);
-      if (x == 0.f) continue;      // an empty state, whose row may never have been written
-      z += x;
-      for (int c = 0; c < D / 32; ++c) o[c] = fmaf(x, __ldcg(part_o + row * D + lane * (D / 32) + c), o[c]);
+  float m = -INFINITY, z = 0.f, o[C] = {};
+  for (int eb = part; eb < ne; eb += 8 * WARPS) {
+    float l[8], v[8][C];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int e = eb + k * WARPS;
+      const int64_t at = (int64_t)(e0 + min(e, ne - 1)) * Hq + qh;
+      l[k] = e < ne ? __ldcg(part_l + at) : -INFINITY;
+      if (C == 4) {
+        const float4 x = __ldcg(reinterpret_cast<const float4*>(part_o + at * D) + lane);
+        v[k][0] = x.x; v[k][1] = x.y; v[k][C - 2] = x.z; v[k][C - 1] = x.w;
+      } else {
+        const float2 x = __ldcg(reinterpret_cast<const float2*>(part_o + at * D) + lane);
+        v[k][0] = x.x; v[k][1] = x.y;
+      }
     }
+    float top = m;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) top = max_nan(top, l[k]);
+    if (top == -INFINITY) continue;
+    const float a = ex2(m - top);
+    m = top;
+    z *= a;
+#pragma unroll
+    for (int c = 0; c < C; ++c) o[c] *= a;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float x = ex2(l[k] - m);
+      if (x == 0.f) continue;
+      z += x;
+#pragma unroll
+      for (int c = 0; c < C; ++c) o[c] = fmaf(x, v[k][c], o[c]);
+    }
+  }
+  if (WARPS > 1) {
+    sm[warp] = m;
+    sz[warp] = z;
+#pragma unroll
+    for (int c = 0; c < C; ++c) so[warp][lane * C + c] = o[c];
+    __syncthreads();
+    if (part > 0) return;
+    float top = m;
+#pragma unroll
+    for (int k = 1; k < WARPS; ++k) top = max_nan(top, sm[warp + k]);
+    if (top != -INFINITY) {
+      const float a = ex2(m - top);
+      z *= a;
+#pragma unroll
+      for (int c = 0; c < C; ++c) o[c] = a == 0.f ? 0.f : o[c] * a;
+#pragma unroll
+      for (int k = 1; k < WARPS; ++k) {
+        const float x = ex2(sm[warp + k] - top);
+        if (x == 0.f) continue;
+        z = fmaf(x, sz[warp + k], z);
+#pragma unroll
+        for (int c = 0; c < C; ++c) o[c] = fmaf(x, so[warp + k][lane * C + c], o[c]);
+      }
+    }
+    m = top;
+  }
+  if (ne < 0) return;                  // written by its only segment
   const float inv = m == -INFINITY ? 0.f : 1.f / z;
-  for (int c = 0; c < D / 32; c += 2)
-    *reinterpret_cast<uint32_t*>(out + ((int64_t)r * Hq + qh) * D + lane * (D / 32) + c) = pack_bf16x2(o[c] * inv, o[c + 1] * inv);
-  if (lane == 0 && lse) lse[(int64_t)r * Hq + qh] = m == -INFINITY ? -INFINITY : (m + __log2f(z)) * kLn2;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(out + w * D) + lane * (C / 2);
+#pragma unroll
+  for (int c = 0; c < C; c += 2) dst[c / 2] = pack_bf16x2(o[c] * inv, o[c + 1] * inv);
+  if (lane == 0 && lse) lse[w] = m == -INFINITY ? -INFINITY : (m + __log2f(z)) * kLn2;
+}
+
+size_t gather_smem(int hkv, int d) { return (size_t)hkv * stages(d) * stage_bytes(d); }
+
+template <int D, int G>
+int launch_gather_t(const Kv4Params& p, int ctas, cudaStream_t st) {
+  const size_t smem = gather_smem(p.Hkv, D);
+  auto kern = kv4_gather_kernel<D, G>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return (int)e;
+  return (int)launch_pdl(kern, dim3(ctas), dim3(32 * p.Hkv), smem, st, p);
 }
 
 }  // namespace
 
-int kv4_ctas_per_sm(const gk_pool_config* cfg) { return 16 / cfg->num_kv_heads; }
+// As many CTAs of Hkv warps as fit an SM's registers (16 warps) and shared memory.
+int kv4_ctas_per_sm(const gk_pool_config* cfg) {
+  const int by_smem = (int)(kSmSmem / (gather_smem(cfg->num_kv_heads, cfg->head_dim) + 1024));
+  const int by_warps = kSmWarps / cfg->num_kv_heads;
+  return by_smem < by_warps ? by_smem : by_warps;
+}
 
 int launch_kv4_gather(const LaunchCommon& lc, void* stream, int32_t layer, const gk_batch* b, const Plan* pl, void* d_out) {
   const gk_pool_config& c = *lc.cfg;
@@ -166,6 +560,9 @@ int launch_kv4_gather(const LaunchCommon& lc, void* stream, int32_t layer, const
   p.rows = (const uint8_t*)c.cold_k + layer * c.cold_slots * (int64_t)kv4::row_bytes(c.num_kv_heads, c.head_dim);
   p.num_blocks = c.cold_slots / c.cold_page_size;
   p.page = c.cold_page_size;
+  p.page_shift = -1;
+  for (int sh = 0; sh < 31; ++sh)
+    if ((1 << sh) == c.cold_page_size) p.page_shift = sh;
   p.Hkv = c.num_kv_heads;
   p.Hq = c.num_q_heads;
   p.table = b->d_block_table;
@@ -180,15 +577,34 @@ int launch_kv4_gather(const LaunchCommon& lc, void* stream, int32_t layer, const
   p.segs = (const SegmentDev*)(base + pl->off_suf_segs);
   p.scale = kLog2e / sqrtf((float)c.head_dim);
   p.err = lc.d_error;
-  auto kern = c.head_dim == 128 ? kv4_gather_kernel<128> : kv4_gather_kernel<64>;
-  return (int)launch_pdl(kern, dim3(pl->summary.suffix_ctas), dim3(32 * c.num_kv_heads), 0, (cudaStream_t)stream, p);
+  const int ctas = pl->summary.suffix_ctas, g = c.num_q_heads / c.num_kv_heads;
+  cudaStream_t st = (cudaStream_t)stream;
+  if (c.head_dim == 128) {
+    switch (g) {
+      case 1: return launch_gather_t<128, 1>(p, ctas, st);
+      case 2: return launch_gather_t<128, 2>(p, ctas, st);
+      case 4: return launch_gather_t<128, 4>(p, ctas, st);
+      case 5: return launch_gather_t<128, 5>(p, ctas, st);
+      case 8: return launch_gather_t<128, 8>(p, ctas, st);
+    }
+  } else {
+    switch (g) {
+      case 1: return launch_gather_t<64, 1>(p, ctas, st);
+      case 2: return launch_gather_t<64, 2>(p, ctas, st);
+      case 4: return launch_gather_t<64, 4>(p, ctas, st);
+    }
+  }
+  return (int)cudaErrorInvalidValue;
 }
 
 int launch_kv4_join(const LaunchCommon& lc, void* stream, const gk_batch* b, const Plan* pl, void* d_out) {
   const gk_pool_config& c = *lc.cfg;
-  const int64_t warps = (int64_t)pl->B * c.num_q_heads;
-  return (int)launch_pdl(kv4_join_kernel, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, (cudaStream_t)stream, pl->d_part_o,
-                         pl->d_part_l, (const RequestDev*)((const uint8_t*)pl->d_buf + pl->off_reqs), pl->B, c.num_q_heads, c.head_dim,
+  const int64_t rows = (int64_t)pl->B * c.num_q_heads;
+  const bool wide = pl->kv4_most_states > 8;
+  auto kern = c.head_dim == 128 ? (wide ? kv4_join_kernel<128, 8> : kv4_join_kernel<128, 1>)
+                                : (wide ? kv4_join_kernel<64, 8> : kv4_join_kernel<64, 1>);
+  return (int)launch_pdl(kern, dim3((unsigned)(wide ? rows : (rows + 7) / 8)), dim3(256), 0, (cudaStream_t)stream, pl->d_part_o,
+                         pl->d_part_l, (const RequestDev*)((const uint8_t*)pl->d_buf + pl->off_reqs), pl->B, c.num_q_heads,
                          (uint16_t*)d_out, b->d_lse);
 }
 
