@@ -81,6 +81,7 @@ constexpr int kPrefixTileN = 128;    // prefix keys per tile
 constexpr int kPrefixWarpRows = 128; // stacked query rows per warp-MMA prefix item (8 warps x 16)
 constexpr int kGatherT = 16;         // tokens per gather pipeline stage
 constexpr int kMaxKvHeads = 8;
+constexpr int kKv4Tokens = 32;       // tokens per stage of the 4-bit gather
 
 struct DeviceInfo {
   int device = -1;

@@ -11,7 +11,9 @@
 // one head (d = 128), so the instructions a token costs decide how near the gather comes.  Codes become
 // operands by one logic instruction a pair: the pair (code & 0x000f000f) read as fp16 is the subnormal pair
 // code * 2^-24, and (code & 0x00f000f0) is 16 * code * 2^-24, both exact, and the tensor core multiplies
-// subnormals exactly.  The factor 16 goes into the query's fragment, and into the output for V.
+// subnormals exactly.  The factor 16 goes into the query's fragment, and into the output for V.  (As 8-bit floats
+// four codes would take one mask, but the warp-level products of 8-bit operands are made of conversions to fp16
+// and fp16 products on this chip: 608 requests of 2048 tokens 265 us, so 450.)
 #include <cmath>
 
 #include "device_common.cuh"
@@ -22,7 +24,7 @@
 namespace gk {
 namespace {
 
-constexpr int kTok = 32;       // tokens of a stage
+constexpr int kTok = kKv4Tokens;
 constexpr int kSmWarps = 16;   // warps of an SM: 128 registers a thread
 constexpr size_t kSmSmem = 228 * 1024;  // shared memory of an SM, 1 KB of it taken by each resident CTA
 
@@ -65,14 +67,12 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-// BYTES from global to shared memory, zeros where !live
 template <int BYTES>
-__device__ __forceinline__ void copy_or_zero(uint32_t dst, const void* src, bool live) {
-  const int n = live ? BYTES : 0;
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
   if (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
   else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ uint2 lds64(uint32_t addr) {
   uint2 v;
@@ -89,6 +89,7 @@ __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)
 // floor(log2 x) of a normal x >= 0; -127 for 0
 __device__ __forceinline__ int exponent(float x) { return (int)(__float_as_uint(x) >> 23) - 127; }
 
+constexpr float kSlack = 4.f;
 constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
 
 // Warp h of a CTA is KV head h and its G query heads, and moves its own data: it copies its head's codes and
@@ -117,8 +118,8 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
   griddep_wait();
   const uint32_t ring = smem_u32(smem) + (uint32_t)(h * NST * stage_bytes(D));
   const int row_bytes = kv4::row_bytes(p.Hkv, D);
-  const uint8_t* const codes = p.rows + kv4::codes_at(h, D) + (lane % CPT) * 16;
-  const uint8_t* const scales = p.rows + kv4::scales_at(p.Hkv, h, D);
+  const uint8_t* const code_src = p.rows + kv4::codes_at(h, D) + (lane % CPT) * 16;
+  const uint8_t* const scale_src = p.rows + kv4::scales_at(p.Hkv, h, D);
 
   // ---- copies ----
   // where this thread's chunk of the tokens it copies lands: token T's K row at place T ^ bit 2 of T (d = 128; at d = 64
@@ -148,17 +149,16 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
       ltab = p.table + (int64_t)sd.req * p.max_blocks;
     }
   };
-  int32_t id = 0, in_page = 0;
-  int idn = 0;                       // tokens of the stage looked up
-  auto lookup = [&]() {
-    idn = 0;
+  // tokens of the next stage (0: none left), and this thread's token's block id and place in the block
+  auto lookup = [&](int& n, int32_t& id, int32_t& in_page) {
+    n = 0;
     if (lsg < sg1) {
-      idn = min(kTok, lt1 - lt);
+      n = min(kTok, lt1 - lt);
       const int t = lt + lane;
       const int b = p.page_shift >= 0 ? t >> p.page_shift : t / p.page;
       in_page = t - b * p.page;
-      if (lane < idn) id = __ldg(ltab + b);
-      lt += idn;
+      if (lane < n) id = __ldg(ltab + b);
+      lt += n;
       if (lt == lt1) {
         ++lsg;
         look_at();
@@ -166,32 +166,59 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
     }
   };
   int islot = 0;
-  auto issue = [&]() {
+  auto issue = [&](int idn, int32_t id, int32_t in_page) {
     if (idn > 0) {
-      int32_t slot = -1;
-      if (lane < idn) {
-        if (id >= 0 && id < p.num_blocks)
-          slot = id * p.page + in_page;
-        else
-          report_error(p.err, kErrBounds);
-      }
+      const bool bad = lane < idn && (id < 0 || id >= p.num_blocks);
+      int32_t slot = lane < idn && !bad ? id * p.page + in_page : 0;
+      if (idn < kTok) slot = __shfl_sync(0xffffffffu, slot, min(lane, idn - 1));
       const uint32_t st = ring + (uint32_t)islot * stage_bytes(D);
+      // places past the stage's tokens get its last token's row: they meet weights and spans of 0
 #pragma unroll
       for (int j = 0; j < kTok / TPI; ++j) {
         const int32_t s = __shfl_sync(0xffffffffu, slot, j * TPI + lane / CPT);
-        copy_or_zero<16>(st + (j & 1 ? dst1 : dst0) + j * TPI * (D / 2), codes + (int64_t)max(s, 0) * row_bytes, s >= 0);
+        copy_async<16>(st + (j & 1 ? dst1 : dst0) + j * TPI * (D / 2), code_src + (int64_t)s * row_bytes);
+        // a token's scales right behind its codes, in a copy of the few threads that just touched its row: one copy of all
+        // the stage's scales costs as many address translations as it has pages at once (pages of one token:
+        // 608 requests of 2048 tokens 454 us, so 265)
+        if (lane % CPT == 0)
+          copy_async<D / 8>(st + kTok * D + (j * TPI + lane / CPT) * (D / 8), scale_src + (int64_t)s * row_bytes);
       }
-      copy_or_zero<D / 8>(st + kTok * D + lane * (D / 8), scales + (int64_t)max(slot, 0) * row_bytes, slot >= 0);
+      const uint32_t zero = __ballot_sync(0xffffffffu, bad);
+      if (zero) {
+        // ids outside the pool: their tokens' rows count as zeros
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncwarp();
+        if (bad) report_error(p.err, kErrBounds);
+        for (uint32_t left = zero; left; left &= left - 1) {
+          const int t = __ffs(left) - 1;
+          const uint32_t k = D == 128 ? st + (t ^ (t >> 2 & 1)) * 64 : st + (t ^ (t >> 2 & 1) << 1) * 32;
+          const uint32_t v = st + kTok * (D / 2) + t * (D / 2) - D / 2;
+          if (lane < D / 16) sts128((lane < D / 32 ? k : v) + lane * 16, make_uint4(0, 0, 0, 0));
+          if (lane < D / 64) asm volatile("st.shared.v2.u32 [%0], {%1, %1};" ::"r"(st + kTok * D + t * (D / 8) + lane * 8), "r"(0) : "memory");
+        }
+        __syncwarp();
+      }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
     if (++islot == NST) islot = 0;
   };
+  // the next segment's query rows to L1, a 128-byte line a thread
+  auto prefetch_q = [&](int32_t req) {
+    const char* row = reinterpret_cast<const char*>(p.q + ((int64_t)req * p.Hq + h * G) * D) + lane * 128;
+    if (lane * 128 < G * D * 2) asm volatile("prefetch.global.L1 [%0];" ::"l"(row));
+  };
+  if (sg < sg1) prefetch_q(p.segs[sg].req);
   look_at();
-  lookup();
+  int nid;                           // the stage whose ids are on their way
+  int32_t id = 0, in_page = 0;
+  {
+    int n[NST - 1];
+    int32_t ids[NST - 1] = {}, at[NST - 1] = {};
 #pragma unroll
-  for (int i = 0; i < NST - 1; ++i) {
-    issue();
-    lookup();
+    for (int i = 0; i < NST - 1; ++i) lookup(n[i], ids[i], at[i]);
+    lookup(nid, id, in_page);
+#pragma unroll
+    for (int i = 0; i < NST - 1; ++i) issue(n[i], ids[i], at[i]);
   }
 
   // ---- compute ----
@@ -203,23 +230,27 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
   int cslot = 0;
   for (; sg < sg1; ++sg) {
     const SegmentDev seg = p.segs[sg];
-    // Q as B fragments: word i of a thread's K is channels ch .. ch + 7, paired (c, c + 4); scaled by a power of two
-    // to between 2^13 and 2^14, so that fp16 holds a row's bf16 values to 2^-38 of the largest
+    const int32_t dest = seg.entry >= 0 ? seg.entry : ~seg.req;
+    // Q as B fragments: the channels of a thread's word i of K, paired (c, c + 4); scaled by a power of two to
+    // between 2^13 and 2^14, so that fp16 holds a head's bf16 values to 2^-38 of the largest
     uint32_t qf[KW][4];
     float F[2], Z[NG][2];
     {
-      float x[KW][8], top = 0.f, sum[NG] = {};
+      uint4 raw[KW];
+      float top = 0.f, sum[NG] = {};
 #pragma unroll
       for (int i = 0; i < KW; ++i) {
-        const int w = KW * tq + i, ch = D == 128 ? 8 * (w >> 1) + 64 * (w & 1) : 8 * w;
-        uint4 r = make_uint4(0, 0, 0, 0);
-        if (gq < G) r = *reinterpret_cast<const uint4*>(p.q + ((int64_t)seg.req * p.Hq + h * G + gq) * D + ch);
-        x[i][0] = bf_lo(r.x); x[i][1] = bf_hi(r.x); x[i][2] = bf_lo(r.y); x[i][3] = bf_hi(r.y);
-        x[i][4] = bf_lo(r.z); x[i][5] = bf_hi(r.z); x[i][6] = bf_lo(r.w); x[i][7] = bf_hi(r.w);
+        const int w = KW * tq + i, ch = D == 128 ? 8 * (w >> 1) + 64 * (w & 1) : 8 * w;   // channels ch .. ch + 7
+        raw[i] = make_uint4(0, 0, 0, 0);
+        if (gq < G) raw[i] = *reinterpret_cast<const uint4*>(p.q + ((int64_t)seg.req * p.Hq + h * G + gq) * D + ch);
+      }
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          top = fmaxf(top, fabsf(x[i][c]));
-          sum[D == 128 ? i & 1 : 0] += x[i][c];
+      for (int i = 0; i < KW; ++i) {
+        const uint32_t r[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          top = fmaxf(top, fmaxf(fabsf(bf_lo(r[c])), fabsf(bf_hi(r[c]))));
+          sum[D == 128 ? i & 1 : 0] += bf_lo(r[c]) + bf_hi(r[c]);
         }
       }
 #pragma unroll
@@ -232,10 +263,11 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
       const float s = pow2(e), s16 = pow2(e - 4);
 #pragma unroll
       for (int i = 0; i < KW; ++i) {
-        qf[i][0] = pack_f16x2(x[i][0] * s, x[i][4] * s);
-        qf[i][1] = pack_f16x2(x[i][1] * s16, x[i][5] * s16);
-        qf[i][2] = pack_f16x2(x[i][2] * s, x[i][6] * s);
-        qf[i][3] = pack_f16x2(x[i][3] * s16, x[i][7] * s16);
+        const uint4 r = raw[i];
+        qf[i][0] = pack_f16x2(bf_lo(r.x) * s, bf_lo(r.z) * s);
+        qf[i][1] = pack_f16x2(bf_hi(r.x) * s16, bf_hi(r.z) * s16);
+        qf[i][2] = pack_f16x2(bf_lo(r.y) * s, bf_lo(r.w) * s);
+        qf[i][3] = pack_f16x2(bf_hi(r.y) * s16, bf_hi(r.w) * s16);
       }
       const float f = p.scale * (16777216.f / 15.f) * pow2(-e);
 #pragma unroll
@@ -248,12 +280,15 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
     float o[MT][4], R[NG][2] = {}, m[2] = {-INFINITY, -INFINITY}, l[2] = {};
 #pragma unroll
     for (int i = 0; i < MT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    float vs = 0.f;                    // spans of V are scaled by this power of two (0: not chosen yet)
+    // V's spans, up to the word `most`, are scaled by the power of two vs, to below 2^11: with kSlack the weights that
+    // fp16 holds stay below 2^15, and one below its normal range is off by 2^-35 of the largest span at most
+    float vs = 1.f;
+    int32_t most = -1;                 // not chosen yet
 
     for (int t = seg.t0; t < seg.t1; t += kTok) {
       const int n = min(kTok, seg.t1 - t);
-      issue();
-      lookup();
+      issue(nid, id, in_page);
+      lookup(nid, id, in_page);
       asm volatile("cp.async.wait_group %0;" ::"n"(NST - 1) : "memory");
       __syncwarp();
       const uint32_t st = ring + (uint32_t)cslot * stage_bytes(D);
@@ -311,28 +346,33 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
         for (int u = 0; u < 2; ++u)
 #pragma unroll
           for (int r = 0; r < 2; ++r)
-            if (16 * u + 8 * r + ta >= n) sc[u][2 * r] = sc[u][2 * r + 1] = -INFINITY;
+            if (16 * u + 8 * r + ta >= n) {
+              sc[u][2 * r] = sc[u][2 * r + 1] = -INFINITY;
+#pragma unroll
+              for (int g = 0; g < NG; ++g) vscale[u][r][g] = 0;
+            }
       }
-      // running maximum; weights
+      // The exponents' reference m is raised only where a score passes it by kSlack (a vote in place of a
+      // maximum over the warp), the scale vs of V's spans lowered only where one passes `most`.
       float x0 = fmaxf(fmaxf(sc[0][0], sc[0][2]), fmaxf(sc[1][0], sc[1][2]));
       float x1 = fmaxf(fmaxf(sc[0][1], sc[0][3]), fmaxf(sc[1][1], sc[1][3]));
-#pragma unroll
-      for (int off = 4; off < 32; off <<= 1) {
-        x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, off));
-        x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, off));
-      }
-      x0 = fmaxf(m[0], x0);
-      x1 = fmaxf(m[1], x1);
-      // the largest span of V this thread sees, in the current scale
-      float top = 0.f;
+      // (the span is a word's high half and not negative: words order as their spans)
+      int32_t top = 0;
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int r = 0; r < 2; ++r)
 #pragma unroll
-          for (int g = 0; g < NG; ++g) top = fmaxf(top, bf_hi(vscale[u][r][g]));
-      const bool grow = vs == 0.f || top * vs >= 32768.f;
-      if (__any_sync(0xffffffffu, x0 != m[0] || x1 != m[1] || grow)) {
+          for (int g = 0; g < NG; ++g) top = max(top, (int32_t)vscale[u][r][g]);
+      const bool grow = top > most;
+      if (__any_sync(0xffffffffu, x0 > m[0] + kSlack || x1 > m[1] + kSlack || grow)) {
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) {
+          x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, off));
+          x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, off));
+        }
+        x0 = fmaxf(m[0], x0);
+        x1 = fmaxf(m[1], x1);
         float a0 = ex2(m[0] - x0), a1 = ex2(m[1] - x1);
         if (x0 == m[0]) a0 = 1.f;      // -inf - -inf
         if (x1 == m[1]) a1 = 1.f;
@@ -344,15 +384,15 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
           R[g][1] *= a1;
         }
         if (__any_sync(0xffffffffu, grow)) {
-          // a scale that puts the stage's largest span between 2^13 and 2^14
-#pragma unroll
-          for (int off = 1; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-          const float to = pow2(min(113, 13 - exponent(top)));
-          if (vs != 0.f) {
+          top = __reduce_max_sync(0xffffffffu, top);
+          const int e = exponent(__uint_as_float((uint32_t)top & 0xffff0000u));
+          const float to = pow2(min(113, 10 - e));
+          if (most >= 0) {
             a0 *= to / vs;
             a1 *= to / vs;
           }
           vs = to;
+          most = (e + 127) << 23 | 0x007fffff;   // the largest word of a span below 2^(e + 1)
         }
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
@@ -404,6 +444,8 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
       __syncwarp();                    // every lane has read the stage before it is refilled
     }
 
+    // the next segment's query is on its way while this one's state is written
+    if (sg + 1 < sg1) prefetch_q(p.segs[sg + 1].req);
     // the sums over tokens live on the eight threads that share tq
 #pragma unroll
     for (int off = 4; off < 32; off <<= 1)
@@ -419,7 +461,7 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
       const int hh = 2 * tq + k;
       if (hh >= G) continue;
       const float inv = 1.f / l[k], f = inv * (16777216.f / 15.f);
-      const int64_t row = (int64_t)(seg.entry >= 0 ? seg.entry : seg.req) * p.Hq + h * G + hh;
+      const int64_t row = (int64_t)(dest >= 0 ? dest : ~dest) * p.Hq + h * G + hh;
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         float y[8];                    // channels 64 g + 8 gq .. + 7
@@ -429,7 +471,7 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
           y[2 * i + 1] = fmaf(o[4 * g + i][2 + k] * (f * 0.0625f), back, R[g][k] * inv);
         }
         const int64_t at = row * D + 64 * g + 8 * gq;
-        if (seg.entry >= 0) {
+        if (dest >= 0) {
           *reinterpret_cast<float4*>(p.part_o + at) = make_float4(y[0], y[1], y[2], y[3]);
           *reinterpret_cast<float4*>(p.part_o + at + 4) = make_float4(y[4], y[5], y[6], y[7]);
         } else {
@@ -439,7 +481,7 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
       }
       if (gq == 0) {
         const float lse = m[k] + __log2f(l[k]);
-        if (seg.entry >= 0)
+        if (dest >= 0)
           p.part_l[row] = lse;
         else if (p.lse)
           p.lse[row] = lse * kLn2;
@@ -454,13 +496,14 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
 // e = its index + WARPS i, then the first one theirs.  A state of LSE -inf (weight 0) may hold anything.
 // Bound by latency: a warp asks for eight states' rows before it uses any.
 template <int D, int WARPS>
-__global__ void __launch_bounds__(256) kv4_join_kernel(const float* part_o, const float* part_l, const RequestDev* __restrict__ reqs,
+__global__ void __launch_bounds__(WARPS > 8 ? 32 * WARPS : 256) kv4_join_kernel(const float* part_o, const float* part_l, const RequestDev* __restrict__ reqs,
                                                        int32_t B, int32_t Hq, uint16_t* out, float* lse) {
   constexpr int C = D / 32;            // channels of a thread
-  __shared__ float sm[8], sz[8], so[8][D];
+  constexpr int N = WARPS > 8 ? WARPS : 8;  // warps of a block
+  __shared__ float sm[N], sz[N], so[N][D];
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % WARPS;
-  const int64_t w = blockIdx.x * (int64_t)(8 / WARPS) + warp / WARPS;
+  const int64_t w = blockIdx.x * (int64_t)(N / WARPS) + warp / WARPS;
   const bool row = w < (int64_t)B * Hq;
   const int r = row ? (int)(w / Hq) : 0, qh = (int)(w % Hq);
   const int e0 = reqs[r].entry_cas, ne = row ? reqs[r].n_entry_cas : -1;
@@ -600,12 +643,15 @@ int launch_kv4_gather(const LaunchCommon& lc, void* stream, int32_t layer, const
 int launch_kv4_join(const LaunchCommon& lc, void* stream, const gk_batch* b, const Plan* pl, void* d_out) {
   const gk_pool_config& c = *lc.cfg;
   const int64_t rows = (int64_t)pl->B * c.num_q_heads;
-  const bool wide = pl->kv4_most_states > 8;
-  auto kern = c.head_dim == 128 ? (wide ? kv4_join_kernel<128, 8> : kv4_join_kernel<128, 1>)
-                                : (wide ? kv4_join_kernel<64, 8> : kv4_join_kernel<64, 1>);
-  return (int)launch_pdl(kern, dim3((unsigned)(wide ? rows : (rows + 7) / 8)), dim3(256), 0, (cudaStream_t)stream, pl->d_part_o,
-                         pl->d_part_l, (const RequestDev*)((const uint8_t*)pl->d_buf + pl->off_reqs), pl->B, c.num_q_heads,
-                         (uint16_t*)d_out, b->d_lse);
+  const int most = pl->kv4_most_states;
+  const int warps = most <= 8 ? 1 : most <= 64 ? 8 : 32;
+  auto kern = c.head_dim == 128
+                  ? (warps == 1 ? kv4_join_kernel<128, 1> : warps == 8 ? kv4_join_kernel<128, 8> : kv4_join_kernel<128, 32>)
+                  : (warps == 1 ? kv4_join_kernel<64, 1> : warps == 8 ? kv4_join_kernel<64, 8> : kv4_join_kernel<64, 32>);
+  return (int)launch_pdl(kern, dim3((unsigned)(warps == 1 ? (rows + 7) / 8 : rows)), dim3(warps == 32 ? 1024 : 256), 0,
+                         (cudaStream_t)stream, pl->d_part_o, pl->d_part_l,
+                         (const RequestDev*)((const uint8_t*)pl->d_buf + pl->off_reqs), pl->B, c.num_q_heads, (uint16_t*)d_out,
+                         b->d_lse);
 }
 
 }  // namespace gk

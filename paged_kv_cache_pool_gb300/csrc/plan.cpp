@@ -125,7 +125,7 @@ size_t append_region(size_t* off, size_t count, size_t align = 16) {
 // Split the concatenated token stream of all requests (lengths n[r]) into CTA
 // quotas; each CTA's slice becomes one segment per request it touches.
 void partition_tokens(const std::vector<int64_t>& n, int64_t max_ctas, std::vector<int32_t>* begin,
-                      std::vector<SegmentDev>* segs) {
+                      std::vector<SegmentDev>* segs, int64_t quantum = kGatherQuantum) {
   begin->clear();
   segs->clear();
   int64_t total = 0;
@@ -134,7 +134,7 @@ void partition_tokens(const std::vector<int64_t>& n, int64_t max_ctas, std::vect
   if (total == 0) return;
   int64_t quota = (total + max_ctas - 1) / max_ctas;
   quota = std::max<int64_t>(quota, kMinGatherQuota);
-  quota = (quota + kGatherQuantum - 1) / kGatherQuantum * kGatherQuantum;
+  quota = (quota + quantum - 1) / quantum * quantum;
   int64_t left = quota;
   for (size_t r = 0; r < n.size(); ++r) {
     int64_t t = 0;
@@ -150,6 +150,55 @@ void partition_tokens(const std::vector<int64_t>& n, int64_t max_ctas, std::vect
     }
   }
   if (begin->back() != (int32_t)segs->size()) begin->push_back((int32_t)segs->size());
+}
+
+// The stream of partition_tokens with no request cut: consecutive whole requests a CTA, up to the least limit that
+// max_ctas CTAs can hold.  A request in one piece needs no partial state and the step no join, a launch of about 4 us on
+// GB300; a CTA gathers kWholeSlack 4-bit tokens in that time.  False (and nothing written) where the limit is further than
+// that above an equal share.
+constexpr int64_t kWholeSlack = 64;
+bool partition_whole(const std::vector<int64_t>& n, int64_t max_ctas, std::vector<int32_t>* begin, std::vector<SegmentDev>* segs) {
+  int64_t total = 0, most = 0;
+  for (int64_t x : n) {
+    total += x;
+    most = std::max(most, x);
+  }
+  const int64_t share = (total + max_ctas - 1) / max_ctas;
+  auto ctas = [&](int64_t limit) {
+    int64_t count = 0, sum = limit;
+    for (int64_t x : n) {
+      if (x == 0) continue;
+      sum += x;
+      if (sum > limit) {
+        ++count;
+        sum = x;
+      }
+    }
+    return count;
+  };
+  int64_t lo = std::max(most, share), hi = share + kWholeSlack;
+  if (lo > hi || ctas(hi) > max_ctas) return false;
+  while (lo < hi) {
+    const int64_t mid = (lo + hi) / 2;
+    if (ctas(mid) <= max_ctas)
+      hi = mid;
+    else
+      lo = mid + 1;
+  }
+  begin->assign(1, 0);
+  segs->clear();
+  int64_t sum = 0;
+  for (size_t r = 0; r < n.size(); ++r) {
+    if (n[r] == 0) continue;
+    if (!segs->empty() && sum + n[r] > lo) {
+      begin->push_back((int32_t)segs->size());
+      sum = 0;
+    }
+    segs->push_back(SegmentDev{(int32_t)r, 0, (int32_t)n[r], -1});
+    sum += n[r];
+  }
+  if (!segs->empty()) begin->push_back((int32_t)segs->size());
+  return true;
 }
 
 // Tangram's ahead-of-time work partitioning (Algorithm 1) with requests in the
@@ -549,8 +598,10 @@ gk_status build_host_plan_kind(Pool* p, const gk_batch* b, Plan* pl, gk_prefix_k
   } else {
     if (p->gather_partition == GK_PARTITION_PER_REQUEST)
       partition_per_request(n_suf, num_sms, &pl->suf_seg_begin, &pl->suf_segs);
-    else
-      partition_tokens(n_suf, (int64_t)num_sms * (p->kv4 ? kv4_ctas_per_sm(&c) : 1), &pl->suf_seg_begin, &pl->suf_segs);
+    else if (!p->kv4)
+      partition_tokens(n_suf, num_sms, &pl->suf_seg_begin, &pl->suf_segs);
+    else if (!partition_whole(n_suf, (int64_t)num_sms * kv4_ctas_per_sm(&c), &pl->suf_seg_begin, &pl->suf_segs))
+      partition_tokens(n_suf, (int64_t)num_sms * kv4_ctas_per_sm(&c), &pl->suf_seg_begin, &pl->suf_segs, kKv4Tokens);
   }
   if (p->gather_partition == GK_PARTITION_PER_REQUEST)
     partition_per_request(n_dense, max_ctas, &pl->dense_seg_begin, &pl->dense_segs);

@@ -9,10 +9,11 @@ sum of d <= 128 squares in 16 + 3 steps, 1/sqrt within 2 units, two products, th
 attention (attend()): with weights p_j and COLD values lo + code * span / 15, the kernel rounds p_j span_j to fp16 (half a step,
 2^-11 of the term) and holds the rest in fp32; over a HOT prefix it rounds p_j to bf16 (2^-8 of the term); the output is rounded to
 bf16 (2^-8 of |O|).  fp32 errors as counted for the prompt attention's tests (scores below 2^9, at most 2^13 keys): 2^-12 of the
-absolute terms.  A weight's product below fp16's normal range is off by at most 2^-38 of the request's largest span (scaled to between
-2^13 and 2^14 or kept below 2^16, with steps of 2^-24), at most 2^13 of them: 2^-25 of the largest span against weights that add up
-to 1 or more.  With H = sum p |v| over HOT, C = sum p (|lo| + span) over COLD, both over Z:
-  |O - O*| <= 2^-8 |O*| + (2^-8 + 2^-12) H + (2^-11 + 2^-12) C + 2^-25 max span,     |LSE - LSE*| <= 2e-4.
+absolute terms.  Weights are relative to a score that the request's largest passes by at most 2^4, so that they add up to 1 or
+more, and the spans they meet are scaled so that the largest so far lies between 2^10 and 2^11; a product below fp16's normal range is
+off by half a step of 2^-24, 2^-35 of the largest span, and at most 2^13 of them by 2^-22.  With H = sum p |v| over HOT,
+C = sum p (|lo| + span) over COLD, both over Z:
+  |O - O*| <= 2^-8 |O*| + (2^-8 + 2^-12) H + (2^-11 + 2^-12) C + 2^-22 max span,     |LSE - LSE*| <= 2e-4.
 """
 import numpy as np
 
@@ -111,7 +112,7 @@ def attend(q, hot, cold):
         L[h] = m + np.log(z)
         size = cold[2][:, k]
         E[h] = 2.0 ** -8 * np.abs(O[h]) + (2.0 ** -8 + 2.0 ** -12) * (p[:n] @ np.abs(hot[1][:, k])) + \
-            (2.0 ** -11 + 2.0 ** -12) * (p[n:] @ size) + (2.0 ** -25 * size.max() if len(size) else 0)
+            (2.0 ** -11 + 2.0 ** -12) * (p[n:] @ size) + (2.0 ** -22 * size.max() if len(size) else 0)
     return O, L, E
 
 
