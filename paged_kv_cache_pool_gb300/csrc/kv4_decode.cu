@@ -11,7 +11,8 @@
 // one head (d = 128), so the instructions a token costs decide how near the gather comes.  Codes become
 // operands by one logic instruction a pair: the pair (code & 0x000f000f) read as fp16 is the subnormal pair
 // code * 2^-24, and (code & 0x00f000f0) is 16 * code * 2^-24, both exact, and the tensor core multiplies
-// subnormals exactly.  The factor 16 goes into the query's fragment, and into the output for V.  (As 8-bit floats
+// subnormals exactly; the factor 16 goes into the query's fragment.  For V the second operand is the whole byte,
+// code + 16 * code', from whose sum the first one's is taken in the end: two instructions a byte pair, not five for two.  (As 8-bit floats
 // four codes would take one mask, but the warp-level products of 8-bit operands are made of conversions to fp16
 // and fp16 products on this chip: 608 requests of 2048 tokens 265 us, so 450.)
 #include <cmath>
@@ -57,6 +58,20 @@ __device__ __forceinline__ void mma_f16(float* d, uint32_t a0, uint32_t a1, uint
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// the same onto zeros
+__device__ __forceinline__ void mma_f16_first(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+// D (16x8, fp32) = A (16x8, row) . B (8x8, col), bf16
+__device__ __forceinline__ void mma_bf16_first(float* d, uint32_t a0, uint32_t a1, uint32_t b0) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%7,%7,%7,%7};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(b0), "f"(0.f));
+}
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -90,7 +105,7 @@ __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)
 __device__ __forceinline__ int exponent(float x) { return (int)(__float_as_uint(x) >> 23) - 127; }
 
 constexpr float kSlack = 4.f;
-constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
+constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u, kByte = 0x00ff00ffu;
 
 // Warp h of a CTA is KV head h and its G query heads, and moves its own data: it copies its head's codes and
 // scales of 32 tokens a stage with cp.async into a private ring, stages(D) - 1 ahead of its compute, so no
@@ -234,7 +249,9 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
     // Q as B fragments: the channels of a thread's word i of K, paired (c, c + 4); scaled by a power of two to
     // between 2^13 and 2^14, so that fp16 holds a head's bf16 values to 2^-38 of the largest
     uint32_t qf[KW][4];
-    float F[2], Z[NG][2];
+    float F[2];
+    uint32_t zf;                     // sum(q) of each group (times scale) as the B fragment that meets lo: column gq, rows
+                                     // 2 tq and 2 tq + 1 the groups' tq-th bf16 terms, three of which make fp32
     {
       uint4 raw[KW];
       float top = 0.f, sum[NG] = {};
@@ -271,10 +288,15 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
       }
       const float f = p.scale * (16777216.f / 15.f) * pow2(-e);
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {    // of query heads 2 tq and 2 tq + 1
-        F[k] = __shfl_sync(0xffffffffu, f, 4 * (2 * tq + k));
+      for (int k = 0; k < 2; ++k) F[k] = __shfl_sync(0xffffffffu, f, 4 * (2 * tq + k));   // of query heads 2 tq and 2 tq + 1
+      float z[2] = {sum[0] * p.scale, NG == 2 ? sum[NG - 1] * p.scale : 0.f};
+      zf = 0;
 #pragma unroll
-        for (int g = 0; g < NG; ++g) Z[g][k] = __shfl_sync(0xffffffffu, sum[g], 4 * (2 * tq + k)) * p.scale;
+      for (int k = 0; k < 3; ++k) {
+        const uint32_t term = pack_bf16x2(z[0], z[1]);
+        if (tq == k) zf = term;
+        z[0] -= bf_lo(term);
+        z[1] -= bf_hi(term);
       }
     }
     float o[MT][4], R[NG][2] = {}, m[2] = {-INFINITY, -INFINITY}, l[2] = {};
@@ -319,26 +341,29 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
           ka[0] = a.x; vscale[u][0][0] = a.y;
           kb[0] = b.x; vscale[u][1][0] = b.y;
         }
-        float acc[NG][4] = {};
+        float acc[NG][4];
+        // the part of lo: k = 2 tq and 2 tq + 1 are the row's two groups
+        mma_bf16_first(sc[u], NG == 2 ? __byte_perm(ka[0], ka[NG - 1], 0x5410) : ka[0] & 0xffffu,
+                       NG == 2 ? __byte_perm(kb[0], kb[NG - 1], 0x5410) : kb[0] & 0xffffu, zf);
 #pragma unroll
         for (int i = 0; i < KW; ++i) {
           float* d = acc[D == 128 ? i & 1 : 0];
-          mma_f16(d, wa[i] & kLow, wb[i] & kLow, wa[i] & kHigh, wb[i] & kHigh, qf[i][0], qf[i][1]);
+          if (i < NG)
+            mma_f16_first(d, wa[i] & kLow, wb[i] & kLow, wa[i] & kHigh, wb[i] & kHigh, qf[i][0], qf[i][1]);
+          else
+            mma_f16(d, wa[i] & kLow, wb[i] & kLow, wa[i] & kHigh, wb[i] & kHigh, qf[i][0], qf[i][1]);
           const uint32_t xa = wa[i] >> 8, xb = wb[i] >> 8;
           mma_f16(d, xa & kLow, xb & kLow, xa & kHigh, xb & kHigh, qf[i][2], qf[i][3]);
         }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          float da = 0.f, db = 0.f, za = 0.f, zb = 0.f;
-#pragma unroll
-          for (int g = 0; g < NG; ++g) {
-            da = fmaf(bf_hi(ka[g]), acc[g][k], da);
-            db = fmaf(bf_hi(kb[g]), acc[g][2 + k], db);
-            za = fmaf(bf_lo(ka[g]), Z[g][k], za);
-            zb = fmaf(bf_lo(kb[g]), Z[g][k], zb);
+          float da = bf_hi(ka[0]) * acc[0][k], db = bf_hi(kb[0]) * acc[0][2 + k];
+          if (NG == 2) {
+            da = fmaf(bf_hi(ka[NG - 1]), acc[NG - 1][k], da);
+            db = fmaf(bf_hi(kb[NG - 1]), acc[NG - 1][2 + k], db);
           }
-          sc[u][k] = fmaf(da, F[k], za);
-          sc[u][2 + k] = fmaf(db, F[k], zb);
+          sc[u][k] = fmaf(da, F[k], sc[u][k]);
+          sc[u][2 + k] = fmaf(db, F[k], sc[u][2 + k]);
         }
       }
       if (n < kTok) {
@@ -354,18 +379,21 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
       }
       // The exponents' reference m is raised only where a score passes it by kSlack (a vote in place of a
       // maximum over the warp), the scale vs of V's spans lowered only where one passes `most`.
-      float x0 = fmaxf(fmaxf(sc[0][0], sc[0][2]), fmaxf(sc[1][0], sc[1][2]));
-      float x1 = fmaxf(fmaxf(sc[0][1], sc[0][3]), fmaxf(sc[1][1], sc[1][3]));
+      float d[2][4];
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[u][i] = sc[u][i] - m[i & 1];
       // (the span is a word's high half and not negative: words order as their spans)
       int32_t top = 0;
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
-#pragma unroll
-          for (int g = 0; g < NG; ++g) top = max(top, (int32_t)vscale[u][r][g]);
-      const bool grow = top > most;
-      if (__any_sync(0xffffffffu, x0 > m[0] + kSlack || x1 > m[1] + kSlack || grow)) {
+        for (int g = 0; g < NG; ++g) top = __vimax3_s32(top, (int32_t)vscale[u][0][g], (int32_t)vscale[u][1][g]);
+      const float past = fmaxf(fmax3(fmax3(d[0][0], d[0][1], d[0][2]), d[0][3], d[1][0]), fmax3(d[1][1], d[1][2], d[1][3]));
+      if (__any_sync(0xffffffffu, past > kSlack || top > most)) {
+        float x0 = fmaxf(fmaxf(sc[0][0], sc[0][2]), fmaxf(sc[1][0], sc[1][2]));
+        float x1 = fmaxf(fmaxf(sc[0][1], sc[0][3]), fmaxf(sc[1][1], sc[1][3]));
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) {
           x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, off));
@@ -383,7 +411,7 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
           R[g][0] *= a0;
           R[g][1] *= a1;
         }
-        if (__any_sync(0xffffffffu, grow)) {
+        if (__any_sync(0xffffffffu, top > most)) {
           top = __reduce_max_sync(0xffffffffu, top);
           const int e = exponent(__uint_as_float((uint32_t)top & 0xffff0000u));
           const float to = pow2(min(113, 10 - e));
@@ -400,13 +428,17 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
         }
         m[0] = x0;
         m[1] = x1;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) d[u][i] = sc[u][i] - m[i & 1];
       }
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         uint32_t b[NG][2];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const float p0 = ex2(sc[u][2 * r] - m[0]), p1 = ex2(sc[u][2 * r + 1] - m[1]);
+          const float p0 = ex2(d[u][2 * r]), p1 = ex2(d[u][2 * r + 1]);
           l[0] += p0;
           l[1] += p1;
 #pragma unroll
@@ -436,8 +468,9 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
           for (int hf = 0; hf < 2; ++hf) {      // channels 0 .. 3, then 4 .. 7
             const uint32_t x = __byte_perm(w[0][g], w[1][g], hf ? 0x7632 : 0x5410);
             const uint32_t y = __byte_perm(w[2][g], w[3][g], hf ? 0x7632 : 0x5410);
-            mma_f16(o[4 * g + 2 * hf], x & kLow, x & kHigh, y & kLow, y & kHigh, b[g][0], b[g][1]);
-            mma_f16(o[4 * g + 2 * hf + 1], (x >> 8) & kLow, (x >> 8) & kHigh, (y >> 8) & kLow, (y >> 8) & kHigh, b[g][0], b[g][1]);
+            const uint32_t x1 = __byte_perm(x, 0, 0x4341), y1 = __byte_perm(y, 0, 0x4341);
+            mma_f16(o[4 * g + 2 * hf], x & kLow, x & kByte, y & kLow, y & kByte, b[g][0], b[g][1]);
+            mma_f16(o[4 * g + 2 * hf + 1], x1 & kLow, x1, y1 & kLow, y1, b[g][0], b[g][1]);
           }
         }
       }
@@ -468,7 +501,7 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           y[2 * i] = fmaf(o[4 * g + i][k] * f, back, R[g][k] * inv);
-          y[2 * i + 1] = fmaf(o[4 * g + i][2 + k] * (f * 0.0625f), back, R[g][k] * inv);
+          y[2 * i + 1] = fmaf((o[4 * g + i][2 + k] - o[4 * g + i][k]) * (f * 0.0625f), back, R[g][k] * inv);
         }
         const int64_t at = row * D + 64 * g + 8 * gq;
         if (dest >= 0) {
