@@ -47,6 +47,8 @@ struct Kv4Params {
   int32_t* err;
 };
 
+constexpr int kSegCache = 32;  // segment records a CTA keeps in shared memory
+
 // a stage of one warp: K codes, V codes, scales of kTok tokens
 __host__ __device__ constexpr int stage_bytes(int d) { return kTok * (d + d / 8); }
 __host__ __device__ constexpr int stages(int d) { return d == 128 ? 3 : 4; }
@@ -125,13 +127,21 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
   constexpr int CPT = D / 16;        // 16-byte chunks of a token's codes (K and V)
   constexpr int TPI = 32 / CPT;      // tokens a copy instruction of the warp covers
   extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int4 cache[kSegCache];
   const int lane = threadIdx.x & 31, h = threadIdx.x >> 5;
   const int gq = lane >> 2, tq = lane & 3;
-  const int sg1 = p.seg_begin[blockIdx.x + 1];
-  int sg = p.seg_begin[blockIdx.x];
+  // The CTA's segments: the plan's tables are not written by the kernels of a step, so the records are read while the
+  // kernel ahead ends, and a change of segment costs no trip to memory.
+  const int sg0 = p.seg_begin[blockIdx.x], sg1 = p.seg_begin[blockIdx.x + 1];
+  for (int i = threadIdx.x; i < min(sg1 - sg0, kSegCache); i += blockDim.x)
+    cache[i] = *reinterpret_cast<const int4*>(p.segs + sg0 + i);
+  __syncthreads();
+  auto seg_at = [&](int i) {         // request, first and end token, partial state
+    return i - sg0 < kSegCache ? cache[i - sg0] : *reinterpret_cast<const int4*>(p.segs + i);
+  };
   griddep_launch_dependents();
   griddep_wait();
-  const uint32_t ring = smem_u32(smem) + (uint32_t)(h * NST * stage_bytes(D));
+  const uint32_t ring = smem_u32(smem) + h * NST * stage_bytes(D);
   const int row_bytes = kv4::row_bytes(p.Hkv, D);
   const uint8_t* const code_src = p.rows + kv4::codes_at(h, D) + (lane % CPT) * 16;
   const uint8_t* const scale_src = p.rows + kv4::scales_at(p.Hkv, h, D);
@@ -154,14 +164,20 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
       dst0 = dst1 = kTok * (D / 2) + (D == 128 ? t * 64 + (cv ^ ((t >> 1 & 1) << 1)) * 16 : t * 32 + cv * 16);
     }
   }
-  int lsg = sg, lt = 0, lt1 = 0;     // the look-up's segment and tokens
+  // a segment's query rows to L1, a 128-byte line a thread, when its first stage is looked up
+  auto prefetch_q = [&](int32_t req) {
+    const char* row = reinterpret_cast<const char*>(p.q + ((int64_t)req * p.Hq + h * G) * D) + lane * 128;
+    if (lane * 128 < G * D * 2) asm volatile("prefetch.global.L1 [%0];" ::"l"(row));
+  };
+  int lsg = sg0, lt = 0, lt1 = 0;     // the look-up's segment and tokens
   const int32_t* ltab = nullptr;
   auto look_at = [&]() {
     if (lsg < sg1) {
-      const SegmentDev sd = p.segs[lsg];
-      lt = sd.t0;
-      lt1 = sd.t1;
-      ltab = p.table + (int64_t)sd.req * p.max_blocks;
+      const int4 s = seg_at(lsg);
+      lt = s.y;
+      lt1 = s.z;
+      ltab = p.table + (int64_t)s.x * p.max_blocks;
+      prefetch_q(s.x);
     }
   };
   // tokens of the next stage (0: none left), and this thread's token's block id and place in the block
@@ -180,13 +196,13 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
       }
     }
   };
-  int islot = 0;
+  int next = 0;
   auto issue = [&](int idn, int32_t id, int32_t in_page) {
     if (idn > 0) {
       const bool bad = lane < idn && (id < 0 || id >= p.num_blocks);
       int32_t slot = lane < idn && !bad ? id * p.page + in_page : 0;
       if (idn < kTok) slot = __shfl_sync(0xffffffffu, slot, min(lane, idn - 1));
-      const uint32_t st = ring + (uint32_t)islot * stage_bytes(D);
+      const uint32_t st = ring + (uint32_t)next * stage_bytes(D);
       // places past the stage's tokens get its last token's row: they meet weights and spans of 0
 #pragma unroll
       for (int j = 0; j < kTok / TPI; ++j) {
@@ -215,14 +231,8 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
-    if (++islot == NST) islot = 0;
+    if (++next == NST) next = 0;
   };
-  // the next segment's query rows to L1, a 128-byte line a thread
-  auto prefetch_q = [&](int32_t req) {
-    const char* row = reinterpret_cast<const char*>(p.q + ((int64_t)req * p.Hq + h * G) * D) + lane * 128;
-    if (lane * 128 < G * D * 2) asm volatile("prefetch.global.L1 [%0];" ::"l"(row));
-  };
-  if (sg < sg1) prefetch_q(p.segs[sg].req);
   look_at();
   int nid;                           // the stage whose ids are on their way
   int32_t id = 0, in_page = 0;
@@ -243,9 +253,9 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
                         (D == 128 ? tq * 64 + ((gq >> 1) ^ ((tq >> 1) << 1)) * 16 + (gq & 1) * 8 : tq * 32 + gq * 4);
   const uint32_t s_at = kTok * D + ta * (D / 8);
   int cslot = 0;
-  for (; sg < sg1; ++sg) {
-    const SegmentDev seg = p.segs[sg];
-    const int32_t dest = seg.entry >= 0 ? seg.entry : ~seg.req;
+  for (int sg = sg0; sg < sg1; ++sg) {
+    const int4 seg = seg_at(sg);
+    const int32_t dest = seg.w >= 0 ? seg.w : ~seg.x;
     // Q as B fragments: the channels of a thread's word i of K, paired (c, c + 4); scaled by a power of two to
     // between 2^13 and 2^14, so that fp16 holds a head's bf16 values to 2^-38 of the largest
     uint32_t qf[KW][4];
@@ -259,7 +269,7 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
       for (int i = 0; i < KW; ++i) {
         const int w = KW * tq + i, ch = D == 128 ? 8 * (w >> 1) + 64 * (w & 1) : 8 * w;   // channels ch .. ch + 7
         raw[i] = make_uint4(0, 0, 0, 0);
-        if (gq < G) raw[i] = *reinterpret_cast<const uint4*>(p.q + ((int64_t)seg.req * p.Hq + h * G + gq) * D + ch);
+        if (gq < G) raw[i] = *reinterpret_cast<const uint4*>(p.q + ((int64_t)seg.x * p.Hq + h * G + gq) * D + ch);
       }
 #pragma unroll
       for (int i = 0; i < KW; ++i) {
@@ -307,8 +317,8 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
     float vs = 1.f;
     int32_t most = -1;                 // not chosen yet
 
-    for (int t = seg.t0; t < seg.t1; t += kTok) {
-      const int n = min(kTok, seg.t1 - t);
+    for (int t = seg.y; t < seg.z; t += kTok) {
+      const int n = min(kTok, seg.z - t);
       issue(nid, id, in_page);
       lookup(nid, id, in_page);
       asm volatile("cp.async.wait_group %0;" ::"n"(NST - 1) : "memory");
@@ -477,8 +487,6 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
       __syncwarp();                    // every lane has read the stage before it is refilled
     }
 
-    // the next segment's query is on its way while this one's state is written
-    if (sg + 1 < sg1) prefetch_q(p.segs[sg + 1].req);
     // the sums over tokens live on the eight threads that share tq
 #pragma unroll
     for (int off = 4; off < 32; off <<= 1)
@@ -622,9 +630,10 @@ int launch_gather_t(const Kv4Params& p, int ctas, cudaStream_t st) {
 
 }  // namespace
 
-// As many CTAs of Hkv warps as fit an SM's registers (16 warps) and shared memory.
+// As many CTAs of Hkv warps as an SM's registers (kSmWarps warps) and shared memory hold.
 int kv4_ctas_per_sm(const gk_pool_config* cfg) {
-  const int by_smem = (int)(kSmSmem / (gather_smem(cfg->num_kv_heads, cfg->head_dim) + 1024));
+  const int by_smem =
+      (int)(kSmSmem / (gather_smem(cfg->num_kv_heads, cfg->head_dim) + sizeof(int4) * kSegCache + 1024));
   const int by_warps = kSmWarps / cfg->num_kv_heads;
   return by_smem < by_warps ? by_smem : by_warps;
 }

@@ -201,6 +201,12 @@ bool partition_whole(const std::vector<int64_t>& n, int64_t max_ctas, std::vecto
   return true;
 }
 
+// The 4-bit gather's work of each CTA: whole requests where that is no further from equal shares than a join costs, else
+// the stream cut into equal quotas of whole stages.
+void partition_kv4(const std::vector<int64_t>& n, int64_t slots, std::vector<int32_t>* begin, std::vector<SegmentDev>* segs) {
+  if (!partition_whole(n, slots, begin, segs)) partition_tokens(n, slots, begin, segs, kKv4Tokens);
+}
+
 // Tangram's ahead-of-time work partitioning (Algorithm 1) with requests in the
 // place of its head groups and their token counts as budgets: the per-split
 // target is tau = max(1, ceil(total / ctas)), request r takes
@@ -596,12 +602,12 @@ gk_status build_host_plan_kind(Pool* p, const gk_batch* b, Plan* pl, gk_prefix_k
     const std::vector<double> w = split_weights(cm, num_sms, it, (double)S, gsm, v, prefix_cta_share > 0.0);
     partition_tokens_weighted(n_suf, w, &pl->suf_seg_begin, &pl->suf_segs);
   } else {
-    if (p->gather_partition == GK_PARTITION_PER_REQUEST)
+    if (p->kv4)
+      partition_kv4(n_suf, (int64_t)num_sms * kv4_ctas_per_sm(&c), &pl->suf_seg_begin, &pl->suf_segs);
+    else if (p->gather_partition == GK_PARTITION_PER_REQUEST)
       partition_per_request(n_suf, num_sms, &pl->suf_seg_begin, &pl->suf_segs);
-    else if (!p->kv4)
+    else
       partition_tokens(n_suf, num_sms, &pl->suf_seg_begin, &pl->suf_segs);
-    else if (!partition_whole(n_suf, (int64_t)num_sms * kv4_ctas_per_sm(&c), &pl->suf_seg_begin, &pl->suf_segs))
-      partition_tokens(n_suf, (int64_t)num_sms * kv4_ctas_per_sm(&c), &pl->suf_seg_begin, &pl->suf_segs, kKv4Tokens);
   }
   if (p->gather_partition == GK_PARTITION_PER_REQUEST)
     partition_per_request(n_dense, max_ctas, &pl->dense_seg_begin, &pl->dense_segs);
