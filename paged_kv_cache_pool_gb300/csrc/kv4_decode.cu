@@ -49,9 +49,11 @@ struct Kv4Params {
 
 constexpr int kSegCache = 32;  // segment records a CTA keeps in shared memory
 
+constexpr int kStages = 2;     // a warp's ring: 3 hold as many bytes more as the SM can use, and cost 2 %
+constexpr int kFewPages = 8;   // tokens a page from which a stage touches few of them
+
 // a stage of one warp: K codes, V codes, scales of kTok tokens
 __host__ __device__ constexpr int stage_bytes(int d) { return kTok * (d + d / 8); }
-__host__ __device__ constexpr int stages(int d) { return d == 128 ? 3 : 4; }
 
 // D (16x8, fp32) += A (16x16, row) . B (16x8, col), fp16
 __device__ __forceinline__ void mma_f16(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -110,7 +112,7 @@ constexpr float kSlack = 4.f;
 constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u, kByte = 0x00ff00ffu;
 
 // Warp h of a CTA is KV head h and its G query heads, and moves its own data: it copies its head's codes and
-// scales of 32 tokens a stage with cp.async into a private ring, stages(D) - 1 ahead of its compute, so no
+// scales of 32 tokens a stage with cp.async into a private ring, kStages - 1 ahead of its compute, so no
 // warp waits for another; 16 warps share an SM.  Block ids are loaded a stage before its copies.
 //
 // A stage is two tiles of 16 tokens.  S^T[16 tok x 8] = K . Q^T: a thread's 16 bytes of a token's K row are the
@@ -123,7 +125,7 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
   constexpr int NG = D / 64;         // groups
   constexpr int KW = D / 32;         // words of K a thread takes of a token
   constexpr int MT = D / 16;         // m16 tiles of O^T
-  constexpr int NST = stages(D);
+  constexpr int NST = kStages;
   constexpr int CPT = D / 16;        // 16-byte chunks of a token's codes (K and V)
   constexpr int TPI = 32 / CPT;      // tokens a copy instruction of the warp covers
   extern __shared__ __align__(128) uint8_t smem[];
@@ -204,15 +206,25 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
       if (idn < kTok) slot = __shfl_sync(0xffffffffu, slot, min(lane, idn - 1));
       const uint32_t st = ring + (uint32_t)next * stage_bytes(D);
       // places past the stage's tokens get its last token's row: they meet weights and spans of 0
+      const uint32_t sdst = st + kTok * D;
+      if (p.page >= kFewPages) {
 #pragma unroll
-      for (int j = 0; j < kTok / TPI; ++j) {
-        const int32_t s = __shfl_sync(0xffffffffu, slot, j * TPI + lane / CPT);
-        copy_async<16>(st + (j & 1 ? dst1 : dst0) + j * TPI * (D / 2), code_src + (int64_t)s * row_bytes);
-        // a token's scales right behind its codes, in a copy of the few threads that just touched its row: one copy of all
-        // the stage's scales costs as many address translations as it has pages at once (pages of one token:
-        // 608 requests of 2048 tokens 454 us, so 265)
-        if (lane % CPT == 0)
-          copy_async<D / 8>(st + kTok * D + (j * TPI + lane / CPT) * (D / 8), scale_src + (int64_t)s * row_bytes);
+        for (int j = 0; j < kTok / TPI; ++j) {
+          const int32_t s = __shfl_sync(0xffffffffu, slot, j * TPI + lane / CPT);
+          copy_async<16>(st + (j & 1 ? dst1 : dst0) + j * TPI * (D / 2), code_src + (int64_t)s * row_bytes);
+        }
+        copy_async<D / 8>(sdst + lane * (D / 8), scale_src + (int64_t)slot * row_bytes);
+      } else {
+        // A copy of all the stage's scales costs as many address translations as it has pages at once: with pages of
+        // one token 608 requests of 2048 tokens take 454 us, and 265 where the few threads that just touched a token's row
+        // copy its scales.  With pages of 16 this form takes 263 us and the other 250.
+#pragma unroll
+        for (int j = 0; j < kTok / TPI; ++j) {
+          const int32_t s = __shfl_sync(0xffffffffu, slot, j * TPI + lane / CPT);
+          copy_async<16>(st + (j & 1 ? dst1 : dst0) + j * TPI * (D / 2), code_src + (int64_t)s * row_bytes);
+          if (lane % CPT == 0)
+            copy_async<D / 8>(sdst + (j * TPI + lane / CPT) * (D / 8), scale_src + (int64_t)s * row_bytes);
+        }
       }
       const uint32_t zero = __ballot_sync(0xffffffffu, bad);
       if (zero) {
@@ -617,7 +629,7 @@ __global__ void __launch_bounds__(WARPS > 8 ? 32 * WARPS : 256) kv4_join_kernel(
   if (lane == 0 && lse) lse[w] = m == -INFINITY ? -INFINITY : (m + __log2f(z)) * kLn2;
 }
 
-size_t gather_smem(int hkv, int d) { return (size_t)hkv * stages(d) * stage_bytes(d); }
+size_t gather_smem(int hkv, int d) { return (size_t)hkv * kStages * stage_bytes(d); }
 
 template <int D, int G>
 int launch_gather_t(const Kv4Params& p, int ctas, cudaStream_t st) {
