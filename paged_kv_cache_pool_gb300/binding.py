@@ -476,48 +476,63 @@ class Rope:
         self.c = gk_qkv(0, rot_dim or 0, int(bool(interleaved)), eps, 0 if cos_sin is None else cos_sin.shape[0], _ptr(cos_sin), None,
                         _ptr(q_weight), _ptr(k_weight))
         self.ref = ctypes.byref(self.c)
+        self.seen = None
 
     def set(self, pool, positions, q, k, v, q_out, k_out, n):
         """Fill the call's rows in: bf16 [n, heads, d] tensors (tokens may be strided) or addresses of packed rows."""
+        c = self.c
+        # what a layout was found to be when it came last (strides, heads and types: not what the tensors hold or where)
+        seen = (pool, n, _layout(q), _layout(q_out), _layout(k), _layout(k_out), _layout(v), _layout(positions))
+        if seen != self.seen:
+            self.seen = None
+            self._check(pool, positions, q, k, v, q_out, k_out, n)
+            self.seen = seen
+        c.d_q, c.d_q_out, c.d_k, c.d_k_out, c.d_v = _ptr(q), _ptr(q_out), _ptr(k), _ptr(k_out), _ptr(v)
+        if self.rotates:
+            c.d_positions = _ptr(positions)
+        return self.ref
+
+    def _check(self, pool, positions, q, k, v, q_out, k_out, n):
         c, torch = self.c, self.torch
         hq, hkv, dim = _geometry.get(pool, (None, None, None))
         if dim is not None and any(d != dim for d in self.dims):
             raise ValueError(f"the norms' weights are of {self.dims} channels, the pool's heads of {dim}")
-        rows = []
+        strides = []
         for x, heads, what in ((q, hq, "q"), (q_out, hq, "q_out"), (k, hkv, "k"), (k_out, hkv, "k_out"), (v, hkv, "v")):
-            h, d, stride, at = _token_rows(x, n, what, torch)
+            h, d, stride, _ = _token_rows(x, n, what, torch)
             if h is not None and heads is not None and (h != heads or d != dim):
                 raise ValueError(f"{what} must have the pool's {heads} heads of {dim}")
-            rows += [at, stride]
-        if self.rotates and positions is None and n:
-            raise ValueError("a rotation needs positions")
-        c.d_positions = _gpu_row(positions, n, torch.int32, "positions") if self.rotates else None
+            strides.append(stride)
+        if self.rotates:
+            if positions is None and n:
+                raise ValueError("a rotation needs positions")
+            _gpu_row(positions, n, torch.int32, "positions")
         c.num_tokens = n
-        c.d_q, c.q_stride, c.d_q_out, c.q_out_stride, c.d_k, c.k_stride, c.d_k_out, c.k_out_stride, c.d_v, c.v_stride = rows
-        return self.ref
+        c.q_stride, c.q_out_stride, c.k_stride, c.k_out_stride, c.v_stride = strides
 
 
-def _tokens(*xs):
-    """The tokens of the first tensor."""
-    return next(x.shape[0] for x in xs if x is not None and not isinstance(x, int))
+def _layout(x):
+    """All that the checks of a tensor look at (an address and None: themselves)."""
+    return x if x is None or isinstance(x, int) else (x.shape, x.stride(), x.dtype, x.is_cuda)
 
 
 def gk_qk_norm_rope(pool, stream, rope, positions, q, k, q_out=None, k_out=None, n=None):
     """q [n, Hq, d] and k [n, Hkv, d] (either may be None), normed and rotated, to q_out and k_out (default: in place)."""
-    q_out, k_out = q if q_out is None else q_out, k if k_out is None else k_out
-    ref = rope.set(pool, positions, q, k, None, q_out, k_out, _tokens(q, k) if n is None else n)
-    st = lib().gk_qk_norm_rope(pool, _stream(stream), ref)
+    n = (k if q is None else q).shape[0] if n is None else n
+    ref = rope.set(pool, positions, q, k, None, q if q_out is None else q_out, k if k_out is None else k_out, n)
+    st = (_lib or lib()).gk_qk_norm_rope(pool, _stream(stream), ref)
     if st:
         _check(st, pool)
 
 
 def gk_append_qkv(pool, stream, layer, rope, positions, d_slot_mapping, q, k, v, q_out=None, k_out=None, d_cow_pairs=None, n=None):
     """As gk_qk_norm_rope, and K and V into the cache; q may be None, q_out defaults to in place, k_out to none."""
-    n = _tokens(k, d_slot_mapping) if n is None else n
+    n = k.shape[0] if n is None else n
     ref = rope.set(pool, positions, q, k, v, q if q_out is None else q_out, k_out, n)
+    i32, i64 = rope.torch.int32, rope.torch.int64
     n_cow = 0 if d_cow_pairs is None else d_cow_pairs.numel() // 2
-    st = lib().gk_append_qkv(pool, _stream(stream), layer, ref, _gpu_row(d_slot_mapping, n, rope.torch.int64, "the slot mapping"), n_cow,
-                             _gpu_row(d_cow_pairs, 2 * n_cow, rope.torch.int32, "copy-on-write pairs") if n_cow else None)
+    st = (_lib or lib()).gk_append_qkv(pool, _stream(stream), layer, ref, _gpu_row(d_slot_mapping, n, i64, "the slot mapping"), n_cow,
+                                       _gpu_row(d_cow_pairs, 2 * n_cow, i32, "copy-on-write pairs") if n_cow else None)
     if st:
         _check(st, pool)
 

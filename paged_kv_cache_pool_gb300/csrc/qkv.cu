@@ -21,6 +21,8 @@ namespace gk {
 namespace {
 
 constexpr int kWarps = 4;  // warps of a block
+constexpr int kChunk = 7;  // most passes of a warp (5, 12 or 14 a warp: 3 - 10 % slower)
+constexpr int kFewWarps = 64;
 
 // how channels rotate: not at all, whole heads in halves, neighbouring pairs, a part of the head in halves
 enum Rotation { kNone, kHalves, kPairs, kPart };
@@ -55,6 +57,12 @@ __device__ __forceinline__ void load8(const float* p, float* x) {
   const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
   x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
 }
+// 16 bytes that this call reads once
+__device__ __forceinline__ uint4 load_once(const uint16_t* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+  return v;
+}
 __device__ __forceinline__ float min_nan(float a, float b) {
   float m;
   asm("min.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
@@ -74,6 +82,12 @@ __device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
   a = x;
 }
 
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 // lo and span (as bf16 bits, lo in the low half) of a group whose least and greatest values are given
 __device__ __forceinline__ uint32_t group_scale(float lo, float hi, float& span) {
   const uint32_t w = pack_bf16x2(lo, __fsub_rn(hi, lo));
@@ -89,147 +103,121 @@ __device__ __forceinline__ uint32_t group_scale(float lo, float hi, float& span)
   return w;
 }
 
-// eight codes, the first in the lowest nibble
+// Eight codes round(15 (x - lo) / span), ties to even, the first in the lowest nibble.  A product with the reciprocal is
+// within 2^-21 of the quotient; where its nearest integer leaves a remainder of half the span or more (exact: the
+// integer has four bits, the span eight) the neighbour, or of two the even one, is right.
 __device__ __forceinline__ uint32_t codes8(const float* x, float lo, float span) {
+  if (span == 0.f) return 0u;
+  constexpr float kMagic = 12582912.f;   // 1.5 * 2^23: a sum with it is rounded to an integer, in its low bits
+  const float inv = __frcp_rn(span), half = 0.5f * span;
   uint32_t w = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    // round(15 (x - lo) / span) to even
-    const float c = rintf(__fdiv_rn(__fmul_rn(__fsub_rn(x[i], lo), 15.f), span));
-    w |= (uint32_t)fminf(c, 15.f) << (4 * i);
+    const float t = __fmul_rn(__fsub_rn(x[i], lo), 15.f);
+    const float y = __fadd_rn(__fmul_rn(t, inv), kMagic);
+    float c = __fsub_rn(y, kMagic);
+    const float rem = fmaf(-c, span, t);
+    uint32_t code = __float_as_uint(y) & 15u;
+    if (fabsf(rem) >= half && (fabsf(rem) > half || (code & 1u))) code += rem > 0.f ? 1u : -1u;
+    w |= (code & 15u) << (4 * i);
   }
-  return span > 0.f ? w : 0u;
+  return w;
 }
 
-template <int D, int ROT, bool KV4>
-__global__ void __launch_bounds__(32 * kWarps) qkv_kernel(const QkvParams p, int passes) {
-  constexpr int LPH = D / 16;       // lanes of a head
-  constexpr int HPW = 32 / LPH;     // heads of a pass
-  griddep_launch_dependents();
-  griddep_wait();
-  const int lane = threadIdx.x & 31, j = lane % LPH;
-  const int64_t w = blockIdx.x * (int64_t)kWarps + (threadIdx.x >> 5);
-  const int64_t tok = w / passes;
-  if (tok >= p.n) return;
-  int64_t at = 0;
-  if (ROT != kNone) {
-    at = p.pos[tok];
-    if (at < 0 || at >= p.num_pos) {
-      if (lane == 0) report_error(p.err, kErrBounds);
-      return;
+// What the rotation of a thread's two chunks takes: of whole heads in halves one set of eight cosines and sines for the
+// pairs (i, i + 8) of its 16 channels, of neighbouring pairs four for each chunk, of a part in halves eight for each.
+template <int ROT>
+struct Angles {
+  float c[ROT == kPart ? 16 : 8], s[ROT == kPart ? 16 : 8];
+};
+
+template <int D, int ROT>
+__device__ __forceinline__ void load_angles(const QkvParams& p, int64_t at, int j, Angles<ROT>& w) {
+  constexpr int LPH = D / 16;
+  const float* cs = p.table + at * p.rot;
+  const int half = p.rot / 2;
+  if (ROT == kHalves) {
+    load8(cs + 8 * j, w.c);
+    load8(cs + half + 8 * j, w.s);
+  } else if (ROT == kPairs) {
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const int ch = j + b * LPH;                // pairs 4 ch .. 4 ch + 3
+      if (ch * 8 >= p.rot) continue;
+      const float4 x = __ldg(reinterpret_cast<const float4*>(cs + 4 * ch));
+      const float4 y = __ldg(reinterpret_cast<const float4*>(cs + half + 4 * ch));
+      w.c[4 * b] = x.x; w.c[4 * b + 1] = x.y; w.c[4 * b + 2] = x.z; w.c[4 * b + 3] = x.w;
+      w.s[4 * b] = y.x; w.s[4 * b + 1] = y.y; w.s[4 * b + 2] = y.z; w.s[4 * b + 3] = y.w;
+    }
+  } else if (ROT == kPart) {
+    const int hc = half / 8;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const int ch = j + b * LPH, i = ch < hc ? ch : ch - hc;
+      if (ch >= 2 * hc) continue;
+      load8(cs + 8 * i, w.c + 8 * b % (ROT == kPart ? 16 : 8));
+      load8(cs + half + 8 * i, w.s + 8 * b % (ROT == kPart ? 16 : 8));
     }
   }
-  // the heads of q, k and v in one row: head hh is this thread's
-  const int hh = (int)(w % passes) * HPW + lane / LPH;
-  const int kind = hh < p.Hq ? 0 : hh < p.Hq + p.Hkv ? 1 : p.slots && hh < p.Hq + 2 * p.Hkv ? 2 : 3;
-  const int h = kind == 0 ? hh : kind == 1 ? hh - p.Hq : hh - p.Hq - p.Hkv;
-  const uint16_t* src = kind == 0 ? p.q + tok * p.qs : kind == 1 ? p.k + tok * p.ks : p.v + tok * p.vs;
-  const uint16_t* wgt = kind == 0 ? p.wq : kind == 1 ? p.wk : nullptr;
+}
+
+// x: chunk j of a head, then chunk j + D / 16
+template <int D, int ROT>
+__device__ __forceinline__ void rotate(const QkvParams& p, int j, int lane, const Angles<ROT>& w, float* x) {
+  constexpr int LPH = D / 16;
+  if (ROT == kHalves) {
+    const uint64_t minus = f2pack(-1.f, -1.f);
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      const uint64_t a = f2pack(x[i], x[i + 1]), b = f2pack(x[i + 8], x[i + 9]);
+      const uint64_t c = f2pack(w.c[i], w.c[i + 1]), s = f2pack(w.s[i], w.s[i + 1]);
+      f2unpack(ffma2(mul2(b, s), minus, mul2(a, c)), x[i], x[i + 1]);
+      f2unpack(fadd2(mul2(b, c), mul2(a, s)), x[i + 8], x[i + 9]);
+    }
+  } else if (ROT == kPairs) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if ((j + i / 4 * LPH) * 8 < p.rot) turn(x[2 * i], x[2 * i + 1], w.c[i], w.s[i]);
+  } else if (ROT == kPart) {
+    // chunk ch < rot / 16 pairs with chunk ch + rot / 16, which another thread of the head may hold
+    const int hc = p.rot / 16;
+    float other[16];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const int ch = j + b * LPH;
+      const int pc = ch < hc ? ch + hc : ch < 2 * hc ? ch - hc : ch;
+      const int from = (lane & ~(LPH - 1)) | (pc & (LPH - 1));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        // not all that ask a thread want the same of its chunks: both cross
+        const float lo = __shfl_sync(0xffffffffu, x[i], from), hi = __shfl_sync(0xffffffffu, x[i + 8], from);
+        other[8 * b + i] = pc < LPH ? lo : hi;
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const int ch = j + b * LPH;
+      if (ch >= 2 * hc) continue;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int k = (8 * b + i) % (ROT == kPart ? 16 : 8);
+        float mine = x[8 * b + i], theirs = other[8 * b + i];
+        if (ch < hc)
+          turn(mine, theirs, w.c[k], w.s[k]);
+        else
+          turn(theirs, mine, w.c[k], w.s[k]);
+        x[8 * b + i] = mine;
+      }
+    }
+  }
+}
+
+// Codes and scales of a thread's chunks y0 and y1 (bf16) of head h, K or V, to its token's row; all threads of the
+// warp call it, those with ok store.
+template <int D>
+__device__ __forceinline__ void store_codes(uint4 y0, uint4 y1, uint8_t* row, int hkv, int h, bool is_v, int j, bool ok) {
+  constexpr int LPH = D / 16;
   float x[16];
-  if (kind < 3) {
-    unpack8(reinterpret_cast<const uint4*>(src + h * D)[j], x);
-    unpack8(reinterpret_cast<const uint4*>(src + h * D)[j + LPH], x + 8);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = 0.f;
-  }
-  if (p.wq || p.wk) {
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) ss = fmaf(x[i], x[i], ss);
-#pragma unroll
-    for (int off = 1; off < LPH; off <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-    if (wgt) {
-      const float r = rsqrtf(ss * (1.f / D) + p.eps);
-      float g[16];
-      unpack8(reinterpret_cast<const uint4*>(wgt)[j], g);
-      unpack8(reinterpret_cast<const uint4*>(wgt)[j + LPH], g + 8);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = __fmul_rn(__fmul_rn(x[i], r), g[i]);
-    }
-  }
-  if (ROT != kNone) {
-    const float* cs = p.table + at * p.rot;
-    const int half = p.rot / 2;
-    if (ROT == kHalves) {
-      float c[8], s[8];
-      load8(cs + 8 * j, c);
-      load8(cs + half + 8 * j, s);
-      if (kind < 2) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) turn(x[i], x[i + 8], c[i], s[i]);
-      }
-    } else if (ROT == kPairs) {
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const int ch = j + b * LPH;            // chunk: pairs 4 ch .. 4 ch + 3
-        if (kind < 2 && ch * 8 < p.rot) {
-          const float4 c = __ldg(reinterpret_cast<const float4*>(cs + 4 * ch));
-          const float4 s = __ldg(reinterpret_cast<const float4*>(cs + half + 4 * ch));
-          float* y = x + 8 * b;
-          turn(y[0], y[1], c.x, s.x);
-          turn(y[2], y[3], c.y, s.y);
-          turn(y[4], y[5], c.z, s.z);
-          turn(y[6], y[7], c.w, s.w);
-        }
-      }
-    } else {
-      // chunk ch < half / 8 pairs with chunk ch + half / 8, which another thread of the head holds
-      const int hc = half / 8;
-      float other[16];
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const int ch = j + b * LPH;
-        const int pc = ch < hc ? ch + hc : ch < 2 * hc ? ch - hc : ch;
-        const int from = (lane & ~(LPH - 1)) | (pc & (LPH - 1));
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float lo = __shfl_sync(0xffffffffu, x[i], from), hi = __shfl_sync(0xffffffffu, x[i + 8], from);
-          other[8 * b + i] = pc < LPH ? lo : hi;
-        }
-      }
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const int ch = j + b * LPH;
-        if (kind < 2 && ch < 2 * hc) {
-          float c[8], s[8];
-          load8(cs + 8 * (ch < hc ? ch : ch - hc), c);
-          load8(cs + half + 8 * (ch < hc ? ch : ch - hc), s);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            float mine = x[8 * b + i], theirs = other[8 * b + i];
-            if (ch < hc)
-              turn(mine, theirs, c[i], s[i]);
-            else
-              turn(theirs, mine, c[i], s[i]);
-            x[8 * b + i] = mine;
-          }
-        }
-      }
-    }
-  }
-  const uint4 y0 = pack8(x), y1 = pack8(x + 8);
-  if (kind < 2) {
-    uint16_t* out = kind == 0 ? p.q_out + tok * p.qos : p.k_out ? p.k_out + tok * p.kos : nullptr;
-    if (out) {
-      reinterpret_cast<uint4*>(out + h * D)[j] = y0;
-      reinterpret_cast<uint4*>(out + h * D)[j + LPH] = y1;
-    }
-  }
-  if (!p.slots) return;
-  if (__all_sync(0xffffffffu, kind == 0)) return;
-  const int64_t slot = p.slots[tok];
-  const bool ok = slot >= 0 && slot < p.num_slots;
-  if (!ok && kind == 1 && h == 0 && j == 0) report_error(p.err, kErrBounds);
-  if (!KV4) {
-    if (ok && (kind == 1 || kind == 2)) {
-      uint16_t* out = (kind == 1 ? p.cold_k : p.cold_v) + (slot * p.Hkv + h) * D;
-      reinterpret_cast<uint4*>(out)[j] = y0;
-      reinterpret_cast<uint4*>(out)[j + LPH] = y1;
-    }
-    return;
-  }
-  // 4-bit rows: of the bf16 values
   unpack8(y0, x);
   unpack8(y1, x + 8);
   float lo[2] = {x[0], x[8]}, hi[2] = {x[0], x[8]};
@@ -251,10 +239,9 @@ __global__ void __launch_bounds__(32 * kWarps) qkv_kernel(const QkvParams p, int
       lo[g] = min_nan(lo[g], __shfl_xor_sync(0xffffffffu, lo[g], off));
       hi[g] = max_nan(hi[g], __shfl_xor_sync(0xffffffffu, hi[g], off));
     }
-  if (!ok || kind == 0 || kind == 3) return;
-  uint8_t* row = p.rows + slot * kv4::row_bytes(p.Hkv, D);
-  uint8_t* codes = row + kv4::codes_at(h, D) + (kind == 2 ? D / 2 : 0);
-  uint8_t* scales = row + kv4::scales_at(p.Hkv, h, D) + (kind == 2 ? D / 16 : 0);
+  if (!ok) return;
+  uint8_t* codes = row + kv4::codes_at(h, D) + (is_v ? D / 2 : 0);
+  uint8_t* scales = row + kv4::scales_at(hkv, h, D) + (is_v ? D / 16 : 0);
   float span;
   const uint32_t s0 = group_scale(lo[0], hi[0], span);
   const uint32_t c0 = codes8(x, lo[0], span);
@@ -266,6 +253,117 @@ __global__ void __launch_bounds__(32 * kWarps) qkv_kernel(const QkvParams p, int
     const uint32_t s1 = group_scale(lo[1], hi[1], span);
     reinterpret_cast<uint2*>(codes)[j] = make_uint2(c0, codes8(x + 8, lo[1], span));
     if (j == 0) *reinterpret_cast<uint2*>(scales) = make_uint2(s0, s1);
+  }
+}
+
+// A warp takes passes [part * chunk, (part + 1) * chunk) of a token's: its heads of q, of k and of v, HPW at a time.  Their
+// rows are asked for at once, into shared memory; angles and weights are loaded once for all.
+// GB300, 16384 tokens of 32/8 heads of 128, normed (344 MB): 77 us with a pass a warp, 75 with four a warp unrolled (290
+// instructions a pass), 66 with two passes ahead in registers, 58 as it is, 5.9 TB/s; a copy of the same bytes takes 50.
+// Small blocks and many of them (seven of four warps an SM) hide the chain position -> angles -> first pass.
+template <int D, int ROT, bool KV4>
+__global__ void __launch_bounds__(32 * kWarps, KV4 ? 6 : 7) qkv_kernel(const QkvParams p, int passes, int parts, int chunk) {
+  constexpr int LPH = D / 16;       // lanes of a head
+  constexpr int HPW = 32 / LPH;     // heads of a pass
+  griddep_launch_dependents();
+  griddep_wait();
+  const int lane = threadIdx.x & 31, j = lane % LPH;
+  const int64_t w = blockIdx.x * (int64_t)kWarps + (threadIdx.x >> 5);
+  const int64_t tok = w / parts;
+  if (tok >= p.n) return;
+  const int first = (int)(w - tok * parts) * chunk, end = min(passes, first + chunk);
+  const int q_passes = (p.Hq + HPW - 1) / HPW, k_end = q_passes + (p.Hkv + HPW - 1) / HPW;
+  const uint16_t* const src_q = p.q + tok * p.qs + 8 * j;
+  const uint16_t* const src_k = p.k + tok * p.ks + 8 * j;
+  const uint16_t* const src_v = p.v + tok * p.vs + 8 * j;
+  // pass i is of q, k or v (kind 0, 1, 2), head h this thread's
+  auto kind_of = [&](int i) { return i < q_passes ? 0 : i < k_end ? 1 : 2; };
+  auto head_of = [&](int i, int kind) {
+    return (i - (kind == 0 ? 0 : kind == 1 ? q_passes : k_end)) * HPW + lane / LPH;
+  };
+  // every pass's rows are asked for at once, each thread's chunks to its own places: no thread waits for another's
+  extern __shared__ __align__(16) uint4 rows[];
+  uint4* const buf = rows + (threadIdx.x >> 5) * chunk * 64 + lane;
+#pragma unroll 1
+  for (int i = first; i < end; ++i) {
+    const int kind = kind_of(i), h = head_of(i, kind);
+    const uint16_t* src = (kind == 0 ? src_q : kind == 1 ? src_k : src_v) + h * D;
+    if (h < (kind == 0 ? p.Hq : p.Hkv)) {
+      const uint32_t dst = smem_u32(buf + (i - first) * 64);
+      cp_async16(dst, src);
+      cp_async16(dst + 512, src + 8 * LPH);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  for (int i = end - first; i < kChunk; ++i) asm volatile("cp.async.commit_group;" ::: "memory");
+  int64_t slot = -1;
+  if (p.slots) slot = p.slots[tok];
+  Angles<ROT> angles;
+  if (ROT != kNone) {
+    const int64_t at = p.pos[tok];
+    if (at < 0 || at >= p.num_pos) {
+      if (lane == 0) report_error(p.err, kErrBounds);
+      return;
+    }
+    if (first < k_end) load_angles<D, ROT>(p, at, j, angles);
+  }
+  const bool stored = slot >= 0 && slot < p.num_slots;
+  if (p.slots && !stored && first == 0 && lane == 0) report_error(p.err, kErrBounds);
+  float g[16];                      // the weights of the kind that was normed last
+  int of = -1;
+#pragma unroll 1
+  for (int i = first; i < end; ++i) {
+    const int kind = kind_of(i), h = head_of(i, kind);
+    const bool mine = h < (kind == 0 ? p.Hq : p.Hkv);
+    // a group a pass, and one more for each pass done: all but the last kChunk - 1 have landed
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    asm volatile("cp.async.wait_group %0;" ::"n"(kChunk - 1) : "memory");
+    uint4 y0 = buf[(i - first) * 64], y1 = buf[(i - first) * 64 + 32];
+    if (kind < 2) {
+      float x[16];
+      unpack8(y0, x);
+      unpack8(y1, x + 8);
+      const uint16_t* weight = kind == 0 ? p.wq : p.wk;
+      if (weight) {
+        if (of != kind) {
+          of = kind;
+          unpack8(reinterpret_cast<const uint4*>(weight)[j], g);
+          unpack8(reinterpret_cast<const uint4*>(weight)[j + LPH], g + 8);
+        }
+        uint64_t sum = 0;
+#pragma unroll
+        for (int k = 0; k < 16; k += 2) {
+          const uint64_t v = f2pack(x[k], x[k + 1]);
+          sum = ffma2(v, v, sum);
+        }
+        float ss, odd;
+        f2unpack(sum, ss, odd);
+        ss += odd;
+#pragma unroll
+        for (int off = 1; off < LPH; off <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+        const float r = rsqrtf(ss * (1.f / D) + p.eps);
+        const uint64_t rr = f2pack(r, r);
+#pragma unroll
+        for (int k = 0; k < 16; k += 2)
+          f2unpack(mul2(mul2(f2pack(x[k], x[k + 1]), rr), f2pack(g[k], g[k + 1])), x[k], x[k + 1]);
+      }
+      rotate<D, ROT>(p, j, lane, angles, x);
+      y0 = pack8(x);
+      y1 = pack8(x + 8);
+      uint16_t* out = kind == 0 ? p.q_out + tok * p.qos : p.k_out ? p.k_out + tok * p.kos : nullptr;
+      if (out && mine) {
+        *reinterpret_cast<uint4*>(out + h * D + 8 * j) = y0;
+        *reinterpret_cast<uint4*>(out + h * D + 8 * (j + LPH)) = y1;
+      }
+      if (kind == 0 || !p.slots) continue;
+    }
+    if (KV4) {
+      store_codes<D>(y0, y1, p.rows + slot * kv4::row_bytes(p.Hkv, D), p.Hkv, h, kind == 2, j, stored && mine);
+    } else if (stored && mine) {
+      uint16_t* out = (kind == 1 ? p.cold_k : p.cold_v) + (slot * p.Hkv + h) * D + 8 * j;
+      *reinterpret_cast<uint4*>(out) = y0;
+      *reinterpret_cast<uint4*>(out + 8 * LPH) = y1;
+    }
   }
 }
 
@@ -288,44 +386,64 @@ __device__ __forceinline__ uint4 values8(uint32_t w, float lo, float step) {
   return pack8(x);
 }
 
-template <int D, bool KV4>
-__global__ void __launch_bounds__(32 * kWarps) read_kernel(const ReadParams p, int passes) {
+template <int D, bool KV4, int U>
+__global__ void __launch_bounds__(32 * kWarps) read_kernel(const ReadParams p, int warps_per_token) {
   constexpr int LPH = D / 16, HPW = 32 / LPH;
   griddep_launch_dependents();
   griddep_wait();
   const int lane = threadIdx.x & 31, j = lane % LPH;
   const int64_t w = blockIdx.x * (int64_t)kWarps + (threadIdx.x >> 5);
-  const int64_t tok = w / passes;
-  const int hh = (int)(w % passes) * HPW + lane / LPH;
-  if (tok >= p.n || hh >= 2 * p.Hkv) return;
-  const bool is_v = hh >= p.Hkv;
-  const int h = is_v ? hh - p.Hkv : hh;
+  const int64_t tok = w / warps_per_token;
+  if (tok >= p.n) return;
+  const int hh0 = (int)(w % warps_per_token) * HPW * U + lane / LPH;
   const int64_t slot = p.slots[tok];
-  uint4 y0 = make_uint4(0, 0, 0, 0), y1 = y0;
-  if (slot < 0 || slot >= p.num_slots) {
-    if (hh == 0 && j == 0) report_error(p.err, kErrBounds);
-  } else if (KV4) {
-    const uint8_t* row = p.rows + slot * kv4::row_bytes(p.Hkv, D);
-    const uint8_t* codes = row + kv4::codes_at(h, D) + (is_v ? D / 2 : 0);
-    const uint32_t* scales = reinterpret_cast<const uint32_t*>(row + kv4::scales_at(p.Hkv, h, D) + (is_v ? D / 16 : 0));
-    const uint32_t s0 = scales[0], s1 = scales[D / 64 - 1];
-    uint2 c;
-    if (D == 64) {
-      c.x = reinterpret_cast<const uint32_t*>(codes)[j];
-      c.y = reinterpret_cast<const uint32_t*>(codes)[j + LPH];
+  const bool ok = slot >= 0 && slot < p.num_slots;
+  if (!ok && hh0 == 0 && j == 0) report_error(p.err, kErrBounds);
+  // every pass's loads before the first is used
+  uint4 y[U][2];
+  uint32_t sc[U][2];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int hh = hh0 + u * HPW;
+    const bool is_v = hh >= p.Hkv;
+    const int h = is_v ? hh - p.Hkv : hh;
+    y[u][0] = y[u][1] = make_uint4(0, 0, 0, 0);
+    sc[u][0] = sc[u][1] = 0;
+    if (!ok || hh >= 2 * p.Hkv) continue;
+    if (KV4) {
+      const uint8_t* row = p.rows + slot * kv4::row_bytes(p.Hkv, D);
+      const uint32_t* codes = reinterpret_cast<const uint32_t*>(row + kv4::codes_at(h, D) + (is_v ? D / 2 : 0));
+      const uint32_t* scales = reinterpret_cast<const uint32_t*>(row + kv4::scales_at(p.Hkv, h, D) + (is_v ? D / 16 : 0));
+      if (D == 64) {
+        y[u][0].x = codes[j];
+        y[u][1].x = codes[j + LPH];
+        sc[u][0] = sc[u][1] = scales[0];
+      } else {
+        const uint2 c = reinterpret_cast<const uint2*>(codes)[j], s = *reinterpret_cast<const uint2*>(scales);
+        y[u][0].x = c.x;
+        y[u][1].x = c.y;
+        sc[u][0] = s.x;
+        sc[u][1] = s.y;
+      }
     } else {
-      c = reinterpret_cast<const uint2*>(codes)[j];
+      const uint16_t* src = (is_v ? p.cold_v : p.cold_k) + (slot * p.Hkv + h) * D;
+      y[u][0] = load_once(src + 8 * j);
+      y[u][1] = load_once(src + 8 * (j + LPH));
     }
-    y0 = values8(c.x, bf_lo(s0), __fdiv_rn(bf_hi(s0), 15.f));
-    y1 = values8(c.y, bf_lo(s1), __fdiv_rn(bf_hi(s1), 15.f));
-  } else {
-    const uint4* src = reinterpret_cast<const uint4*>((is_v ? p.cold_v : p.cold_k) + (slot * p.Hkv + h) * D);
-    y0 = src[j];
-    y1 = src[j + LPH];
   }
-  uint4* out = reinterpret_cast<uint4*>((is_v ? p.v + tok * p.vs : p.k + tok * p.ks) + h * D);
-  out[j] = y0;
-  out[j + LPH] = y1;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int hh = hh0 + u * HPW;
+    if (hh >= 2 * p.Hkv) continue;
+    const bool is_v = hh >= p.Hkv;
+    uint4* out = reinterpret_cast<uint4*>(is_v ? p.v + tok * p.vs + (hh - p.Hkv) * D : p.k + tok * p.ks + hh * D);
+    if (KV4) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b) y[u][b] = values8(y[u][b].x, bf_lo(sc[u][b]), __fdiv_rn(bf_hi(sc[u][b]), 15.f));
+    }
+    out[j] = y[u][0];
+    out[j + LPH] = y[u][1];
+  }
 }
 
 // One CTA per copy-on-write pair: the rows of a block, 16 bytes at a time.
@@ -342,20 +460,26 @@ __global__ void kv4_cow_kernel(uint4* layer, int64_t block_vecs, int64_t n_block
     layer[dst * block_vecs + i] = layer[src * block_vecs + i];
 }
 
+template <int D, int ROT, bool KV4>
+int launch_qkv_u(const QkvParams& p, int num_sms, cudaStream_t st) {
+  const int per = 512 / D, kv = (p.Hkv + per - 1) / per, passes = (p.Hq + per - 1) / per + kv * (p.slots ? 2 : 1);
+  // one pass a warp while the SMs (64 warps each) hold them all: the shortest way for a few tokens.  Else about kChunk
+  const int chunk = (int64_t)p.n * passes <= (int64_t)num_sms * kFewWarps ? 1 : kChunk;
+  const int parts = (passes + chunk - 1) / chunk, each = (passes + parts - 1) / parts;
+  const int64_t blocks = ((int64_t)p.n * parts + kWarps - 1) / kWarps;
+  return (int)launch_pdl(qkv_kernel<D, ROT, KV4>, dim3((unsigned)blocks), dim3(32 * kWarps), kWarps * each * 1024, st, p, passes, parts, each);
+}
+
 template <int D, int ROT>
-int launch_qkv_t(bool kv4, const QkvParams& p, cudaStream_t st) {
-  const int heads = p.Hq + p.Hkv * (p.slots ? 2 : 1);
-  const int passes = (heads + 512 / D - 1) / (512 / D);
-  const int64_t blocks = ((int64_t)p.n * passes + kWarps - 1) / kWarps;
-  auto kern = kv4 ? qkv_kernel<D, ROT, true> : qkv_kernel<D, ROT, false>;
-  return (int)launch_pdl(kern, dim3((unsigned)blocks), dim3(32 * kWarps), 0, st, p, passes);
+int launch_qkv_t(bool kv4, const QkvParams& p, int num_sms, cudaStream_t st) {
+  return kv4 ? launch_qkv_u<D, ROT, true>(p, num_sms, st) : launch_qkv_u<D, ROT, false>(p, num_sms, st);
 }
 
 template <int D>
-int launch_qkv_d(bool kv4, const QkvParams& p, bool interleaved, cudaStream_t st) {
-  if (p.rot == 0) return launch_qkv_t<D, kNone>(kv4, p, st);
-  if (interleaved) return launch_qkv_t<D, kPairs>(kv4, p, st);
-  return p.rot == D ? launch_qkv_t<D, kHalves>(kv4, p, st) : launch_qkv_t<D, kPart>(kv4, p, st);
+int launch_qkv_d(bool kv4, const QkvParams& p, bool interleaved, int num_sms, cudaStream_t st) {
+  if (p.rot == 0) return launch_qkv_t<D, kNone>(kv4, p, num_sms, st);
+  if (interleaved) return launch_qkv_t<D, kPairs>(kv4, p, num_sms, st);
+  return p.rot == D ? launch_qkv_t<D, kHalves>(kv4, p, num_sms, st) : launch_qkv_t<D, kPart>(kv4, p, num_sms, st);
 }
 
 }  // namespace
@@ -405,8 +529,8 @@ int launch_qkv(const LaunchCommon& lc, void* stream, bool kv4, int32_t layer, co
   }
   p.err = lc.d_error;
   cudaStream_t st = (cudaStream_t)stream;
-  return c.head_dim == 128 ? launch_qkv_d<128>(kv4, p, x->interleaved != 0, st)
-                           : launch_qkv_d<64>(kv4, p, x->interleaved != 0, st);
+  return c.head_dim == 128 ? launch_qkv_d<128>(kv4, p, x->interleaved != 0, lc.num_sms, st)
+                           : launch_qkv_d<64>(kv4, p, x->interleaved != 0, lc.num_sms, st);
 }
 
 int launch_read_kv(const LaunchCommon& lc, void* stream, bool kv4, int32_t layer, int64_t n, const int64_t* d_slots,
@@ -430,10 +554,15 @@ int launch_read_kv(const LaunchCommon& lc, void* stream, bool kv4, int32_t layer
   p.Hkv = c.num_kv_heads;
   p.err = lc.d_error;
   const int per = 512 / c.head_dim, passes = (2 * c.num_kv_heads + per - 1) / per;
-  const int64_t blocks = (n * passes + kWarps - 1) / kWarps;
-  auto kern = c.head_dim == 128 ? (kv4 ? read_kernel<128, true> : read_kernel<128, false>)
-                                : (kv4 ? read_kernel<64, true> : read_kernel<64, false>);
-  return (int)launch_pdl(kern, dim3((unsigned)blocks), dim3(32 * kWarps), 0, (cudaStream_t)stream, p, passes);
+  const int u = n * passes <= (int64_t)lc.num_sms * kFewWarps ? 1 : 4;
+  const int warps = (passes + u - 1) / u;
+  const int64_t blocks = (n * warps + kWarps - 1) / kWarps;
+  auto kern = c.head_dim == 128
+                  ? (u == 1 ? (kv4 ? read_kernel<128, true, 1> : read_kernel<128, false, 1>)
+                            : (kv4 ? read_kernel<128, true, 4> : read_kernel<128, false, 4>))
+                  : (u == 1 ? (kv4 ? read_kernel<64, true, 1> : read_kernel<64, false, 1>)
+                            : (kv4 ? read_kernel<64, true, 4> : read_kernel<64, false, 4>));
+  return (int)launch_pdl(kern, dim3((unsigned)blocks), dim3(32 * kWarps), 0, (cudaStream_t)stream, p, warps);
 }
 
 }  // namespace gk
