@@ -93,6 +93,11 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
   else
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ __forceinline__ uint2 lds64(uint32_t addr) {
   uint2 v;
   asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
@@ -405,7 +410,8 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) d[u][i] = sc[u][i] - m[i & 1];
+        for (int i = 0; i < 4; i += 2)
+          f2unpack(fadd2(f2pack(sc[u][i], sc[u][i + 1]), f2pack(-m[0], -m[1])), d[u][i], d[u][i + 1]);
       // (the span is a word's high half and not negative: words order as their spans)
       int32_t top = 0;
 #pragma unroll
@@ -458,18 +464,28 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         uint32_t b[NG][2];
+        float e[4];                    // rows a and b of head 2 tq, then of head 2 tq + 1
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const float p0 = ex2(d[u][2 * r]), p1 = ex2(d[u][2 * r + 1]);
-          l[0] += p0;
-          l[1] += p1;
+        for (int i = 0; i < 4; ++i) e[i] = ex2(d[u][i]);
+        l[0] += e[0];
+        l[0] += e[2];
+        l[1] += e[1];
+        l[1] += e[3];
+        const uint64_t vv = f2pack(vs, vs), e0 = f2pack(e[0], e[2]), e1 = f2pack(e[1], e[3]);
 #pragma unroll
-          for (int g = 0; g < NG; ++g) {
-            const float span = bf_hi(vscale[u][r][g]) * vs, lo = bf_lo(vscale[u][r][g]);
-            R[g][0] = fmaf(p0, lo, R[g][0]);
-            R[g][1] = fmaf(p1, lo, R[g][1]);
-            b[g][r] = transpose8x8(pack_f16x2(p0 * span, p1 * span));
-          }
+        for (int g = 0; g < NG; ++g) {
+          const uint32_t wa = vscale[u][0][g], wb = vscale[u][1][g];
+          const float la = bf_lo(wa), lb = bf_lo(wb);
+          R[g][0] = fmaf(e[0], la, R[g][0]);
+          R[g][1] = fmaf(e[1], la, R[g][1]);
+          R[g][0] = fmaf(e[2], lb, R[g][0]);
+          R[g][1] = fmaf(e[3], lb, R[g][1]);
+          const uint64_t span = mul2(f2pack(bf_hi(wa), bf_hi(wb)), vv);
+          float a0, b0, a1, b1;
+          f2unpack(mul2(e0, span), a0, b0);
+          f2unpack(mul2(e1, span), a1, b1);
+          b[g][0] = transpose8x8(pack_f16x2(a0, a1));
+          b[g][1] = transpose8x8(pack_f16x2(b0, b1));
         }
         // tokens tq, tq + 4, tq + 8, tq + 12 of the tile
         uint32_t w[4][NG];
