@@ -714,7 +714,8 @@ int launch_kv4_join(const LaunchCommon& lc, void* stream, const gk_batch* b, con
   const gk_pool_config& c = *lc.cfg;
   const int64_t rows = (int64_t)pl->B * c.num_q_heads;
   const int most = pl->kv4_most_states;
-  const int warps = most <= 8 ? 1 : most <= 64 ? 8 : 32;
+  // a warp a row while two rounds hold its states, or while the rows alone fill the SMs
+  const int warps = most <= 16 || rows >= 32 * (int64_t)lc.num_sms ? 1 : most <= 64 ? 8 : 32;
   auto kern = c.head_dim == 128
                   ? (warps == 1 ? kv4_join_kernel<128, 1> : warps == 8 ? kv4_join_kernel<128, 8> : kv4_join_kernel<128, 32>)
                   : (warps == 1 ? kv4_join_kernel<64, 1> : warps == 8 ? kv4_join_kernel<64, 8> : kv4_join_kernel<64, 32>);

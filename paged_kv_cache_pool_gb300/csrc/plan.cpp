@@ -125,7 +125,7 @@ size_t append_region(size_t* off, size_t count, size_t align = 16) {
 // Split the concatenated token stream of all requests (lengths n[r]) into CTA
 // quotas; each CTA's slice becomes one segment per request it touches.
 void partition_tokens(const std::vector<int64_t>& n, int64_t max_ctas, std::vector<int32_t>* begin,
-                      std::vector<SegmentDev>* segs, int64_t quantum = kGatherQuantum) {
+                      std::vector<SegmentDev>* segs) {
   begin->clear();
   segs->clear();
   int64_t total = 0;
@@ -134,7 +134,7 @@ void partition_tokens(const std::vector<int64_t>& n, int64_t max_ctas, std::vect
   if (total == 0) return;
   int64_t quota = (total + max_ctas - 1) / max_ctas;
   quota = std::max<int64_t>(quota, kMinGatherQuota);
-  quota = (quota + quantum - 1) / quantum * quantum;
+  quota = (quota + kGatherQuantum - 1) / kGatherQuantum * kGatherQuantum;
   int64_t left = quota;
   for (size_t r = 0; r < n.size(); ++r) {
     int64_t t = 0;
@@ -202,9 +202,50 @@ bool partition_whole(const std::vector<int64_t>& n, int64_t max_ctas, std::vecto
 }
 
 // The 4-bit gather's work of each CTA: whole requests where that is no further from equal shares than a join costs, else
-// the stream cut into equal quotas of whole stages.
+// the stream cut so that the CTAs cost the same: a piece of a request costs its stages and kPieceTokens more, for the query
+// that it loads and the state that it writes.  A cut moves to a request's end that is near.
+constexpr int64_t kPieceTokens = 32;
+bool fill_kv4(const std::vector<int64_t>& n, int64_t slots, int64_t budget, std::vector<int32_t>* begin,
+              std::vector<SegmentDev>* segs) {
+  begin->assign(1, 0);
+  segs->clear();
+  auto stages = [](int64_t tokens) { return (tokens + kKv4Tokens - 1) / kKv4Tokens * kKv4Tokens; };
+  int64_t left = budget;
+  for (size_t r = 0; r < n.size(); ++r)
+    for (int64_t t = 0; t < n[r];) {
+      int64_t take = n[r] - t;
+      const int64_t room = (left - kPieceTokens) / kKv4Tokens * kKv4Tokens;
+      if (stages(take) > room + kKv4Tokens) take = room;
+      if (take < std::min<int64_t>(kMinGatherQuota, n[r] - t)) {   // too little room: the next CTA's
+        if (left == budget) return false;
+        begin->push_back((int32_t)segs->size());
+        left = budget;
+        if ((int64_t)begin->size() > slots) return false;
+        continue;
+      }
+      segs->push_back(SegmentDev{(int32_t)r, (int32_t)t, (int32_t)(t + take), -1});
+      t += take;
+      left -= stages(take) + kPieceTokens;
+    }
+  if (begin->back() != (int32_t)segs->size()) begin->push_back((int32_t)segs->size());
+  return (int64_t)begin->size() - 1 <= slots;
+}
+
 void partition_kv4(const std::vector<int64_t>& n, int64_t slots, std::vector<int32_t>* begin, std::vector<SegmentDev>* segs) {
-  if (!partition_whole(n, slots, begin, segs)) partition_tokens(n, slots, begin, segs, kKv4Tokens);
+  if (partition_whole(n, slots, begin, segs)) return;
+  int64_t total = 0;
+  for (int64_t x : n) total += x;
+  // the least budget that the slots suffice for, to half a stage or 0.4 %
+  int64_t lo = std::max<int64_t>(kMinGatherQuota + kPieceTokens, total / slots), hi = lo;
+  while (!fill_kv4(n, slots, hi, begin, segs)) hi += std::max<int64_t>(hi / 2, kKv4Tokens);
+  while (hi - lo > std::max<int64_t>(kKv4Tokens / 2, hi / 256)) {
+    const int64_t mid = (lo + hi) / 2;
+    if (fill_kv4(n, slots, mid, begin, segs))
+      hi = mid;
+    else
+      lo = mid;
+  }
+  fill_kv4(n, slots, hi, begin, segs);
 }
 
 // Tangram's ahead-of-time work partitioning (Algorithm 1) with requests in the
