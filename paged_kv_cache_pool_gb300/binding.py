@@ -482,7 +482,7 @@ class Rope:
         """Fill the call's rows in: bf16 [n, heads, d] tensors (tokens may be strided) or addresses of packed rows."""
         c = self.c
         # what a layout was found to be when it came last (strides, heads and types: not what the tensors hold or where)
-        seen = (pool, n, _layout(q), _layout(q_out), _layout(k), _layout(k_out), _layout(v), _layout(positions))
+        seen = (_geometry.get(pool), n, _layout(q), _layout(q_out), _layout(k), _layout(k_out), _layout(v), _layout(positions))
         if seen != self.seen:
             self.seen = None
             self._check(pool, positions, q, k, v, q_out, k_out, n)
@@ -537,19 +537,29 @@ def gk_append_qkv(pool, stream, layer, rope, positions, d_slot_mapping, q, k, v,
         _check(st, pool)
 
 
+_read_seen = {}      # (geometry, layouts) of reads that were checked: the token strides of k and v
+
+
 def gk_read_kv(pool, stream, layer, d_slot_mapping, d_k, d_v, n=None):
     """K and V of the slots as bf16 [n, Hkv, d] (tokens may be strided)."""
     n = d_slot_mapping.numel() if n is None else n
-    torch = sys.modules.get("torch")
-    heads, dim = _geometry.get(pool, (None, None, None))[1:]
-    rows = []
-    for x, what in ((d_k, "k"), (d_v, "v")):
-        h, d, stride, at = _token_rows(x, n, what, torch)
-        if h is not None and heads is not None and (h != heads or d != dim):
-            raise ValueError(f"{what} must have the pool's {heads} heads of {dim}")
-        rows.append((at, stride))
-    slots = d_slot_mapping if isinstance(d_slot_mapping, int) else _gpu_row(d_slot_mapping, n, torch.int64, "the slot mapping")
-    st = lib().gk_read_kv(pool, _stream(stream), layer, n, slots, rows[0][0], rows[1][0], rows[0][1], rows[1][1])
+    seen = (_geometry.get(pool), n, _layout(d_slot_mapping), _layout(d_k), _layout(d_v))
+    strides = _read_seen.get(seen)
+    if strides is None:
+        torch = sys.modules.get("torch")
+        heads, dim = (seen[0] or (None, None, None))[1:]
+        strides = []
+        for x, what in ((d_k, "k"), (d_v, "v")):
+            h, d, stride, _ = _token_rows(x, n, what, torch)
+            if h is not None and heads is not None and (h != heads or d != dim):
+                raise ValueError(f"{what} must have the pool's {heads} heads of {dim}")
+            strides.append(stride)
+        if not isinstance(d_slot_mapping, int):
+            _gpu_row(d_slot_mapping, n, torch.int64, "the slot mapping")
+        if len(_read_seen) >= 256:
+            _read_seen.clear()
+        _read_seen[seen] = strides
+    st = (_lib or lib()).gk_read_kv(pool, _stream(stream), layer, n, _ptr(d_slot_mapping), _ptr(d_k), _ptr(d_v), *strides)
     if st:
         _check(st, pool)
 

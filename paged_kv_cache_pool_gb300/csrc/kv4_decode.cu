@@ -15,6 +15,7 @@
 // code + 16 * code', from whose sum the first one's is taken in the end: two instructions a byte pair, not five for two.  (As 8-bit floats
 // four codes would take one mask, but the warp-level products of 8-bit operands are made of conversions to fp16
 // and fp16 products on this chip: 608 requests of 2048 tokens 265 us, so 450.)
+#include <atomic>
 #include <cmath>
 
 #include "device_common.cuh"
@@ -651,8 +652,17 @@ template <int D, int G>
 int launch_gather_t(const Kv4Params& p, int ctas, cudaStream_t st) {
   const size_t smem = gather_smem(p.Hkv, D);
   auto kern = kv4_gather_kernel<D, G>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // once a device (64 of them; setting it again does no harm): the largest a CTA of any geometry takes
+  static std::atomic<uint64_t> set{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return (int)e;
+  const uint64_t bit = (uint64_t)1 << (dev & 63);
+  if (dev > 63 || !(set.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)gather_smem(kMaxKvHeads, D));
+    if (e != cudaSuccess) return (int)e;
+    set.fetch_or(bit, std::memory_order_relaxed);
+  }
   return (int)launch_pdl(kern, dim3(ctas), dim3(32 * p.Hkv), smem, st, p);
 }
 
