@@ -204,7 +204,7 @@ bool partition_whole(const std::vector<int64_t>& n, int64_t max_ctas, std::vecto
 // The 4-bit gather's work of each CTA: whole requests where that is no further from equal shares than a join costs, else
 // the stream cut so that the CTAs cost the same: a piece of a request costs its stages and kPieceTokens more, for the query
 // that it loads and the state that it writes.  A cut moves to a request's end that is near.
-constexpr int64_t kPieceTokens = 32;
+constexpr int64_t kPieceTokens = 32, kMostPieces = 512;
 bool fill_kv4(const std::vector<int64_t>& n, int64_t slots, int64_t budget, std::vector<int32_t>* begin,
               std::vector<SegmentDev>* segs) {
   begin->assign(1, 0);
@@ -233,10 +233,16 @@ bool fill_kv4(const std::vector<int64_t>& n, int64_t slots, int64_t budget, std:
 
 void partition_kv4(const std::vector<int64_t>& n, int64_t slots, std::vector<int32_t>* begin, std::vector<SegmentDev>* segs) {
   if (partition_whole(n, slots, begin, segs)) return;
-  int64_t total = 0;
-  for (int64_t x : n) total += x;
-  // the least budget that the slots suffice for, to half a stage or 0.4 %
-  int64_t lo = std::max<int64_t>(kMinGatherQuota + kPieceTokens, total / slots), hi = lo;
+  int64_t total = 0, most = 0;
+  for (int64_t x : n) {
+    total += x;
+    most = std::max(most, x);
+  }
+  // the least budget that the slots suffice for, to half a stage or 0.4 %, with at most kMostPieces of a request (where a
+  // CTA is one warp an SM has 15 of them, and the join of 2048 states took longer than the gather)
+  int64_t lo = std::max<int64_t>(kMinGatherQuota + kPieceTokens, total / slots);
+  lo = std::max(lo, most / kMostPieces + kPieceTokens);
+  int64_t hi = lo;
   while (!fill_kv4(n, slots, hi, begin, segs)) hi += std::max<int64_t>(hi / 2, kKv4Tokens);
   while (hi - lo > std::max<int64_t>(kKv4Tokens / 2, hi / 256)) {
     const int64_t mid = (lo + hi) / 2;
