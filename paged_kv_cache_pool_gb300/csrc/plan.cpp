@@ -241,7 +241,7 @@ void partition_kv4(const std::vector<int64_t>& n, int64_t slots, std::vector<int
   // the least budget that the slots suffice for, to half a stage or 0.4 %, with at most kMostPieces of a request (where a
   // CTA is one warp an SM has 15 of them, and the join of 2048 states took longer than the gather)
   int64_t lo = std::max<int64_t>(kMinGatherQuota + kPieceTokens, total / slots);
-  lo = std::max(lo, most / kMostPieces + kPieceTokens);
+  lo = std::max(lo, (most / kMostPieces + kKv4Tokens - 1) / kKv4Tokens * kKv4Tokens + kPieceTokens);
   int64_t hi = lo;
   while (!fill_kv4(n, slots, hi, begin, segs)) hi += std::max<int64_t>(hi / 2, kKv4Tokens);
   while (hi - lo > std::max<int64_t>(kKv4Tokens / 2, hi / 256)) {

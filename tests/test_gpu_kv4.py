@@ -190,6 +190,47 @@ def test_bad_blocks_count_as_zeros():
         s.close()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("page", [1, 4, 8, 32])
+def test_bad_blocks_in_both_ways_of_copying(d, page):
+    """Bad ids among good ones, alone, first and last of a stage, with pages of few tokens and of many."""
+    s = Step(d, 2, 3, [70, 33, page], page=page)
+    s.run()
+    s.check()
+    table = s.table.cpu().numpy().copy()
+    bad = [(0, 0), (0, (69 // page)), (0, min(33, 69) // page), (1, 32 // page), (2, 0)]
+    for r, b in bad:
+        table[r, b] = 1 << 30 if b % 2 else -7
+    s.table.copy_(torch.from_numpy(table))
+    s.run()
+    torch.cuda.synchronize()
+    assert s.eng.device_error() == gk.GK_ERR_DEVICE_BOUNDS
+    K, V, size = (x.copy() for x in values(s.eng.cold[1, s.slots].cpu().numpy(), 3, d))
+    at = np.cumsum([0, 70, 33, page])
+    for r, b in bad:
+        i = slice(at[r] + b * page, min(at[r + 1], at[r] + (b + 1) * page))
+        K[i], V[i], size[i] = 0, 0, 0
+    none = np.zeros((0, 3, d))
+    for r in range(3):
+        i = slice(at[r], at[r + 1])
+        check_attention(np64(s.out[r]), np64(s.lse[r]), attend(np64(s.q[r]), (none, none), (K[i], V[i], size[i])), f"request {r}")
+    s.close()
+
+
+@pytest.mark.parametrize("hkv", [1, 8])
+def test_more_segments_than_a_cta_keeps(hkv):
+    """Thousands of requests of a few tokens: a CTA's list of segments is longer than what it keeps of it."""
+    rnd = random.Random(3)
+    b = 11000 if hkv == 8 else 80000
+    s = Step(64, 1, hkv, [rnd.randint(1, 4) for _ in range(b)], page=2, layers=1, layer=0)
+    begin, segs = gk.gk_plan_segments(s.plan)
+    assert np.diff(begin).max() > 34 and len(segs) == b
+    s.run()
+    some = sorted(rnd.sample(range(b), 300)) + [b - 1]
+    s.check(requests=some)
+    s.close()
+
+
 def test_rows_behind_a_request_do_not_matter():
     """Pages' places past a request's length, and blocks that no table names, hold NaN; block ids past the length are never read."""
     s = Step(128, 4, 2, [17, 33, 1], page=16, wide=3)

@@ -1,6 +1,8 @@
 """4-bit pools and the calls on q, k, v rows without a GPU: sizes, plans and refusals."""
 import ctypes
+import random
 
+import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -90,6 +92,47 @@ def test_plans(gk, pool):
         assert info["num_partials"] > max(entries)
         assert all(b > a for a, b in zip(begin, begin[1:]))
         gk.gk_plan_destroy(plan)
+
+
+@pytest.mark.parametrize("d,hkv", [(128, 8), (64, 1), (128, 3), (64, 8)])
+def test_work_covers_every_token_once(gk, d, hkv):
+    """The gather's pieces: every token once and in order, as many CTAs as run at a time, pieces of at least 64 tokens but at ends,
+    partial states one run a request, whole requests alone where they fit."""
+    rnd = random.Random(d + hkv)
+    p = gk.gk_pool_create_kv4(1, hkv, hkv, d, 5000, 1 << 22, 1, 0)
+    base = gk.gk_prefix_alloc(p, 1000)
+    try:
+        for lens in ([1], [0, 0], [131072], [700] * 9, [20] * 400, [64] * 304, [65] * 305, [4096, 1, 0, 4095], [2] * 5000,
+                     [rnd.randint(1, 4096) for _ in range(368)], [rnd.randint(0, 70) for _ in range(900)], [100000] + [5] * 600):
+            for hot in (False, True):
+                n = len(lens)
+                b = gk.Batch([base if hot else -1] * n, [1000 if hot else 0] * n, lens, None, 131072)
+                plan = gk.gk_plan_build(p, b)
+                begin, segs = gk.gk_plan_segments(plan)
+                info = gk.gk_plan_info(plan)
+                got = {}
+                for r, t0, t1, _ in segs.tolist():
+                    assert t0 == got.get(r, 0) and t1 > t0
+                    got[r] = t1
+                assert all(got.get(r, 0) == x for r, x in enumerate(lens))
+                assert begin[0] == 0 and begin[-1] == len(segs) and (np.diff(begin) > 0).all()
+                assert len(begin) - 1 == info["suffix_ctas"] <= 152 * 16
+                pieces = np.bincount(segs[:, 0], minlength=n) if len(segs) else np.zeros(n, int)
+                assert pieces.max(initial=0) <= 513
+                for r, t0, t1, _ in segs.tolist():
+                    assert t1 - t0 >= 64 or t1 == lens[r] and (t0 == 0 or t1 - t0 >= 1)
+                entries = {}
+                for r, _, _, e in segs.tolist():
+                    if not hot and pieces[r] == 1:
+                        assert e == -1
+                    else:
+                        entries.setdefault(r, []).append(e)
+                every = [e for v in entries.values() for e in v]
+                assert len(set(every)) == len(every) and all(v == list(range(v[0], v[0] + len(v))) for v in entries.values())
+                assert not every or max(every) < info["num_partials"]
+                gk.gk_plan_destroy(plan)
+    finally:
+        gk.gk_pool_destroy(p)
 
 
 def test_calls_of_bf16_pools_refuse(gk, pool):
@@ -211,6 +254,11 @@ def test_tensors_of_rows(gk, pool):
                    dict(positions=OnGpu(torch.zeros(14, dtype=torch.int32)[::2])), dict(positions=torch.zeros(7, dtype=torch.int32))):
         with pytest.raises(ValueError):
             rope.set(pool, n=7, **rows(gk, **change))
+    # the same layouts for another pool: its geometry counts
+    other = gk.gk_pool_create(1, 16, 2, 128, 64, 64, 1)
+    with pytest.raises(ValueError, match="heads"):
+        rope.set(other, n=7, **rows(gk))
+    gk.gk_pool_destroy(other)
     with pytest.raises(ValueError, match="weights"):
         gk.Rope(None, None, False, bf16(64)).set(pool, n=7, **rows(gk))
     for bad in (torch.zeros(100, 64, dtype=torch.float64), torch.zeros(64), torch.zeros(64, 100).t()):
