@@ -93,6 +93,7 @@ struct Pool {
   gk_pool_config cfg{};
   bool has_device = false;
   bool kv4 = false;                  // COLD in 4-bit rows (cfg.cold_k; cfg.cold_v is null)
+  bool kv4_smem_set = false;         // the gather of the pool's geometry may take its shared memory
   HotAllocator hot;
   HotCache hot_cache;
   BlockManager cold;

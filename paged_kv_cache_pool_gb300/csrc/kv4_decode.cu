@@ -15,7 +15,6 @@
 // code + 16 * code', from whose sum the first one's is taken in the end: two instructions a byte pair, not five for two.  (As 8-bit floats
 // four codes would take one mask, but the warp-level products of 8-bit operands are made of conversions to fp16
 // and fp16 products on this chip: 608 requests of 2048 tokens 265 us, so 450.)
-#include <atomic>
 #include <cmath>
 
 #include "device_common.cuh"
@@ -196,7 +195,7 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
       const int t = lt + lane;
       const int b = p.page_shift >= 0 ? t >> p.page_shift : t / p.page;
       in_page = t - b * p.page;
-      if (lane < n) id = __ldg(ltab + b);
+      if (lane < n) id = __ldcg(ltab + b);
       lt += n;
       if (lt == lt1) {
         ++lsg;
@@ -335,8 +334,8 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
     float vs = 1.f;
     int32_t most = -1;                 // not chosen yet
 
-    for (int t = seg.y; t < seg.z; t += kTok) {
-      const int n = min(kTok, seg.z - t);
+    for (int left = seg.z - seg.y; left > 0; left -= kTok) {
+      const int n = min(kTok, left);
       issue(nid, id, in_page);
       lookup(nid, id, in_page);
       asm volatile("cp.async.wait_group %0;" ::"n"(NST - 1) : "memory");
@@ -649,19 +648,13 @@ __global__ void __launch_bounds__(WARPS > 8 ? 32 * WARPS : 256) kv4_join_kernel(
 size_t gather_smem(int hkv, int d) { return (size_t)hkv * kStages * stage_bytes(d); }
 
 template <int D, int G>
-int launch_gather_t(const Kv4Params& p, int ctas, cudaStream_t st) {
+int launch_gather_t(Pool* pool, const Kv4Params& p, int ctas, cudaStream_t st) {
   const size_t smem = gather_smem(p.Hkv, D);
   auto kern = kv4_gather_kernel<D, G>;
-  // once a device (64 of them; setting it again does no harm): the largest a CTA of any geometry takes
-  static std::atomic<uint64_t> set{0};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return (int)e;
-  const uint64_t bit = (uint64_t)1 << (dev & 63);
-  if (dev > 63 || !(set.load(std::memory_order_relaxed) & bit)) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)gather_smem(kMaxKvHeads, D));
+  if (!pool->kv4_smem_set) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return (int)e;
-    set.fetch_or(bit, std::memory_order_relaxed);
+    pool->kv4_smem_set = true;
   }
   return (int)launch_pdl(kern, dim3(ctas), dim3(32 * p.Hkv), smem, st, p);
 }
@@ -704,17 +697,17 @@ int launch_kv4_gather(const LaunchCommon& lc, void* stream, int32_t layer, const
   cudaStream_t st = (cudaStream_t)stream;
   if (c.head_dim == 128) {
     switch (g) {
-      case 1: return launch_gather_t<128, 1>(p, ctas, st);
-      case 2: return launch_gather_t<128, 2>(p, ctas, st);
-      case 4: return launch_gather_t<128, 4>(p, ctas, st);
-      case 5: return launch_gather_t<128, 5>(p, ctas, st);
-      case 8: return launch_gather_t<128, 8>(p, ctas, st);
+      case 1: return launch_gather_t<128, 1>(pl->pool, p, ctas, st);
+      case 2: return launch_gather_t<128, 2>(pl->pool, p, ctas, st);
+      case 4: return launch_gather_t<128, 4>(pl->pool, p, ctas, st);
+      case 5: return launch_gather_t<128, 5>(pl->pool, p, ctas, st);
+      case 8: return launch_gather_t<128, 8>(pl->pool, p, ctas, st);
     }
   } else {
     switch (g) {
-      case 1: return launch_gather_t<64, 1>(p, ctas, st);
-      case 2: return launch_gather_t<64, 2>(p, ctas, st);
-      case 4: return launch_gather_t<64, 4>(p, ctas, st);
+      case 1: return launch_gather_t<64, 1>(pl->pool, p, ctas, st);
+      case 2: return launch_gather_t<64, 2>(pl->pool, p, ctas, st);
+      case 4: return launch_gather_t<64, 4>(pl->pool, p, ctas, st);
     }
   }
   return (int)cudaErrorInvalidValue;

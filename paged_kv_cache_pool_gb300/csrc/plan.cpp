@@ -205,30 +205,34 @@ bool partition_whole(const std::vector<int64_t>& n, int64_t max_ctas, std::vecto
 // the stream cut so that the CTAs cost the same: a piece of a request costs its stages and kPieceTokens more, for the query
 // that it loads and the state that it writes.  A cut moves to a request's end that is near.
 constexpr int64_t kPieceTokens = 32, kMostPieces = 512;
-bool fill_kv4(const std::vector<int64_t>& n, int64_t slots, int64_t budget, std::vector<int32_t>* begin,
-              std::vector<SegmentDev>* segs) {
-  begin->assign(1, 0);
-  segs->clear();
+
+// Pieces for CTAs of `budget` tokens' cost each, to segs unless it is null; the CTAs, or slots + 1 where they are more, or a
+// CTA has no room for a piece of kMinGatherQuota tokens.
+int64_t fill_kv4(const std::vector<int64_t>& n, int64_t slots, int64_t budget, std::vector<int32_t>* begin,
+                 std::vector<SegmentDev>* segs) {
+  if (segs) {
+    begin->assign(1, 0);
+    segs->clear();
+  }
   auto stages = [](int64_t tokens) { return (tokens + kKv4Tokens - 1) / kKv4Tokens * kKv4Tokens; };
-  int64_t left = budget;
+  int64_t ctas = 0, left = 0;
   for (size_t r = 0; r < n.size(); ++r)
     for (int64_t t = 0; t < n[r];) {
       int64_t take = n[r] - t;
       const int64_t room = (left - kPieceTokens) / kKv4Tokens * kKv4Tokens;
       if (stages(take) > room + kKv4Tokens) take = room;
       if (take < std::min<int64_t>(kMinGatherQuota, n[r] - t)) {   // too little room: the next CTA's
-        if (left == budget) return false;
-        begin->push_back((int32_t)segs->size());
+        if (left == budget || ++ctas > slots) return slots + 1;
+        if (segs && ctas > 1) begin->push_back((int32_t)segs->size());
         left = budget;
-        if ((int64_t)begin->size() > slots) return false;
         continue;
       }
-      segs->push_back(SegmentDev{(int32_t)r, (int32_t)t, (int32_t)(t + take), -1});
+      if (segs) segs->push_back(SegmentDev{(int32_t)r, (int32_t)t, (int32_t)(t + take), -1});
       t += take;
       left -= stages(take) + kPieceTokens;
     }
-  if (begin->back() != (int32_t)segs->size()) begin->push_back((int32_t)segs->size());
-  return (int64_t)begin->size() - 1 <= slots;
+  if (segs) begin->push_back((int32_t)segs->size());
+  return ctas;
 }
 
 void partition_kv4(const std::vector<int64_t>& n, int64_t slots, std::vector<int32_t>* begin, std::vector<SegmentDev>* segs) {
@@ -243,10 +247,10 @@ void partition_kv4(const std::vector<int64_t>& n, int64_t slots, std::vector<int
   int64_t lo = std::max<int64_t>(kMinGatherQuota + kPieceTokens, total / slots);
   lo = std::max(lo, (most / kMostPieces + kKv4Tokens - 1) / kKv4Tokens * kKv4Tokens + kPieceTokens);
   int64_t hi = lo;
-  while (!fill_kv4(n, slots, hi, begin, segs)) hi += std::max<int64_t>(hi / 2, kKv4Tokens);
+  while (fill_kv4(n, slots, hi, nullptr, nullptr) > slots) hi += std::max<int64_t>(hi / 2, kKv4Tokens);
   while (hi - lo > std::max<int64_t>(kKv4Tokens / 2, hi / 256)) {
     const int64_t mid = (lo + hi) / 2;
-    if (fill_kv4(n, slots, mid, begin, segs))
+    if (fill_kv4(n, slots, mid, nullptr, nullptr) <= slots)
       hi = mid;
     else
       lo = mid;
@@ -618,9 +622,10 @@ gk_status build_host_plan_kind(Pool* p, const gk_batch* b, Plan* pl, gk_prefix_k
   int64_t suf_tokens = 0, dense_tokens = 0;
   for (int32_t r = 0; r < B; ++r) {
     n_suf[(size_t)r] = pl->reqs[(size_t)r].slen;
-    n_dense[(size_t)r] = (int64_t)pl->reqs[(size_t)r].lp + pl->reqs[(size_t)r].slen;
+    // (a 4-bit pool has no flat backend)
+    n_dense[(size_t)r] = p->kv4 ? 0 : (int64_t)pl->reqs[(size_t)r].lp + pl->reqs[(size_t)r].slen;
     suf_tokens += n_suf[(size_t)r];
-    dense_tokens += n_dense[(size_t)r];
+    dense_tokens += (int64_t)pl->reqs[(size_t)r].lp + pl->reqs[(size_t)r].slen;
   }
   pl->slot_of_sm.clear();
   if (pl->split) {
@@ -703,7 +708,7 @@ gk_status build_host_plan_kind(Pool* p, const gk_batch* b, Plan* pl, gk_prefix_k
     } else {
       rq.n_entry_dense = nseg_dense[(size_t)r];
       e += nseg_dense[(size_t)r];
-      pl->dense_needs_merge = true;
+      pl->dense_needs_merge = !p->kv4;
     }
   }
   pl->n_entries_dense = e;

@@ -54,7 +54,7 @@ __device__ __forceinline__ uint4 pack8(const float* x) {
   return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
 }
 __device__ __forceinline__ void load8(const float* p, float* x) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
   x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
 }
 // 16 bytes that this call reads once
@@ -144,8 +144,8 @@ __device__ __forceinline__ void load_angles(const QkvParams& p, int64_t at, int 
     for (int b = 0; b < 2; ++b) {
       const int ch = j + b * LPH;                // pairs 4 ch .. 4 ch + 3
       if (ch * 8 >= p.rot) continue;
-      const float4 x = __ldg(reinterpret_cast<const float4*>(cs + 4 * ch));
-      const float4 y = __ldg(reinterpret_cast<const float4*>(cs + half + 4 * ch));
+      const float4 x = *reinterpret_cast<const float4*>(cs + 4 * ch);
+      const float4 y = *reinterpret_cast<const float4*>(cs + half + 4 * ch);
       w.c[4 * b] = x.x; w.c[4 * b + 1] = x.y; w.c[4 * b + 2] = x.z; w.c[4 * b + 3] = x.w;
       w.s[4 * b] = y.x; w.s[4 * b + 1] = y.y; w.s[4 * b + 2] = y.z; w.s[4 * b + 3] = y.w;
     }
