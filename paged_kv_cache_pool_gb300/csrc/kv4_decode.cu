@@ -652,7 +652,8 @@ int launch_gather_t(Pool* pool, const Kv4Params& p, int ctas, cudaStream_t st) {
   const size_t smem = gather_smem(p.Hkv, D);
   auto kern = kv4_gather_kernel<D, G>;
   if (!pool->kv4_smem_set) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // (the most that any pool of these heads takes: the attribute is the kernel's, not the pool's)
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)gather_smem(kMaxKvHeads, D));
     if (e != cudaSuccess) return (int)e;
     pool->kv4_smem_set = true;
   }

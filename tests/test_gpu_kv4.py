@@ -399,6 +399,17 @@ def test_two_pools_at_once():
     b.close()
 
 
+def test_pools_of_more_and_fewer_kv_heads():
+    """Pools whose heads share a kernel but whose CTAs take different shared memory, in turn."""
+    steps = [Step(128, 4, hkv, [300, 40], seed=hkv) for hkv in (8, 1, 5)]
+    for s in steps + steps:
+        s.out[:-1].fill_(3)
+        s.run()
+        s.check(f"{s.hkv} KV heads")
+    for s in steps:
+        s.close()
+
+
 def test_steps_from_the_projection_on():
     """Prompts and decode steps over a 4-bit cache as an engine runs them: slots, norm + rotation + append, prompt attention over the
     bf16 keys, then steps of decode with a forked request, each against 64 bits."""
