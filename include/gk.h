@@ -242,7 +242,8 @@ gk_status gk_tables_step(gk_pool* pool, void* stream, const gk_tables* t, const 
  * d_slot_mapping: device int64 [n]; d_k, d_v: device bf16 [n][Hkv][d];
  * d_cow_pairs: device int32 [n_cow][2] (src, dst) or NULL when n_cow = 0.
  * Out-of-range slots or blocks are skipped and reported as GK_ERR_DEVICE_BOUNDS
- * by gk_device_error().  On a 4-bit pool the rows are encoded (gk_pool_create_kv4). */
+ * by gk_device_error().  On a 4-bit pool the rows are encoded (gk_pool_create_kv4); d_k and d_v are then
+ * 16-byte aligned and the pool's device the current one (else GK_ERR_INVALID). */
 gk_status gk_append_kv(gk_pool* pool, void* stream, int32_t layer, int32_t n, const int64_t* d_slot_mapping,
                        const void* d_k, const void* d_v, int32_t n_cow, const int32_t* d_cow_pairs);
 /* Write prefix tokens [t0, t0+n) of one layer into the HOT slab at hot_base

@@ -572,7 +572,11 @@ gk_status gk_append_kv(gk_pool* pool, void* stream, int32_t layer, int32_t n, co
     return gk::fail(p, GK_ERR_INVALID, "bad layer or count");
   if ((n > 0 && (!d_slot_mapping || !d_k || !d_v)) || (n_cow > 0 && !d_cow_pairs))
     return gk::fail(p, GK_ERR_INVALID, "null device pointer");
+  if (p->kv4 && ((uintptr_t)d_k % 16 != 0 || (uintptr_t)d_v % 16 != 0 || (uintptr_t)d_slot_mapping % 8 != 0 ||
+                 (uintptr_t)d_cow_pairs % 4 != 0))
+    return gk::fail(p, GK_ERR_INVALID, "rows must be 16-byte, slots 8-byte and copy-on-write pairs 4-byte aligned");
   gk_status st = gk::ensure_device(p);
+  if (st == GK_OK && p->kv4) st = gk::device_is_current(p);
   if (st != GK_OK) return st;
   gk::LaunchCommon lc{&p->cfg, p->d_error, p->dev.num_sms};
   if (n_cow > 0) {

@@ -220,6 +220,14 @@ def test_rows_good_and_bad_for_one_call(gk, pool):
     assert gk.lib().gk_append_qkv(pool, None, 0, None, None, 0, None) == gk.GK_ERR_INVALID
 
 
+def test_append_of_misaligned_rows_refuses(gk, pool):
+    append = lambda layer=0, n=3, s=4096, k=4096, v=4096, n_cow=0, cow=None: (  # noqa: E731
+        gk.lib().gk_append_kv(pool, None, layer, n, s, k, v, n_cow, cow), gk.gk_last_error(pool))
+    assert "storage" in append()[1] and "storage" in append(n=0, s=None, k=None, v=None, n_cow=1, cow=4100)[1]
+    for st, text in (append(k=4104), append(v=4098), append(s=4100), append(n_cow=1, cow=4098), append(k=None), append(layer=2)):
+        assert st == gk.GK_ERR_INVALID and "storage" not in text, text
+
+
 def test_read_refuses(gk, pool):
     read = lambda layer=0, n=3, s=4096, k=4096, v=4096, ks=0, vs=0: (  # noqa: E731
         gk.lib().gk_read_kv(pool, None, layer, n, s, k, v, ks, vs), gk.gk_last_error(pool))
