@@ -12,9 +12,13 @@
 // operands by one logic instruction a pair: the pair (code & 0x000f000f) read as fp16 is the subnormal pair
 // code * 2^-24, and (code & 0x00f000f0) is 16 * code * 2^-24, both exact, and the tensor core multiplies
 // subnormals exactly; the factor 16 goes into the query's fragment.  For V the second operand is the whole byte,
-// code + 16 * code', from whose sum the first one's is taken in the end: two instructions a byte pair, not five for two.  (As 8-bit floats
-// four codes would take one mask, but the warp-level products of 8-bit operands are made of conversions to fp16
-// and fp16 products on this chip: 608 requests of 2048 tokens 265 us, so 450.)
+// code + 16 * code', from whose sum the first one's is taken in the end.  (As 8-bit floats four codes would take one
+// mask, but the warp-level products of 8-bit operands cost several times the fp16 ones on this chip: 608 requests of
+// 2048 tokens took 450 us so and 265 with fp16.)
+//
+// GB300, 4 requests of 262144 tokens, 32/8 heads of 128, pages of 16 (1.2 GB of rows): 210 us, 5.7 TB/s, 84 % of the
+// measured copy rate; the same work on rows that stay in L2 takes 190, so instructions bind it next to HBM: 473 a
+// warp and stage, half of the issue slots and of the ALU pipe's (masks, byte permutes, integer tests) busy.
 #include <cmath>
 
 #include "device_common.cuh"
@@ -49,8 +53,7 @@ struct Kv4Params {
 
 constexpr int kSegCache = 32;  // segment records a CTA keeps in shared memory
 
-constexpr int kStages = 2;     // a warp's ring: 3 hold as many bytes more as the SM can use, and cost 2 %
-constexpr int kFewPages = 8;   // tokens a page from which a stage touches few of them
+constexpr int kStages = 2;     // of a warp's ring (three cost 2 %)
 
 // a stage of one warp: K codes, V codes, scales of kTok tokens
 __host__ __device__ constexpr int stage_bytes(int d) { return kTok * (d + d / 8); }
@@ -212,7 +215,11 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
       const uint32_t st = ring + (uint32_t)next * stage_bytes(D);
       // places past the stage's tokens get its last token's row: they meet weights and spans of 0
       const uint32_t sdst = st + kTok * D;
-      if (p.page >= kFewPages) {
+      // All of the stage's scales by one instruction, but for pages of one token at d = 128: 608 requests of 2048 tokens (8 KV
+      // heads) take 463 us so, and 258 where the threads that just touched a token's row copy its scales, likely for the
+      // translation of the 32 places at once (380 and 292 by two and four instructions).  With pages of two tokens the one
+      // instruction takes 241 and the other form 255, at d = 64 with pages of one 86 and 90 (304 requests of 4096).
+      if (D == 64 || p.page > 1) {
 #pragma unroll
         for (int j = 0; j < kTok / TPI; ++j) {
           const int32_t s = __shfl_sync(0xffffffffu, slot, j * TPI + lane / CPT);
@@ -220,9 +227,6 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
         }
         copy_async<D / 8>(sdst + lane * (D / 8), scale_src + (int64_t)slot * row_bytes);
       } else {
-        // A copy of all the stage's scales costs as many address translations as it has pages at once: with pages of
-        // one token 608 requests of 2048 tokens take 454 us, and 265 where the few threads that just touched a token's row
-        // copy its scales.  With pages of 16 this form takes 263 us and the other 250.
 #pragma unroll
         for (int j = 0; j < kTok / TPI; ++j) {
           const int32_t s = __shfl_sync(0xffffffffu, slot, j * TPI + lane / CPT);

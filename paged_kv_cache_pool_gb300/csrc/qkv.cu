@@ -22,7 +22,7 @@ namespace {
 
 constexpr int kWarps = 4;  // warps of a block
 constexpr int kChunk = 7;  // most passes of a warp (5, 12 or 14 a warp: 3 - 10 % slower)
-constexpr int kFewWarps = 64;
+constexpr int kFewWarps = 64;  // warps that an SM holds
 
 // how channels rotate: not at all, whole heads in halves, neighbouring pairs, a part of the head in halves
 enum Rotation { kNone, kHalves, kPairs, kPart };
@@ -463,7 +463,7 @@ __global__ void kv4_cow_kernel(uint4* layer, int64_t block_vecs, int64_t n_block
 template <int D, int ROT, bool KV4>
 int launch_qkv_u(const QkvParams& p, int num_sms, cudaStream_t st) {
   const int per = 512 / D, kv = (p.Hkv + per - 1) / per, passes = (p.Hq + per - 1) / per + kv * (p.slots ? 2 : 1);
-  // one pass a warp while the SMs (64 warps each) hold them all: the shortest way for a few tokens.  Else about kChunk
+  // one pass a warp while the SMs hold them all: the shortest way for a few tokens.  Else about kChunk
   const int chunk = (int64_t)p.n * passes <= (int64_t)num_sms * kFewWarps ? 1 : kChunk;
   const int parts = (passes + chunk - 1) / chunk, each = (passes + parts - 1) / parts;
   const int64_t blocks = ((int64_t)p.n * parts + kWarps - 1) / kWarps;
