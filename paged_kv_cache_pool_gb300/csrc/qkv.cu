@@ -106,12 +106,14 @@ __device__ __forceinline__ uint32_t group_scale(float lo, float hi, float& span)
 }
 
 // Eight codes round(15 (x - lo) / span), ties to even, the first in the lowest nibble.  A product with the reciprocal is
-// within 2^-21 of the quotient; where its nearest integer leaves a remainder of half the span or more (exact: the
+// within 2^-21 of the quotient, relatively; where its nearest integer leaves a remainder of half the span or more (exact: the
 // integer has four bits, the span eight) the neighbour, or of two the even one, is right.
 __device__ __forceinline__ uint32_t codes8(const float* x, float lo, float span) {
   if (span == 0.f) return 0u;
   constexpr float kMagic = 12582912.f;   // 1.5 * 2^23: a sum with it is rounded to an integer, in its low bits
-  const float inv = __frcp_rn(span), half = 0.5f * span;
+  const float half = 0.5f * span;
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(span));   // to 2^-23; the span is between 2^-100 and 2^120
   uint32_t w = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
