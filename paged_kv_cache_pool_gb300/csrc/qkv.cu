@@ -38,6 +38,8 @@ struct QkvParams {
   const int32_t* pos;
   int64_t num_pos;
   int32_t rot;
+  float one;                      // 1, which the compiler must not know: a packed product and a packed sum it contracts, for
+                                  // all their .rn, while a product times this plus a term keeps its own rounding
   float eps;
   int32_t n, Hq, Hkv;
   // cache of the layer (slots null: none)
@@ -65,15 +67,16 @@ __device__ __forceinline__ uint4 load_once(const uint16_t* p) {
   asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
   return v;
 }
-__device__ __forceinline__ float min_nan(float a, float b) {
-  float m;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
-  return m;
+// of two bf16 each, NaN where either is
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float m;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
-  return m;
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 
 // (a, b) <- (a c - b s, b c + a s), each product and sum rounded by itself: the bits that
@@ -105,27 +108,27 @@ __device__ __forceinline__ uint32_t group_scale(float lo, float hi, float& span)
   return w;
 }
 
-// Eight codes round(15 (x - lo) / span), ties to even, the first in the lowest nibble.  A product with the reciprocal is
-// within 2^-21 of the quotient, relatively; where its nearest integer leaves a remainder of half the span or more (exact: the
-// integer has four bits, the span eight) the neighbour, or of two the even one, is right.
+// Eight codes round(15 (x - lo) / span), ties to even, the first in the lowest nibble.  With q0 = t inv, t = 15 (x - lo)
+// rounded and inv the reciprocal to 2^-23, q = q0 + (t - q0 span) inv, its bracket exact, is off by about 2^-45 before it is
+// rounded to fp32.  So where t / span is an integer and a half q is that too; where it is not, t is at least an ulp from
+// (k + 1/2) span, which fp32 holds (span has eight bits), and q rounds to its side.  Two values an instruction.
 __device__ __forceinline__ uint32_t codes8(const float* x, float lo, float span) {
-  if (span == 0.f) return 0u;
   constexpr float kMagic = 12582912.f;   // 1.5 * 2^23: a sum with it is rounded to an integer, in its low bits
-  const float half = 0.5f * span;
+  constexpr uint32_t kBits = 0x4b400000u;
   float inv;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(span));   // to 2^-23; the span is between 2^-100 and 2^120
-  uint32_t w = 0;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(span));   // the span is between 2^-100 and 2^120, or 0
+  const uint64_t nlo = f2pack(-lo, -lo), nspan = f2pack(-span, -span), ii = f2pack(inv, inv);
+  const uint64_t fifteen = f2pack(15.f, 15.f), magic = f2pack(kMagic, kMagic);
+  float y[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float t = __fmul_rn(__fsub_rn(x[i], lo), 15.f);
-    const float y = __fadd_rn(__fmul_rn(t, inv), kMagic);
-    float c = __fsub_rn(y, kMagic);
-    const float rem = fmaf(-c, span, t);
-    uint32_t code = __float_as_uint(y) & 15u;
-    if (fabsf(rem) >= half && (fabsf(rem) > half || (code & 1u))) code += rem > 0.f ? 1u : -1u;
-    w |= (code & 15u) << (4 * i);
+  for (int i = 0; i < 8; i += 2) {
+    const uint64_t t = mul2(fadd2(f2pack(x[i], x[i + 1]), nlo), fifteen), q0 = mul2(t, ii);
+    f2unpack(fadd2(ffma2(ffma2(q0, nspan, t), ii, q0), magic), y[i], y[i + 1]);
   }
-  return w;
+  uint32_t w = __float_as_uint(y[7]);
+#pragma unroll
+  for (int i = 6; i >= 0; --i) w = w * 16u + __float_as_uint(y[i]);
+  return span == 0.f ? 0u : w - kBits * 0x11111111u;
 }
 
 // What the rotation of a thread's two chunks takes: of whole heads in halves one set of eight cosines and sines for the
@@ -170,13 +173,13 @@ template <int D, int ROT>
 __device__ __forceinline__ void rotate(const QkvParams& p, int j, int lane, const Angles<ROT>& w, float* x) {
   constexpr int LPH = D / 16;
   if (ROT == kHalves) {
-    const uint64_t minus = f2pack(-1.f, -1.f);
+    const uint64_t one = f2pack(p.one, p.one), minus = f2pack(-1.f, -1.f);
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
       const uint64_t a = f2pack(x[i], x[i + 1]), b = f2pack(x[i + 8], x[i + 9]);
       const uint64_t c = f2pack(w.c[i], w.c[i + 1]), s = f2pack(w.s[i], w.s[i + 1]);
       f2unpack(ffma2(mul2(b, s), minus, mul2(a, c)), x[i], x[i + 1]);
-      f2unpack(fadd2(mul2(b, c), mul2(a, s)), x[i + 8], x[i + 9]);
+      f2unpack(ffma2(mul2(a, s), one, mul2(b, c)), x[i + 8], x[i + 9]);
     }
   } else if (ROT == kPairs) {
 #pragma unroll
@@ -224,38 +227,33 @@ __device__ __forceinline__ void store_codes(uint4 y0, uint4 y1, uint8_t* row, in
   float x[16];
   unpack8(y0, x);
   unpack8(y1, x + 8);
-  float lo[2] = {x[0], x[8]}, hi[2] = {x[0], x[8]};
-#pragma unroll
-  for (int i = 1; i < 8; ++i) {
-    lo[0] = min_nan(lo[0], x[i]);
-    hi[0] = max_nan(hi[0], x[i]);
-    lo[1] = min_nan(lo[1], x[8 + i]);
-    hi[1] = max_nan(hi[1], x[8 + i]);
-  }
+  // least and greatest: of both chunks in a word's halves, then of the group's threads
+  const uint32_t a0 = min2(min2(y0.x, y0.y), min2(y0.z, y0.w)), a1 = min2(min2(y1.x, y1.y), min2(y1.z, y1.w));
+  const uint32_t b0 = max2(max2(y0.x, y0.y), max2(y0.z, y0.w)), b1 = max2(max2(y1.x, y1.y), max2(y1.z, y1.w));
+  uint32_t lo = min2(__byte_perm(a0, a1, 0x5410), __byte_perm(a0, a1, 0x7632));
+  uint32_t hi = max2(__byte_perm(b0, b1, 0x5410), __byte_perm(b0, b1, 0x7632));
   if (D == 64) {     // both chunks are of the head's one group
-    lo[0] = min_nan(lo[0], lo[1]);
-    hi[0] = max_nan(hi[0], hi[1]);
+    lo = min2(lo, __byte_perm(lo, 0, 0x1032));
+    hi = max2(hi, __byte_perm(hi, 0, 0x1032));
   }
 #pragma unroll
-  for (int g = 0; g < D / 64; ++g)
-#pragma unroll
-    for (int off = 1; off < LPH; off <<= 1) {
-      lo[g] = min_nan(lo[g], __shfl_xor_sync(0xffffffffu, lo[g], off));
-      hi[g] = max_nan(hi[g], __shfl_xor_sync(0xffffffffu, hi[g], off));
-    }
+  for (int off = 1; off < LPH; off <<= 1) {
+    lo = min2(lo, __shfl_xor_sync(0xffffffffu, lo, off));
+    hi = max2(hi, __shfl_xor_sync(0xffffffffu, hi, off));
+  }
   if (!ok) return;
   uint8_t* codes = row + kv4::codes_at(h, D) + (is_v ? D / 2 : 0);
   uint8_t* scales = row + kv4::scales_at(hkv, h, D) + (is_v ? D / 16 : 0);
   float span;
-  const uint32_t s0 = group_scale(lo[0], hi[0], span);
-  const uint32_t c0 = codes8(x, lo[0], span);
+  const uint32_t s0 = group_scale(bf_lo(lo), bf_lo(hi), span);
+  const uint32_t c0 = codes8(x, bf_lo(lo), span);
   if (D == 64) {
     reinterpret_cast<uint32_t*>(codes)[j] = c0;
-    reinterpret_cast<uint32_t*>(codes)[j + LPH] = codes8(x + 8, lo[0], span);
+    reinterpret_cast<uint32_t*>(codes)[j + LPH] = codes8(x + 8, bf_lo(lo), span);
     if (j == 0) *reinterpret_cast<uint32_t*>(scales) = s0;
   } else {
-    const uint32_t s1 = group_scale(lo[1], hi[1], span);
-    reinterpret_cast<uint2*>(codes)[j] = make_uint2(c0, codes8(x + 8, lo[1], span));
+    const uint32_t s1 = group_scale(bf_hi(lo), bf_hi(hi), span);
+    reinterpret_cast<uint2*>(codes)[j] = make_uint2(c0, codes8(x + 8, bf_hi(lo), span));
     if (j == 0) *reinterpret_cast<uint2*>(scales) = make_uint2(s0, s1);
   }
 }
@@ -379,15 +377,23 @@ struct ReadParams {
   uint16_t *k, *v;
   int64_t ks, vs;
   int32_t Hkv;
+  float one;                      // as in QkvParams
   int32_t* err;
 };
 
-// bf16(lo + code * step) of the eight codes of a word
-__device__ __forceinline__ uint4 values8(uint32_t w, float lo, float step) {
-  float x[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = __fadd_rn(lo, __fmul_rn((float)((w >> (4 * i)) & 15u), step));
-  return pack8(x);
+// bf16(lo + code * step) of the eight codes of a word, product and sum rounded to fp32.  A nibble becomes a number where it
+// stands: the low bits of 2^23, less 2^23, are the code times a power of 16, and that power's part of the step meets it.
+__device__ __forceinline__ uint4 values8(uint32_t w, float lo, float step, uint64_t one) {
+  constexpr uint32_t kBits = 0x4b000000u;  // 2^23
+  const uint64_t base = f2pack(-8388608.f, -8388608.f), ll = f2pack(lo, lo);
+  const uint64_t s01 = f2pack(step, step * 0x1p-4f), s23 = f2pack(step * 0x1p-8f, step * 0x1p-12f);
+  auto pair = [&](uint32_t v, uint32_t m0, uint32_t m1, uint64_t s) {
+    float a, b;
+    f2unpack(ffma2(mul2(fadd2(f2pack(__uint_as_float((v & m0) | kBits), __uint_as_float((v & m1) | kBits)), base), s), one, ll), a, b);
+    return pack_bf16x2(a, b);
+  };
+  const uint32_t h = w >> 16;
+  return make_uint4(pair(w, 0xfu, 0xf0u, s01), pair(w, 0xf00u, 0xf000u, s23), pair(h, 0xfu, 0xf0u, s01), pair(h, 0xf00u, 0xf000u, s23));
 }
 
 template <int D, bool KV4, int U>
@@ -443,7 +449,7 @@ __global__ void __launch_bounds__(32 * kWarps) read_kernel(const ReadParams p, i
     uint4* out = reinterpret_cast<uint4*>(is_v ? p.v + tok * p.vs + (hh - p.Hkv) * D : p.k + tok * p.ks + hh * D);
     if (KV4) {
 #pragma unroll
-      for (int b = 0; b < 2; ++b) y[u][b] = values8(y[u][b].x, bf_lo(sc[u][b]), __fdiv_rn(bf_hi(sc[u][b]), 15.f));
+      for (int b = 0; b < 2; ++b) y[u][b] = values8(y[u][b].x, bf_lo(sc[u][b]), __fdiv_rn(bf_hi(sc[u][b]), 15.f), f2pack(p.one, p.one));
     }
     out[j] = y[u][0];
     out[j + LPH] = y[u][1];
@@ -523,6 +529,7 @@ int launch_qkv(const LaunchCommon& lc, void* stream, bool kv4, int32_t layer, co
   p.pos = x->d_positions;
   p.num_pos = x->num_positions;
   p.rot = x->rot_dim;
+  p.one = 1.f;
   p.eps = x->eps;
   p.n = x->num_tokens;
   p.Hq = p.q ? c.num_q_heads : 0;
@@ -560,6 +567,7 @@ int launch_read_kv(const LaunchCommon& lc, void* stream, bool kv4, int32_t layer
   p.ks = k_stride ? k_stride : kv_row;
   p.vs = v_stride ? v_stride : kv_row;
   p.Hkv = c.num_kv_heads;
+  p.one = 1.f;
   p.err = lc.d_error;
   const int per = 512 / c.head_dim, passes = (2 * c.num_kv_heads + per - 1) / per;
   const int u = n * passes <= (int64_t)lc.num_sms * kFewWarps ? 1 : 4;
