@@ -22,8 +22,7 @@ namespace {
 
 constexpr int kWarps = 4;  // warps of a block
 constexpr int kChunk = 7;  // most passes of a warp (5, 12 or 14 a warp: 3 - 10 % slower)
-template <bool KV4>
-constexpr int kBlocks = KV4 ? 6 : 7;  // blocks of an SM (registers)
+constexpr int kBlocks = 7;  // of an SM, as registers allow (4-bit rows, 16384 tokens of 32/8 heads of 128: six 66 us, seven 63)
 constexpr int kFewWarps = 64;  // warps of an SM at most
 
 // how channels rotate: not at all, whole heads in halves, neighbouring pairs, a part of the head in halves
@@ -264,7 +263,7 @@ __device__ __forceinline__ void store_codes(uint4 y0, uint4 y1, uint8_t* row, in
 // instructions a pass), 66 with two passes ahead in registers, 58 as it is, 5.9 TB/s; a copy of the same bytes takes 50.
 // Small blocks and many of them (seven of four warps an SM) hide the chain position -> angles -> first pass.
 template <int D, int ROT, bool KV4>
-__global__ void __launch_bounds__(32 * kWarps, kBlocks<KV4>) qkv_kernel(const QkvParams p, int passes, int parts, int chunk) {
+__global__ void __launch_bounds__(32 * kWarps, kBlocks) qkv_kernel(const QkvParams p, int passes, int parts, int chunk) {
   constexpr int LPH = D / 16;       // lanes of a head
   constexpr int HPW = 32 / LPH;     // heads of a pass
   griddep_launch_dependents();
@@ -473,12 +472,11 @@ __global__ void kv4_cow_kernel(uint4* layer, int64_t block_vecs, int64_t n_block
 template <int D, int ROT, bool KV4>
 int launch_qkv_u(const QkvParams& p, int num_sms, cudaStream_t st) {
   const int per = 512 / D, kv = (p.Hkv + per - 1) / per, passes = (p.Hq + per - 1) / per + kv * (p.slots ? 2 : 1);
-  // The fewest passes a warp that one wave of warps takes all with, while that is few; else kChunk.  Against one pass up to
-  // 64 warps an SM (40/8 heads of 128): 512 tokens 4.4 -> 3.6 us, 768 6.4 -> 4.5, 1024 6.8 -> 5.2, and as before from five
-  // on.  Passes that encode are long: two waves of one beat one of two (368 tokens 6.9, 7.4), three take 10.4, with three
-  // passes 9.7 and with seven 11.8, and from four on seven is as good or better.
-  const int64_t room = (int64_t)num_sms * kWarps * kBlocks<KV4>, waves = ((int64_t)p.n * passes + room - 1) / room;
-  const int chunk = waves > (KV4 ? 3 : 4) ? kChunk : KV4 && waves == 2 ? 1 : (int)waves;
+  // The fewest passes a warp with which one wave of warps takes all, up to four; else kChunk.  40/8 heads of 128, against
+  // one pass while an SM has up to 64 of them: bf16 rows of 512 tokens 4.4 -> 3.6 us, 768 6.4 -> 4.5, 1024 6.8 -> 5.2; from
+  // five on (1500 tokens) 10.4 where seven take 10.0.
+  const int64_t room = (int64_t)num_sms * kWarps * kBlocks, waves = ((int64_t)p.n * passes + room - 1) / room;
+  const int chunk = waves > 4 ? kChunk : (int)waves;
   const int parts = (passes + chunk - 1) / chunk, each = (passes + parts - 1) / parts;
   const int64_t blocks = ((int64_t)p.n * parts + kWarps - 1) / kWarps;
   return (int)launch_pdl(qkv_kernel<D, ROT, KV4>, dim3((unsigned)blocks), dim3(32 * kWarps), kWarps * each * 1024, st, p, passes, parts, each);
