@@ -396,12 +396,13 @@ __device__ __forceinline__ uint4 values8(uint32_t w, float lo, float step, uint6
 }
 
 template <int D, bool KV4, int U>
-__global__ void __launch_bounds__(32 * kWarps) read_kernel(const ReadParams p, int warps_per_token) {
+__global__ void __launch_bounds__(32 * kWarps) read_kernel(const ReadParams p, uint32_t warps_per_token) {
   constexpr int LPH = D / 16, HPW = 32 / LPH;
   griddep_launch_dependents();
   griddep_wait();
   const int lane = threadIdx.x & 31, j = lane % LPH;
-  const int64_t w = blockIdx.x * (int64_t)kWarps + (threadIdx.x >> 5);
+  // (at most 2^27 tokens of four warps)
+  const uint32_t w = blockIdx.x * kWarps + (threadIdx.x >> 5);
   const int64_t tok = w / warps_per_token;
   if (tok >= p.n) return;
   const int hh0 = (int)(w % warps_per_token) * HPW * U + lane / LPH;
@@ -568,7 +569,9 @@ int launch_read_kv(const LaunchCommon& lc, void* stream, bool kv4, int32_t layer
   p.one = 1.f;
   p.err = lc.d_error;
   const int per = 512 / c.head_dim, passes = (2 * c.num_kv_heads + per - 1) / per;
-  const int u = n * passes <= (int64_t)lc.num_sms * kFewWarps ? 1 : 4;
+  // a warp of each pass while the SMs hold them all, or where a token has only one (65536 tokens of 4 heads of 64 in 4 bits: 18
+  // us, 21 with loops of four); else four a warp (of 8 heads of 128: 53, 68 with one)
+  const int u = passes == 1 || n * passes <= (int64_t)lc.num_sms * kFewWarps ? 1 : 4;
   const int warps = (passes + u - 1) / u;
   const int64_t blocks = (n * warps + kWarps - 1) / kWarps;
   auto kern = c.head_dim == 128
@@ -576,7 +579,7 @@ int launch_read_kv(const LaunchCommon& lc, void* stream, bool kv4, int32_t layer
                             : (kv4 ? read_kernel<128, true, 4> : read_kernel<128, false, 4>))
                   : (u == 1 ? (kv4 ? read_kernel<64, true, 1> : read_kernel<64, false, 1>)
                             : (kv4 ? read_kernel<64, true, 4> : read_kernel<64, false, 4>));
-  return (int)launch_pdl(kern, dim3((unsigned)blocks), dim3(32 * kWarps), 0, (cudaStream_t)stream, p, warps);
+  return (int)launch_pdl(kern, dim3((unsigned)blocks), dim3(32 * kWarps), 0, (cudaStream_t)stream, p, (uint32_t)warps);
 }
 
 }  // namespace gk
