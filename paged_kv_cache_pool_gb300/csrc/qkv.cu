@@ -263,16 +263,17 @@ __device__ __forceinline__ void store_codes(uint4 y0, uint4 y1, uint8_t* row, in
 // instructions a pass), 66 with two passes ahead in registers, 58 as it is, 5.9 TB/s; a copy of the same bytes takes 50.
 // Small blocks and many of them (seven of four warps an SM) hide the chain position -> angles -> first pass.
 template <int D, int ROT, bool KV4>
-__global__ void __launch_bounds__(32 * kWarps, kBlocks) qkv_kernel(const QkvParams p, int passes, int parts, int chunk) {
+__global__ void __launch_bounds__(32 * kWarps, kBlocks) qkv_kernel(const QkvParams p, int passes, uint32_t parts, int chunk) {
   constexpr int LPH = D / 16;       // lanes of a head
   constexpr int HPW = 32 / LPH;     // heads of a pass
   griddep_launch_dependents();
   griddep_wait();
   const int lane = threadIdx.x & 31, j = lane % LPH;
-  const int64_t w = blockIdx.x * (int64_t)kWarps + (threadIdx.x >> 5);
-  const int64_t tok = w / parts;
+  const uint32_t w = blockIdx.x * kWarps + (threadIdx.x >> 5);   // of at most 2^27 tokens' few
+  const uint32_t of_token = w / parts;
+  const int64_t tok = of_token;
   if (tok >= p.n) return;
-  const int first = (int)(w - tok * parts) * chunk, end = min(passes, first + chunk);
+  const int first = (int)(w - of_token * parts) * chunk, end = min(passes, first + chunk);
   const int q_passes = (p.Hq + HPW - 1) / HPW, k_end = q_passes + (p.Hkv + HPW - 1) / HPW;
   const uint16_t* const src_q = p.q + tok * p.qs + 8 * j;
   const uint16_t* const src_k = p.k + tok * p.ks + 8 * j;
@@ -480,7 +481,7 @@ int launch_qkv_u(const QkvParams& p, int num_sms, cudaStream_t st) {
   const int chunk = waves > 4 ? kChunk : (int)waves;
   const int parts = (passes + chunk - 1) / chunk, each = (passes + parts - 1) / parts;
   const int64_t blocks = ((int64_t)p.n * parts + kWarps - 1) / kWarps;
-  return (int)launch_pdl(qkv_kernel<D, ROT, KV4>, dim3((unsigned)blocks), dim3(32 * kWarps), kWarps * each * 1024, st, p, passes, parts, each);
+  return (int)launch_pdl(qkv_kernel<D, ROT, KV4>, dim3((unsigned)blocks), dim3(32 * kWarps), kWarps * each * 1024, st, p, passes, (uint32_t)parts, each);
 }
 
 template <int D, int ROT>
