@@ -96,7 +96,9 @@ gk_status gk_pool_create(const gk_pool_config* cfg, gk_pool** out);
  * the lowest four bits; word w has channels 8 w .. 8 w + 7 at d = 64 and 8 (w / 2) + 64 (w % 2) .. + 7 at
  * d = 128, so that a thread's loads hold what its tensor-core fragments take), then per KV head the bf16
  * pairs (lo, span) of K's groups, then of V's; padded to 16 bytes.
- * The block manager, gk_tables_step, the HOT calls and plans work as on any pool.  Written by
+ * The block manager, gk_tables_step, the HOT calls and plans work as on any pool; in a plan's summary
+ * suffix_ctas are the 4-bit gather's, dense_ctas is 0, and levels never share a launch (gk_pool_set_cascade_mode
+ * and gk_pool_set_gather_partition change nothing).  Written by
  * gk_append_kv and gk_append_qkv, read by gk_read_kv and gk_decode_kv4; the other calls that read or
  * write COLD (gk_decode_dense, gk_decode_dense_static, gk_decode_cascade and its stages,
  * gk_sm_speeds_measure, gk_calibrate, gk_dispatch, prompt plans with a COLD context) return

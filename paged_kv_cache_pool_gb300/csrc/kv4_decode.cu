@@ -17,7 +17,7 @@
 // 2048 tokens took 450 us so and 265 with fp16.)
 //
 // GB300, 4 requests of 262144 tokens, 32/8 heads of 128, pages of 16 (1.2 GB of rows): 210 us, 5.7 TB/s, 84 % of the
-// measured copy rate; the same work on rows that stay in L2 takes 190, so instructions bind it next to HBM: 473 a
+// measured copy rate; the same work on rows that stay in L2 takes 187, so instructions bind it next to HBM: 473 a
 // warp and stage, half of the issue slots and of the ALU pipe's (masks, byte permutes, integer tests) busy.
 #include <cmath>
 

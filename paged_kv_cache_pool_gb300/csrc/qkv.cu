@@ -260,7 +260,7 @@ __device__ __forceinline__ void store_codes(uint4 y0, uint4 y1, uint8_t* row, in
 // A warp takes passes [part * chunk, (part + 1) * chunk) of a token's: its heads of q, of k and of v, HPW at a time.  Their
 // rows are asked for at once, into shared memory; angles and weights are loaded once for all.
 // GB300, 16384 tokens of 32/8 heads of 128, normed (344 MB): 77 us with a pass a warp, 75 with four a warp unrolled (290
-// instructions a pass), 66 with two passes ahead in registers, 58 as it is, 5.9 TB/s; a copy of the same bytes takes 50.
+// instructions a pass), 66 with two passes ahead in registers, 56 as it is, 6.1 TB/s; a copy of the same bytes takes 50.
 // Small blocks and many of them (seven of four warps an SM) hide the chain position -> angles -> first pass.
 template <int D, int ROT, bool KV4>
 __global__ void __launch_bounds__(32 * kWarps, kBlocks) qkv_kernel(const QkvParams p, int passes, uint32_t parts, int chunk) {
