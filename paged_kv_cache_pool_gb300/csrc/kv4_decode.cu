@@ -16,9 +16,9 @@
 // mask, but the warp-level products of 8-bit operands cost several times the fp16 ones on this chip: 608 requests of
 // 2048 tokens took 450 us so and 265 with fp16.)
 //
-// GB300, 4 requests of 262144 tokens, 32/8 heads of 128, pages of 16 (1.2 GB of rows): 210 us, 5.7 TB/s, 84 % of the
-// measured copy rate; the same work on rows that stay in L2 takes 187, so instructions bind it next to HBM: 473 a
-// warp and stage, half of the issue slots and of the ALU pipe's (masks, byte permutes, integer tests) busy.
+// GB300, 4 requests of 262144 tokens, 32/8 heads of 128, pages of 16 (1.2 GB of rows): 210 us, 5.8 TB/s, 85 % of the
+// measured copy rate; the same work on rows that stay in L2 takes 171, so instructions bind it next to HBM, half
+// of the issue slots and of the ALU pipe's (masks, byte permutes, integer tests) busy.
 #include <cmath>
 
 #include "device_common.cuh"
@@ -79,6 +79,13 @@ __device__ __forceinline__ void mma_bf16_first(float* d, uint32_t a0, uint32_t a
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(b0), "f"(0.f));
 }
+// D (16x8, fp32) = A (16x16, row) . B (16x8, col), bf16
+__device__ __forceinline__ void mma_bf16_first(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -128,6 +135,11 @@ constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u, kByte = 0x00ff00ffu;
 // tile are tokens (r >> 1) + 4 (r & 1) of its half, which lets the V loads below go without bank conflicts.
 // O^T[d x 8] += V^T . P^T: a thread's 8 bytes of each of four tokens, paired by two byte permutes, are the A fragments
 // of all m16 tiles; P^T is the weights of both heads a thread scored, times the token's span, through movmatrix.
+//
+// Up to four query heads fill half of the eight columns, so the columns are paired: column c + 4 is head c again, and
+// of the scores a column c < 4 takes the first tile's and c + 4 the second's.  A thread then scales, weighs and sums half as many scores,
+// none of them idle; P^T meets a tile with the other tile's columns masked, and the two halves of O are added in
+// the end.  On rows in L2 4 requests of 262144 tokens (g = 4) take 187 us without it and 171 with it, from HBM 212 and 210.
 template <int D, int G>
 __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_gather_kernel(const Kv4Params p) {
   constexpr int NG = D / 64;         // groups
@@ -136,6 +148,9 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
   constexpr int NST = kStages;
   constexpr int CPT = D / 16;        // 16-byte chunks of a token's codes (K and V)
   constexpr int TPI = 32 / CPT;      // tokens a copy instruction of the warp covers
+  constexpr bool PAIR = G <= 4;
+  constexpr int NS = PAIR ? 1 : 2;   // score fragments of a thread
+  constexpr int SHARE = PAIR ? 2 : 4;  // lanes that far apart and further hold the same heads
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int4 cache[kSegCache];
   const int lane = threadIdx.x & 31, h = threadIdx.x >> 5;
@@ -215,11 +230,11 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
       const uint32_t st = ring + (uint32_t)next * stage_bytes(D);
       // places past the stage's tokens get its last token's row: they meet weights and spans of 0
       const uint32_t sdst = st + kTok * D;
-      // All of the stage's scales by one instruction, but for pages of one token at d = 128: 608 requests of 2048 tokens (8 KV
-      // heads) take 463 us so, and 258 where the threads that just touched a token's row copy its scales, likely for the
-      // translation of the 32 places at once (380 and 292 by two and four instructions).  With pages of two tokens the one
-      // instruction takes 241 and the other form 255, at d = 64 with pages of one 86 and 90 (304 requests of 4096).
-      if (D == 64 || p.page > 1) {
+      // Pages of one token: 32 places at once cost address translations that one instruction for the stage's scales waits
+      // for in turn (608 requests of 2048 tokens, 8 KV heads of 128: 463 us), so the threads that copy a few tokens' codes next
+      // touch those rows' scales first (253; 280 behind the codes, 385 a copy later).  At d = 64, 304 requests of 4096: 8 KV heads
+      // 195 so and 260 by one instruction, 4 heads 87 and 85.  From pages of two on the one instruction takes 238, the other 255.
+      if (p.page > 1) {
 #pragma unroll
         for (int j = 0; j < kTok / TPI; ++j) {
           const int32_t s = __shfl_sync(0xffffffffu, slot, j * TPI + lane / CPT);
@@ -230,9 +245,9 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
 #pragma unroll
         for (int j = 0; j < kTok / TPI; ++j) {
           const int32_t s = __shfl_sync(0xffffffffu, slot, j * TPI + lane / CPT);
-          copy_async<16>(st + (j & 1 ? dst1 : dst0) + j * TPI * (D / 2), code_src + (int64_t)s * row_bytes);
           if (lane % CPT == 0)
             copy_async<D / 8>(sdst + (j * TPI + lane / CPT) * (D / 8), scale_src + (int64_t)s * row_bytes);
+          copy_async<16>(st + (j & 1 ? dst1 : dst0) + j * TPI * (D / 2), code_src + (int64_t)s * row_bytes);
         }
       }
       const uint32_t zero = __ballot_sync(0xffffffffu, bad);
@@ -272,7 +287,10 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
   const uint32_t k_at = D == 128 ? (uint32_t)((ta ^ (gq & 1)) * 64 + tq * 16) : (uint32_t)((ta ^ ((gq & 1) << 1)) * 32 + tq * 8);
   const uint32_t v_at = kTok * (D / 2) +
                         (D == 128 ? tq * 64 + ((gq >> 1) ^ ((tq >> 1) << 1)) * 16 + (gq & 1) * 8 : tq * 32 + gq * 4);
-  const uint32_t s_at = kTok * D + ta * (D / 8);
+  const uint32_t first = gq < 4 ? ~0u : 0u;                // paired: of weights, whose column is the first tile's
+  const int head = PAIR ? gq & 3 : gq;                     // of the query's fragments
+  const int half = PAIR ? tq >> 1 : 0;                     // this thread's tile
+  const uint32_t s_at = kTok * D + (ta + 16 * half) * (D / 8);
   int cslot = 0;
   for (int sg = sg0; sg < sg1; ++sg) {
     const int4 seg = seg_at(sg);
@@ -281,8 +299,9 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
     // between 2^13 and 2^14, so that fp16 holds a head's bf16 values to 2^-38 of the largest
     uint32_t qf[KW][4];
     float F[2];
-    uint32_t zf;                     // sum(q) of each group (times scale) as the B fragment that meets lo: column gq, rows
-                                     // 2 tq and 2 tq + 1 the groups' tq-th bf16 terms, three of which make fp32
+    // sum(q) of each group (times scale) as the B fragment that meets lo: column gq, rows 2 tq and 2 tq + 1 the groups' tq-th
+    // bf16 terms, three of which make fp32 (paired: rows of the column's own tile, terms tq & 1 and 2 + (tq & 1))
+    uint32_t zf[2] = {};
     {
       uint4 raw[KW];
       float top = 0.f, sum[NG] = {};
@@ -290,7 +309,7 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
       for (int i = 0; i < KW; ++i) {
         const int w = KW * tq + i, ch = D == 128 ? 8 * (w >> 1) + 64 * (w & 1) : 8 * w;   // channels ch .. ch + 7
         raw[i] = make_uint4(0, 0, 0, 0);
-        if (gq < G) raw[i] = *reinterpret_cast<const uint4*>(p.q + ((int64_t)seg.x * p.Hq + h * G + gq) * D + ch);
+        if (head < G) raw[i] = *reinterpret_cast<const uint4*>(p.q + ((int64_t)seg.x * p.Hq + h * G + head) * D + ch);
       }
 #pragma unroll
       for (int i = 0; i < KW; ++i) {
@@ -321,11 +340,10 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
 #pragma unroll
       for (int k = 0; k < 2; ++k) F[k] = __shfl_sync(0xffffffffu, f, 4 * (2 * tq + k));   // of query heads 2 tq and 2 tq + 1
       float z[2] = {sum[0] * p.scale, NG == 2 ? sum[NG - 1] * p.scale : 0.f};
-      zf = 0;
 #pragma unroll
       for (int k = 0; k < 3; ++k) {
         const uint32_t term = pack_bf16x2(z[0], z[1]);
-        if (tq == k) zf = term;
+        if (PAIR ? (gq >> 2) == half && (tq & 1) == (k & 1) : tq == k) zf[PAIR ? k >> 1 : 0] = term;
         z[0] -= bf_lo(term);
         z[1] -= bf_hi(term);
       }
@@ -347,11 +365,23 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
       const uint32_t st = ring + (uint32_t)cslot * stage_bytes(D);
       if (++cslot == NST) cslot = 0;
       // scores
-      float sc[2][4];                  // rows ta and ta + 8 of each tile, heads 2 tq and 2 tq + 1
-      uint32_t vscale[2][2][NG];       // V's (lo, span) of those tokens
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        uint32_t wa[KW], wb[KW], ka[NG], kb[NG];
+      float sc[NS][4];                 // rows ta and ta + 8 of a tile, heads 2 tq and 2 tq + 1 (paired: 2 (tq & 1) and the next)
+      uint32_t vscale[NS][2][NG];      // V's (lo, span) of those tokens
+      // K's (lo, span) of a fragment's tokens, and V's
+      auto scales = [&](uint32_t at, uint32_t* ka, uint32_t* kb, uint32_t (*v)[NG]) {
+        if (D == 128) {
+          const uint4 a = lds128(at), b = lds128(at + 8 * (D / 8));
+          ka[0] = a.x; ka[NG - 1] = a.y; v[0][0] = a.z; v[0][NG - 1] = a.w;
+          kb[0] = b.x; kb[NG - 1] = b.y; v[1][0] = b.z; v[1][NG - 1] = b.w;
+        } else {
+          const uint2 a = lds64(at), b = lds64(at + 8 * (D / 8));
+          ka[0] = a.x; v[0][0] = a.y;
+          kb[0] = b.x; v[1][0] = b.y;
+        }
+      };
+      auto both_lo = [&](const uint32_t* k) { return NG == 2 ? __byte_perm(k[0], k[NG - 1], 0x5410) : k[0] & 0xffffu; };
+      auto products = [&](int u, float (*acc)[4]) {
+        uint32_t wa[KW], wb[KW];
         const uint32_t kt = st + k_at + u * 16 * (D / 2);
         if (D == 128) {
           const uint4 a = lds128(kt), b = lds128(kt + 8 * (D / 2));
@@ -362,20 +392,6 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
           wa[0] = a.x; wa[1] = a.y;
           wb[0] = b.x; wb[1] = b.y;
         }
-        const uint32_t at = st + s_at + u * 16 * (D / 8);
-        if (D == 128) {
-          const uint4 a = lds128(at), b = lds128(at + 8 * (D / 8));
-          ka[0] = a.x; ka[NG - 1] = a.y; vscale[u][0][0] = a.z; vscale[u][0][NG - 1] = a.w;
-          kb[0] = b.x; kb[NG - 1] = b.y; vscale[u][1][0] = b.z; vscale[u][1][NG - 1] = b.w;
-        } else {
-          const uint2 a = lds64(at), b = lds64(at + 8 * (D / 8));
-          ka[0] = a.x; vscale[u][0][0] = a.y;
-          kb[0] = b.x; vscale[u][1][0] = b.y;
-        }
-        float acc[NG][4];
-        // the part of lo: k = 2 tq and 2 tq + 1 are the row's two groups
-        mma_bf16_first(sc[u], NG == 2 ? __byte_perm(ka[0], ka[NG - 1], 0x5410) : ka[0] & 0xffffu,
-                       NG == 2 ? __byte_perm(kb[0], kb[NG - 1], 0x5410) : kb[0] & 0xffffu, zf);
 #pragma unroll
         for (int i = 0; i < KW; ++i) {
           float* d = acc[D == 128 ? i & 1 : 0];
@@ -386,6 +402,8 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
           const uint32_t xa = wa[i] >> 8, xb = wb[i] >> 8;
           mma_f16(d, xa & kLow, xb & kLow, xa & kHigh, xb & kHigh, qf[i][2], qf[i][3]);
         }
+      };
+      auto scaled = [&](float* s, const uint32_t* ka, const uint32_t* kb, const float (*acc)[4]) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           float da = bf_hi(ka[0]) * acc[0][k], db = bf_hi(kb[0]) * acc[0][2 + k];
@@ -393,16 +411,41 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
             da = fmaf(bf_hi(ka[NG - 1]), acc[NG - 1][k], da);
             db = fmaf(bf_hi(kb[NG - 1]), acc[NG - 1][2 + k], db);
           }
-          sc[u][k] = fmaf(da, F[k], sc[u][k]);
-          sc[u][2 + k] = fmaf(db, F[k], sc[u][2 + k]);
+          s[k] = fmaf(da, F[k], s[k]);
+          s[2 + k] = fmaf(db, F[k], s[2 + k]);
+        }
+      };
+      uint32_t ka[NG], kb[NG];
+      if (PAIR) {
+        float acc[NG][4], other[NG][4];
+        scales(st + s_at, ka, kb, vscale[0]);
+        const uint32_t la = both_lo(ka), lb = both_lo(kb);
+        mma_bf16_first(sc[0], la, lb, la, lb, zf[0], zf[1]);
+        products(0, acc);
+        products(1, other);
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (half) acc[g][i] = other[g][i];
+        scaled(sc[0], ka, kb, acc);
+      } else {
+#pragma unroll
+        for (int u = 0; u < NS; ++u) {
+          float acc[NG][4];
+          scales(st + s_at + u * 16 * (D / 8), ka, kb, vscale[u]);
+          // the part of lo: k = 2 tq and 2 tq + 1 are the row's two groups
+          mma_bf16_first(sc[u], both_lo(ka), both_lo(kb), zf[0]);
+          products(u, acc);
+          scaled(sc[u], ka, kb, acc);
         }
       }
       if (n < kTok) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < NS; ++u)
 #pragma unroll
           for (int r = 0; r < 2; ++r)
-            if (16 * u + 8 * r + ta >= n) {
+            if (16 * (u + half) + 8 * r + ta >= n) {
               sc[u][2 * r] = sc[u][2 * r + 1] = -INFINITY;
 #pragma unroll
               for (int g = 0; g < NG; ++g) vscale[u][r][g] = 0;
@@ -410,24 +453,25 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
       }
       // The exponents' reference m is raised only where a score passes it by kSlack (a vote in place of a
       // maximum over the warp), the scale vs of V's spans lowered only where one passes `most`.
-      float d[2][4];
+      float d[NS][4];
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+      for (int u = 0; u < NS; ++u)
 #pragma unroll
         for (int i = 0; i < 4; i += 2)
           f2unpack(fadd2(f2pack(sc[u][i], sc[u][i + 1]), f2pack(-m[0], -m[1])), d[u][i], d[u][i + 1]);
       // (the span is a word's high half and not negative: words order as their spans)
       int32_t top = 0;
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+      for (int u = 0; u < NS; ++u)
 #pragma unroll
         for (int g = 0; g < NG; ++g) top = __vimax3_s32(top, (int32_t)vscale[u][0][g], (int32_t)vscale[u][1][g]);
-      const float past = fmaxf(fmax3(fmax3(d[0][0], d[0][1], d[0][2]), d[0][3], d[1][0]), fmax3(d[1][1], d[1][2], d[1][3]));
+      float past = fmaxf(fmax3(d[0][0], d[0][1], d[0][2]), d[0][3]);
+      if (!PAIR) past = fmax3(fmax3(past, d[NS - 1][0], d[NS - 1][1]), d[NS - 1][2], d[NS - 1][3]);
       if (__any_sync(0xffffffffu, past > kSlack || top > most)) {
-        float x0 = fmaxf(fmaxf(sc[0][0], sc[0][2]), fmaxf(sc[1][0], sc[1][2]));
-        float x1 = fmaxf(fmaxf(sc[0][1], sc[0][3]), fmaxf(sc[1][1], sc[1][3]));
+        float x0 = fmaxf(fmaxf(sc[0][0], sc[0][2]), fmaxf(sc[NS - 1][0], sc[NS - 1][2]));
+        float x1 = fmaxf(fmaxf(sc[0][1], sc[0][3]), fmaxf(sc[NS - 1][1], sc[NS - 1][3]));
 #pragma unroll
-        for (int off = 4; off < 32; off <<= 1) {
+        for (int off = SHARE; off < 32; off <<= 1) {
           x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, off));
           x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, off));
         }
@@ -461,14 +505,14 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
         m[0] = x0;
         m[1] = x1;
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < NS; ++u)
 #pragma unroll
           for (int i = 0; i < 4; ++i) d[u][i] = sc[u][i] - m[i & 1];
       }
+      uint32_t b[2][NG][2];            // P^T times the spans, of either tile
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        uint32_t b[NG][2];
-        float e[4];                    // rows a and b of head 2 tq, then of head 2 tq + 1
+      for (int u = 0; u < NS; ++u) {
+        float e[4];                    // rows a and b of the first head, then of the second
 #pragma unroll
         for (int i = 0; i < 4; ++i) e[i] = ex2(d[u][i]);
         l[0] += e[0];
@@ -488,9 +532,19 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
           float a0, b0, a1, b1;
           f2unpack(mul2(e0, span), a0, b0);
           f2unpack(mul2(e1, span), a1, b1);
-          b[g][0] = transpose8x8(pack_f16x2(a0, a1));
-          b[g][1] = transpose8x8(pack_f16x2(b0, b1));
+          b[u][g][0] = transpose8x8(pack_f16x2(a0, a1));
+          b[u][g][1] = transpose8x8(pack_f16x2(b0, b1));
+          if (PAIR) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              b[1][g][k] = b[0][g][k] & ~first;
+              b[0][g][k] &= first;
+            }
+          }
         }
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
         // tokens tq, tq + 4, tq + 8, tq + 12 of the tile
         uint32_t w[4][NG];
 #pragma unroll
@@ -511,27 +565,33 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
             const uint32_t x = __byte_perm(w[0][g], w[1][g], hf ? 0x7632 : 0x5410);
             const uint32_t y = __byte_perm(w[2][g], w[3][g], hf ? 0x7632 : 0x5410);
             const uint32_t x1 = __byte_perm(x, 0, 0x4341), y1 = __byte_perm(y, 0, 0x4341);
-            mma_f16(o[4 * g + 2 * hf], x & kLow, x & kByte, y & kLow, y & kByte, b[g][0], b[g][1]);
-            mma_f16(o[4 * g + 2 * hf + 1], x1 & kLow, x1, y1 & kLow, y1, b[g][0], b[g][1]);
+            mma_f16(o[4 * g + 2 * hf], x & kLow, x & kByte, y & kLow, y & kByte, b[u][g][0], b[u][g][1]);
+            mma_f16(o[4 * g + 2 * hf + 1], x1 & kLow, x1, y1 & kLow, y1, b[u][g][0], b[u][g][1]);
           }
         }
       }
       __syncwarp();                    // every lane has read the stage before it is refilled
     }
 
-    // the sums over tokens live on the eight threads that share tq
+    // the sums over tokens live on the threads that share a head, O's on the two that share its rows too
 #pragma unroll
-    for (int off = 4; off < 32; off <<= 1)
+    for (int off = SHARE; off < 32; off <<= 1)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         l[k] += __shfl_xor_sync(0xffffffffu, l[k], off);
 #pragma unroll
         for (int g = 0; g < NG; ++g) R[g][k] += __shfl_xor_sync(0xffffffffu, R[g][k], off);
       }
+    if (PAIR) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[i][k] += __shfl_xor_sync(0xffffffffu, o[i][k], 2);
+    }
     const float back = 1.f / vs;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const int hh = 2 * tq + k;
+      const int hh = 2 * tq + k;       // (paired: lanes from tq = 2 on hold what the others do)
       if (hh >= G) continue;
       const float inv = 1.f / l[k], f = inv * (16777216.f / 15.f);
       const int64_t row = (int64_t)(dest >= 0 ? dest : ~dest) * p.Hq + h * G + hh;
