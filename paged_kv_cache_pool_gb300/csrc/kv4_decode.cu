@@ -627,16 +627,18 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
 // O = sum_e 2^(l_e - m) O_e / sum_e 2^(l_e - m), LSE = (m + log2 sum_e 2^(l_e - m)) ln 2 over the partial
 // states of a request, m the largest l_e, for each query head.  WARPS warps share a row: each joins the states
 // e = its index + WARPS i, then the first one theirs.  A state of LSE -inf (weight 0) may hold anything.
+// SPLIT blocks share a row's channels (one request of 131072 tokens, 32 rows of 304 states: the step 36.7 us, 35.7 by four).
 // Bound by latency: a warp asks for eight states' rows before it uses any.
-template <int D, int WARPS>
+template <int D, int WARPS, int SPLIT = 1>
 __global__ void __launch_bounds__(WARPS > 8 ? 32 * WARPS : 256) kv4_join_kernel(const float* part_o, const float* part_l, const RequestDev* __restrict__ reqs,
                                                        int32_t B, int32_t Hq, uint16_t* out, float* lse) {
-  constexpr int C = D / 32;            // channels of a thread
+  constexpr int C = D / 32 / SPLIT;    // channels of a thread
   constexpr int N = WARPS > 8 ? WARPS : 8;  // warps of a block
-  __shared__ float sm[N], sz[N], so[N][D];
+  __shared__ float sm[N], sz[N], so[N][D / SPLIT];
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % WARPS;
-  const int64_t w = blockIdx.x * (int64_t)(N / WARPS) + warp / WARPS;
+  const int64_t w = SPLIT > 1 ? blockIdx.x / SPLIT : blockIdx.x * (int64_t)(N / WARPS) + warp / WARPS;
+  const int ch = (SPLIT > 1 ? blockIdx.x % SPLIT * (D / SPLIT) : 0) + lane * C;   // the thread's first
   const bool row = w < (int64_t)B * Hq;
   const int r = row ? (int)(w / Hq) : 0, qh = (int)(w % Hq);
   const int e0 = reqs[r].entry_cas, ne = row ? reqs[r].n_entry_cas : -1;
@@ -650,11 +652,13 @@ __global__ void __launch_bounds__(WARPS > 8 ? 32 * WARPS : 256) kv4_join_kernel(
       const int64_t at = (int64_t)(e0 + min(e, ne - 1)) * Hq + qh;
       l[k] = e < ne ? __ldcg(part_l + at) : -INFINITY;
       if (C == 4) {
-        const float4 x = __ldcg(reinterpret_cast<const float4*>(part_o + at * D) + lane);
-        v[k][0] = x.x; v[k][1] = x.y; v[k][C - 2] = x.z; v[k][C - 1] = x.w;
+        const float4 x = __ldcg(reinterpret_cast<const float4*>(part_o + at * D + ch));
+        v[k][0] = x.x; v[k][1 % C] = x.y; v[k][C < 2 ? 0 : C - 2] = x.z; v[k][C - 1] = x.w;
+      } else if (C == 2) {
+        const float2 x = __ldcg(reinterpret_cast<const float2*>(part_o + at * D + ch));
+        v[k][0] = x.x; v[k][C - 1] = x.y;
       } else {
-        const float2 x = __ldcg(reinterpret_cast<const float2*>(part_o + at * D) + lane);
-        v[k][0] = x.x; v[k][1] = x.y;
+        v[k][0] = __ldcg(part_o + at * D + ch);
       }
     }
     float top = m;
@@ -703,10 +707,14 @@ __global__ void __launch_bounds__(WARPS > 8 ? 32 * WARPS : 256) kv4_join_kernel(
   }
   if (ne < 0) return;                  // written by its only segment
   const float inv = m == -INFINITY ? 0.f : 1.f / z;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(out + w * D) + lane * (C / 2);
+  if (C == 1) {
+    out[w * D + ch] = (uint16_t)pack_bf16x2(o[0] * inv, 0.f);
+  } else {
+    uint32_t* dst = reinterpret_cast<uint32_t*>(out + w * D + ch);
 #pragma unroll
-  for (int c = 0; c < C; c += 2) dst[c / 2] = pack_bf16x2(o[c] * inv, o[c + 1] * inv);
-  if (lane == 0 && lse) lse[w] = m == -INFINITY ? -INFINITY : (m + __log2f(z)) * kLn2;
+    for (int c = 0; c < C; c += 2) dst[c / 2] = pack_bf16x2(o[c] * inv, o[(c + 1) % C] * inv);
+  }
+  if (ch == 0 && lse) lse[w] = m == -INFINITY ? -INFINITY : (m + __log2f(z)) * kLn2;
 }
 
 size_t gather_smem(int hkv, int d) { return (size_t)hkv * kStages * stage_bytes(d); }
@@ -784,10 +792,20 @@ int launch_kv4_join(const LaunchCommon& lc, void* stream, const gk_batch* b, con
   const int most = pl->kv4_most_states;
   // a warp a row while two rounds hold its states, or while the rows alone fill the SMs
   const int warps = most <= 16 || rows >= 32 * (int64_t)lc.num_sms ? 1 : most <= 64 ? 8 : 32;
+  // as many blocks a row as one wave holds (of 32 warps; 128 rows by four, in four waves, cost the step 10 %)
+  const int most_split = c.head_dim / 32, sms = lc.num_sms;
+  const int split = warps < 32 ? 1 : rows * most_split <= sms ? most_split : rows * 2 <= sms ? 2 : 1;
   auto kern = c.head_dim == 128
-                  ? (warps == 1 ? kv4_join_kernel<128, 1> : warps == 8 ? kv4_join_kernel<128, 8> : kv4_join_kernel<128, 32>)
-                  : (warps == 1 ? kv4_join_kernel<64, 1> : warps == 8 ? kv4_join_kernel<64, 8> : kv4_join_kernel<64, 32>);
-  return (int)launch_pdl(kern, dim3((unsigned)(warps == 1 ? (rows + 7) / 8 : rows)), dim3(warps == 32 ? 1024 : 256), 0,
+                  ? (warps == 1   ? kv4_join_kernel<128, 1>
+                     : warps == 8 ? kv4_join_kernel<128, 8>
+                     : split == 4 ? kv4_join_kernel<128, 32, 4>
+                     : split == 2 ? kv4_join_kernel<128, 32, 2>
+                                  : kv4_join_kernel<128, 32>)
+                  : (warps == 1   ? kv4_join_kernel<64, 1>
+                     : warps == 8 ? kv4_join_kernel<64, 8>
+                     : split == 2 ? kv4_join_kernel<64, 32, 2>
+                                  : kv4_join_kernel<64, 32>);
+  return (int)launch_pdl(kern, dim3((unsigned)(warps == 1 ? (rows + 7) / 8 : rows * split)), dim3(warps == 32 ? 1024 : 256), 0,
                          (cudaStream_t)stream, pl->d_part_o, pl->d_part_l,
                          (const RequestDev*)((const uint8_t*)pl->d_buf + pl->off_reqs), pl->B, c.num_q_heads, (uint16_t*)d_out,
                          b->d_lse);

@@ -123,6 +123,15 @@ def test_lengths(cold):
     s.close()
 
 
+@pytest.mark.parametrize("d,g,hkv,requests", [(128, 4, 8, 1), (128, 5, 8, 1), (128, 5, 8, 2), (128, 8, 8, 3), (64, 2, 8, 1), (64, 4, 8, 3)])
+def test_joins_of_many_states(d, g, hkv, requests):
+    """From 16 to 192 rows of a hundred states and more, some behind a prefix: every number of blocks that shares a row's join."""
+    s = Step(d, g, hkv, [9000] * requests, [700], [0] + [-1] * (requests - 1), seed=g)
+    s.run()
+    s.check()
+    s.close()
+
+
 def test_random_steps():
     rnd = random.Random(4)
     for i in range(40):
