@@ -10,7 +10,8 @@
 // A warp takes the heads of one token 256 channels at a time (8 heads of 64 or 4 of 128), 16
 // channels a thread in two 16-byte chunks: chunk j and chunk j + d / 16 of the head, the two
 // that a rotation of the whole head pairs, and at d = 128 one of either group of 64 that 4-bit
-// rows scale together.
+// rows scale together.  Where a part of the head rotates in halves the chunks are dealt out so
+// that a thread still holds both of a pair.
 #include <cstdint>
 
 #include "device_common.cuh"
@@ -130,19 +131,27 @@ __device__ __forceinline__ uint32_t codes8(const float* x, float lo, float span)
   return span == 0.f ? 0u : w - kBits * 0x11111111u;
 }
 
-// What the rotation of a thread's two chunks takes: of whole heads in halves one set of eight cosines and sines for the
-// pairs (i, i + 8) of its 16 channels, of neighbouring pairs four for each chunk, of a part in halves eight for each.
-template <int ROT>
+// The two chunks of a head that lane j of its LPH holds: j and j + LPH; where a part of the head rotates in halves, of hc chunks
+// each, the first hc lanes hold the chunks that pair, j and j + hc, and the others the rest in order.
+template <int D, int ROT>
+__device__ __forceinline__ void chunks_of(int j, int hc, int& c0, int& c1) {
+  constexpr int LPH = D / 16;
+  c0 = ROT == kPart && j >= hc ? j + hc : j;
+  c1 = ROT == kPart && j < hc ? j + hc : j + LPH;
+}
+
+// What the rotation of a thread's two chunks takes: eight cosines and sines, in halves of the pairs (i, i + 8) of its 16
+// channels, of neighbouring pairs four for each chunk.
 struct Angles {
-  float c[ROT == kPart ? 16 : 8], s[ROT == kPart ? 16 : 8];
+  float c[8], s[8];
 };
 
 template <int D, int ROT>
-__device__ __forceinline__ void load_angles(const QkvParams& p, int64_t at, int j, Angles<ROT>& w) {
+__device__ __forceinline__ void load_angles(const QkvParams& p, int64_t at, int j, Angles& w) {
   constexpr int LPH = D / 16;
   const float* cs = p.table + at * p.rot;
   const int half = p.rot / 2;
-  if (ROT == kHalves) {
+  if (ROT == kHalves || (ROT == kPart && 8 * j < half)) {
     load8(cs + 8 * j, w.c);
     load8(cs + half + 8 * j, w.s);
   } else if (ROT == kPairs) {
@@ -155,23 +164,14 @@ __device__ __forceinline__ void load_angles(const QkvParams& p, int64_t at, int 
       w.c[4 * b] = x.x; w.c[4 * b + 1] = x.y; w.c[4 * b + 2] = x.z; w.c[4 * b + 3] = x.w;
       w.s[4 * b] = y.x; w.s[4 * b + 1] = y.y; w.s[4 * b + 2] = y.z; w.s[4 * b + 3] = y.w;
     }
-  } else if (ROT == kPart) {
-    const int hc = half / 8;
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const int ch = j + b * LPH, i = ch < hc ? ch : ch - hc;
-      if (ch >= 2 * hc) continue;
-      load8(cs + 8 * i, w.c + 8 * b % (ROT == kPart ? 16 : 8));
-      load8(cs + half + 8 * i, w.s + 8 * b % (ROT == kPart ? 16 : 8));
-    }
   }
 }
 
-// x: chunk j of a head, then chunk j + D / 16
+// x: the thread's two chunks
 template <int D, int ROT>
-__device__ __forceinline__ void rotate(const QkvParams& p, int j, int lane, const Angles<ROT>& w, float* x) {
+__device__ __forceinline__ void rotate(const QkvParams& p, int j, const Angles& w, float* x) {
   constexpr int LPH = D / 16;
-  if (ROT == kHalves) {
+  if (ROT == kHalves || (ROT == kPart && 16 * j < p.rot)) {
     const uint64_t one = f2pack(p.one, p.one), minus = f2pack(-1.f, -1.f);
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
@@ -184,44 +184,13 @@ __device__ __forceinline__ void rotate(const QkvParams& p, int j, int lane, cons
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if ((j + i / 4 * LPH) * 8 < p.rot) turn(x[2 * i], x[2 * i + 1], w.c[i], w.s[i]);
-  } else if (ROT == kPart) {
-    // chunk ch < rot / 16 pairs with chunk ch + rot / 16, which another thread of the head may hold
-    const int hc = p.rot / 16;
-    float other[16];
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const int ch = j + b * LPH;
-      const int pc = ch < hc ? ch + hc : ch < 2 * hc ? ch - hc : ch;
-      const int from = (lane & ~(LPH - 1)) | (pc & (LPH - 1));
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        // not all that ask a thread want the same of its chunks: both cross
-        const float lo = __shfl_sync(0xffffffffu, x[i], from), hi = __shfl_sync(0xffffffffu, x[i + 8], from);
-        other[8 * b + i] = pc < LPH ? lo : hi;
-      }
-    }
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const int ch = j + b * LPH;
-      if (ch >= 2 * hc) continue;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int k = (8 * b + i) % (ROT == kPart ? 16 : 8);
-        float mine = x[8 * b + i], theirs = other[8 * b + i];
-        if (ch < hc)
-          turn(mine, theirs, w.c[k], w.s[k]);
-        else
-          turn(theirs, mine, w.c[k], w.s[k]);
-        x[8 * b + i] = mine;
-      }
-    }
   }
 }
 
-// Codes and scales of a thread's chunks y0 and y1 (bf16) of head h, K or V, to its token's row; all threads of the
-// warp call it, those with ok store.
-template <int D>
-__device__ __forceinline__ void store_codes(uint4 y0, uint4 y1, uint8_t* row, int hkv, int h, bool is_v, int j, bool ok) {
+// Codes and scales of a thread's chunks c0 and c1 (y0 and y1, bf16) of head h, K or V, to its token's row; all threads of
+// the warp call it, those with ok store.  ANY: the chunks are not j and j + LPH.
+template <int D, bool ANY>
+__device__ __forceinline__ void store_codes(uint4 y0, uint4 y1, uint8_t* row, int hkv, int h, bool is_v, int j, int c0, int c1, bool ok) {
   constexpr int LPH = D / 16;
   float x[16];
   unpack8(y0, x);
@@ -231,9 +200,14 @@ __device__ __forceinline__ void store_codes(uint4 y0, uint4 y1, uint8_t* row, in
   const uint32_t b0 = max2(max2(y0.x, y0.y), max2(y0.z, y0.w)), b1 = max2(max2(y1.x, y1.y), max2(y1.z, y1.w));
   uint32_t lo = min2(__byte_perm(a0, a1, 0x5410), __byte_perm(a0, a1, 0x7632));
   uint32_t hi = max2(__byte_perm(b0, b1, 0x5410), __byte_perm(b0, b1, 0x7632));
+  const bool second0 = ANY && D == 128 && c0 >= LPH, first1 = ANY && D == 128 && c1 < LPH;
   if (D == 64) {     // both chunks are of the head's one group
     lo = min2(lo, __byte_perm(lo, 0, 0x1032));
     hi = max2(hi, __byte_perm(hi, 0, 0x1032));
+  } else if (second0 || first1) {  // of one group, the halves' other one gets an infinity
+    const uint32_t l = min2(lo, __byte_perm(lo, 0, 0x1032)), g = max2(hi, __byte_perm(hi, 0, 0x1032));
+    lo = __byte_perm(l, 0x7f80u, second0 ? 0x1054 : 0x5410);
+    hi = __byte_perm(g, 0xff80u, second0 ? 0x1054 : 0x5410);
   }
 #pragma unroll
   for (int off = 1; off < LPH; off <<= 1) {
@@ -245,14 +219,21 @@ __device__ __forceinline__ void store_codes(uint4 y0, uint4 y1, uint8_t* row, in
   uint8_t* scales = row + kv4::scales_at(hkv, h, D) + (is_v ? D / 16 : 0);
   float span;
   const uint32_t s0 = group_scale(bf_lo(lo), bf_lo(hi), span);
-  const uint32_t c0 = codes8(x, bf_lo(lo), span);
   if (D == 64) {
-    reinterpret_cast<uint32_t*>(codes)[j] = c0;
-    reinterpret_cast<uint32_t*>(codes)[j + LPH] = codes8(x + 8, bf_lo(lo), span);
+    reinterpret_cast<uint32_t*>(codes)[c0] = codes8(x, bf_lo(lo), span);
+    reinterpret_cast<uint32_t*>(codes)[c1] = codes8(x + 8, bf_lo(lo), span);
     if (j == 0) *reinterpret_cast<uint32_t*>(scales) = s0;
   } else {
-    const uint32_t s1 = group_scale(bf_hi(lo), bf_hi(hi), span);
-    reinterpret_cast<uint2*>(codes)[j] = make_uint2(c0, codes8(x + 8, bf_hi(lo), span));
+    float span1;
+    const uint32_t s1 = group_scale(bf_hi(lo), bf_hi(hi), span1);
+    const uint32_t w0 = codes8(x, second0 ? bf_hi(lo) : bf_lo(lo), second0 ? span1 : span);
+    const uint32_t w1 = codes8(x + 8, first1 ? bf_lo(lo) : bf_hi(lo), first1 ? span : span1);
+    if (ANY) {       // word 2 (c % LPH) + c / LPH is chunk c's
+      reinterpret_cast<uint32_t*>(codes)[second0 ? 2 * (c0 - LPH) + 1 : 2 * c0] = w0;
+      reinterpret_cast<uint32_t*>(codes)[first1 ? 2 * c1 : 2 * (c1 - LPH) + 1] = w1;
+    } else {
+      reinterpret_cast<uint2*>(codes)[j] = make_uint2(w0, w1);
+    }
     if (j == 0) *reinterpret_cast<uint2*>(scales) = make_uint2(s0, s1);
   }
 }
@@ -275,9 +256,12 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks) qkv_kernel(const QkvPara
   if (tok >= p.n) return;
   const int first = (int)(w - of_token * parts) * chunk, end = min(passes, first + chunk);
   const int q_passes = (p.Hq + HPW - 1) / HPW, k_end = q_passes + (p.Hkv + HPW - 1) / HPW;
-  const uint16_t* const src_q = p.q + tok * p.qs + 8 * j;
-  const uint16_t* const src_k = p.k + tok * p.ks + 8 * j;
-  const uint16_t* const src_v = p.v + tok * p.vs + 8 * j;
+  int c0, c1;                       // this thread's chunks of a head
+  chunks_of<D, ROT>(j, p.rot / 16, c0, c1);
+  const int apart = 8 * (c1 - c0);
+  const uint16_t* const src_q = p.q + tok * p.qs + 8 * c0;
+  const uint16_t* const src_k = p.k + tok * p.ks + 8 * c0;
+  const uint16_t* const src_v = p.v + tok * p.vs + 8 * c0;
   // pass i is of q, k or v (kind 0, 1, 2), head h this thread's
   auto kind_of = [&](int i) { return i < q_passes ? 0 : i < k_end ? 1 : 2; };
   auto head_of = [&](int i, int kind) {
@@ -293,14 +277,14 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks) qkv_kernel(const QkvPara
     if (h < (kind == 0 ? p.Hq : p.Hkv)) {
       const uint32_t dst = smem_u32(buf + (i - first) * 64);
       cp_async16(dst, src);
-      cp_async16(dst + 512, src + 8 * LPH);
+      cp_async16(dst + 512, src + apart);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   }
   for (int i = end - first; i < kChunk; ++i) asm volatile("cp.async.commit_group;" ::: "memory");
   int64_t slot = -1;
   if (p.slots) slot = p.slots[tok];
-  Angles<ROT> angles;
+  Angles angles;
   if (ROT != kNone) {
     const int64_t at = p.pos[tok];
     if (at < 0 || at >= p.num_pos) {
@@ -329,8 +313,8 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks) qkv_kernel(const QkvPara
       if (weight) {
         if (of != kind) {
           of = kind;
-          unpack8(reinterpret_cast<const uint4*>(weight)[j], g);
-          unpack8(reinterpret_cast<const uint4*>(weight)[j + LPH], g + 8);
+          unpack8(reinterpret_cast<const uint4*>(weight)[c0], g);
+          unpack8(reinterpret_cast<const uint4*>(weight)[c1], g + 8);
         }
         uint64_t sum = 0;
 #pragma unroll
@@ -349,22 +333,22 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks) qkv_kernel(const QkvPara
         for (int k = 0; k < 16; k += 2)
           f2unpack(mul2(mul2(f2pack(x[k], x[k + 1]), rr), f2pack(g[k], g[k + 1])), x[k], x[k + 1]);
       }
-      rotate<D, ROT>(p, j, lane, angles, x);
+      rotate<D, ROT>(p, j, angles, x);
       y0 = pack8(x);
       y1 = pack8(x + 8);
       uint16_t* out = kind == 0 ? p.q_out + tok * p.qos : p.k_out ? p.k_out + tok * p.kos : nullptr;
       if (out && mine) {
-        *reinterpret_cast<uint4*>(out + h * D + 8 * j) = y0;
-        *reinterpret_cast<uint4*>(out + h * D + 8 * (j + LPH)) = y1;
+        *reinterpret_cast<uint4*>(out + h * D + 8 * c0) = y0;
+        *reinterpret_cast<uint4*>(out + h * D + 8 * c1) = y1;
       }
       if (kind == 0 || !p.slots) continue;
     }
     if (KV4) {
-      store_codes<D>(y0, y1, p.rows + slot * kv4::row_bytes(p.Hkv, D), p.Hkv, h, kind == 2, j, stored && mine);
+      store_codes<D, ROT == kPart>(y0, y1, p.rows + slot * kv4::row_bytes(p.Hkv, D), p.Hkv, h, kind == 2, j, c0, c1, stored && mine);
     } else if (stored && mine) {
-      uint16_t* out = (kind == 1 ? p.cold_k : p.cold_v) + (slot * p.Hkv + h) * D + 8 * j;
+      uint16_t* out = (kind == 1 ? p.cold_k : p.cold_v) + (slot * p.Hkv + h) * D + 8 * c0;
       *reinterpret_cast<uint4*>(out) = y0;
-      *reinterpret_cast<uint4*>(out + 8 * LPH) = y1;
+      *reinterpret_cast<uint4*>(out + apart) = y1;
     }
   }
 }

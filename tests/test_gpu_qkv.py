@@ -163,6 +163,31 @@ def test_append(d, g, hkv, page, bits):
     eng.close()
 
 
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("d,rot", [(64, 16), (64, 32), (64, 48), (128, 16), (128, 48), (128, 64), (128, 80), (128, 112)])
+def test_append_of_heads_that_rotate_in_part(d, rot, bits):
+    """What the cache holds, and a group of NaN in it, is what gk_append_kv stores of rows that were rotated before."""
+    eng = Engine(1, 8, 4, d, 64, 512, 1, kv_bits=bits)
+    x = Rows(300, 8, 4, d, 8)
+    x.v[7, 1, d - 1] = float("nan")
+    x.v[9, 2, 0] = float("inf")
+    rope = eng.rope(eng.rope_table(5000, rot), False, *x.weights)
+    slots = torch.randperm(512, device="cuda")[:300]
+    q, k, q2, k2 = (torch.empty(300, h, d, dtype=BF, device="cuda") for h in (8, 4, 8, 4))
+    eng.qk_norm_rope(rope, x.pos, x.q, x.k, q, k)
+    store = [eng.cold] if bits == 4 else [eng.cold_k, eng.cold_v]
+    for s in store:
+        s.view(torch.uint8).fill_(0x5A)
+    eng.append_kv(0, slots, k, x.v.contiguous())
+    want = [s.clone() for s in store]
+    for s in store:
+        s.view(torch.uint8).fill_(0x5A)
+    eng.append_qkv(0, rope, x.pos, slots, x.q, x.k, x.v, q2, k2)
+    assert torch.equal(q, q2) and torch.equal(k, k2)
+    assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(store, want))
+    eng.close()
+
+
 def check_codes(rows, k, v, rk, rv):
     """Rows hold the documented codes of k and v in the documented places, and read back as what they stand for."""
     n, hkv, d = k.shape
