@@ -250,9 +250,11 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
           copy_async<16>(st + (j & 1 ? dst1 : dst0) + j * TPI * (D / 2), code_src + (int64_t)s * row_bytes);
         }
       }
-      const uint32_t zero = __ballot_sync(0xffffffffu, bad);
+      uint32_t zero = __ballot_sync(0xffffffffu, bad);
       if (zero) {
-        // ids outside the pool: their tokens' rows count as zeros
+        // ids outside the pool: their tokens' rows count as zeros, and the last token's so do in the places past the stage's, as a
+        // NaN there, though it meets weights of 0, would reach the scores of the other tile's row through the product with lo
+        if (zero >> (idn - 1)) zero |= ~0u << (idn - 1);
         asm volatile("cp.async.wait_all;" ::: "memory");
         __syncwarp();
         if (bad) report_error(p.err, kErrBounds);

@@ -522,3 +522,28 @@ def test_refusals_with_storage():
     s.run()
     s.check()
     s.close()
+
+
+@pytest.mark.parametrize("d,g", [(64, 1), (64, 2), (64, 4), (128, 1), (128, 4), (128, 5), (128, 8)])
+@pytest.mark.parametrize("page,length", [(1, 70), (4, 70), (1, 33), (16, 37), (64, 31), (1, 17)])
+def test_bad_last_block_of_a_request(d, g, page, length):
+    """A request whose last token is in a bad block, in a stage that it does not fill, while the pool's first rows hold NaN: its
+    places past the end must not bring any of them in."""
+    s = Step(d, g, 2, [length] * 3, page=page, seed=page)
+    table = s.table.cpu().numpy().copy()
+    K, V, size = (x.copy() for x in values(s.eng.cold[1, s.slots].cpu().numpy(), 2, d))
+    last = (length - 1) // page
+    free = [r for r in range(3) if 0 not in table[r, :last]]
+    assert len(free) >= 2
+    table[:, last] = -3
+    s.table.copy_(torch.from_numpy(table))
+    s.eng.cold[1, :page].fill_(0xFF)
+    s.run()
+    torch.cuda.synchronize()
+    assert s.eng.device_error() == gk.GK_ERR_DEVICE_BOUNDS
+    none = np.zeros((0, 2, d))
+    for r in free:
+        i, bad = slice(r * length, (r + 1) * length), slice(r * length + last * page, (r + 1) * length)
+        K[bad], V[bad], size[bad] = 0, 0, 0
+        check_attention(np64(s.out[r]), np64(s.lse[r]), attend(np64(s.q[r]), (none, none), (K[i], V[i], size[i])), f"request {r}")
+    s.close()
