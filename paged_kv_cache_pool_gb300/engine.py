@@ -25,6 +25,8 @@ Every method is one library call; the work is in libgk.
 """
 from __future__ import annotations
 
+import contextlib
+
 import numpy as np
 
 from . import binding as gk
@@ -120,10 +122,22 @@ class Engine:
     def append_qkv(self, layer, rope, positions, d_slots, q, k, v, q_out=None, k_out=None, d_cow=None, stream=None):
         gk.gk_append_qkv(self.pool, stream, layer, rope, positions, d_slots, q, k, v, q_out, k_out, d_cow)
 
+    def _on(self, stream):
+        """What torch allocates inside this belongs to the stream of the call that follows (None: the default stream)."""
+        torch, raw = self.torch, gk._stream(stream) or 0
+        if raw == torch.cuda.current_stream(self.device).cuda_stream:
+            return contextlib.nullcontext()
+        if stream is None:
+            raise ValueError("a stream is current that is not the default one: name the stream of the call, on which its results are used")
+        return torch.cuda.stream(torch.cuda.ExternalStream(raw, device=self.device) if raw else torch.cuda.default_stream(self.device))
+
     def read_kv(self, layer, d_slots, k=None, v=None, stream=None):
-        """-> (K, V) bf16 [n, Hkv, d] of the COLD slots."""
-        shape = dict(size=(d_slots.numel(), self.Hkv, self.d), dtype=self.torch.bfloat16, device=self.device)
-        k, v = (self.torch.empty(**shape) if x is None else x for x in (k, v))
+        """-> (K, V) bf16 [n, Hkv, d] of the COLD slots.  What is not given is allocated for `stream`, and is used there (or on
+        others that wait for it) until it is dropped; without a stream, where another than the default one is current, ValueError."""
+        if k is None or v is None:
+            shape = dict(size=(d_slots.numel(), self.Hkv, self.d), dtype=self.torch.bfloat16, device=self.device)
+            with self._on(stream):
+                k, v = (self.torch.empty(**shape) if x is None else x for x in (k, v))
         gk.gk_read_kv(self.pool, stream, layer, d_slots, k, v)
         return k, v
 

@@ -433,3 +433,74 @@ def test_special_values_of_rows():
     eng.qk_norm_rope(rope_norm, x.pos, z, None)
     assert (z == 0).all()
     eng.close()
+
+
+def busy():
+    """Tens of milliseconds of work on the current stream."""
+    a = torch.randn(8192, 8192, device="cuda").to(BF)
+    for _ in range(40):
+        a = a @ a
+
+
+def stored_rows(n=20000):
+    eng = Engine(1, 8, 8, 128, 64, n, 1, kv_bits=4)
+    slots = torch.arange(n, device="cuda")
+    k, v = (torch.randn(n, 8, 128, device="cuda").to(BF) for _ in range(2))
+    eng.append_kv(0, slots, k, v)
+    want = [x.clone() for x in eng.read_kv(0, slots)]
+    torch.cuda.synchronize()
+    return eng, slots, want
+
+
+def test_rows_read_on_a_side_stream_are_of_that_stream():
+    """What read_kv allocates is not memory that the current stream still uses, and what is dropped is not handed to the current
+    stream while the side stream still uses it."""
+    eng, slots, want = stored_rows()
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        used = [torch.empty_like(x) for x in want]
+        torch.cuda.synchronize()
+        busy()
+        for x in used:
+            x.fill_(7)
+        del used, x                                     # free for the current stream, whose fills are still to come
+        got = eng.read_kv(0, slots, stream=stream)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    copies = [torch.empty_like(x) for x in want]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        busy()
+        got = eng.read_kv(0, slots, stream=side)
+        for a, b in zip(copies, got):
+            a.copy_(b)
+    del got, a, b
+    other = [torch.full_like(x, 7) for x in want]        # on the current stream, at once
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(copies, want)) and all((x == 7).all() for x in other)
+    eng.close()
+
+
+def test_rows_read_without_a_stream_of_their_own():
+    """On the default stream while another one is current: refused unless both outputs are given; in a capture, its stream is named."""
+    eng, slots, want = stored_rows(300)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        with pytest.raises(ValueError, match="stream"):
+            eng.read_kv(0, slots)
+        side.synchronize()
+    k, v = (torch.empty_like(x) for x in want)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        eng.read_kv(0, slots, k, v)
+    torch.cuda.synchronize()
+    assert torch.equal(k, want[0]) and torch.equal(v, want[1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = eng.read_kv(0, slots, stream=torch.cuda.current_stream())
+    for x in got:
+        x.fill_(7)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    eng.close()
