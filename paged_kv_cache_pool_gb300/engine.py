@@ -127,14 +127,14 @@ class Engine:
         torch, raw = self.torch, gk._stream(stream) or 0
         if raw == torch.cuda.current_stream(self.device).cuda_stream:
             return contextlib.nullcontext()
-        if stream is None:
-            raise ValueError("a stream is current that is not the default one: name the stream of the call, on which its results are used")
         return torch.cuda.stream(torch.cuda.ExternalStream(raw, device=self.device) if raw else torch.cuda.default_stream(self.device))
 
     def read_kv(self, layer, d_slots, k=None, v=None, stream=None):
         """-> (K, V) bf16 [n, Hkv, d] of the COLD slots.  What is not given is allocated for `stream`, and is used there (or on
         others that wait for it) until it is dropped; without a stream, where another than the default one is current, ValueError."""
         if k is None or v is None:
+            if stream is None and self.torch.cuda.current_stream(self.device).cuda_stream:
+                raise ValueError("a stream is current that is not the default one: name the stream of the call, on which its results are used")
             shape = dict(size=(d_slots.numel(), self.Hkv, self.d), dtype=self.torch.bfloat16, device=self.device)
             with self._on(stream):
                 k, v = (self.torch.empty(**shape) if x is None else x for x in (k, v))
@@ -166,9 +166,11 @@ class Engine:
         return tables, seq
 
     def tables_step(self, tables, d_add, n_slots, d_release=None, stream=None):
-        """-> (slot mapping [n_slots], tokens placed per row) of one step (gk_tables_step)."""
-        slots = self.torch.empty(n_slots, dtype=self.torch.int64, device=self.device)
-        done = self.torch.empty_like(tables.length)
+        """-> (slot mapping [n_slots], tokens placed per row) of one step (gk_tables_step), allocated for `stream` (None: the
+        default stream) as read_kv's rows are."""
+        with self._on(stream):
+            slots = self.torch.empty(n_slots, dtype=self.torch.int64, device=self.device)
+            done = self.torch.empty_like(tables.length)
         gk.gk_tables_step(self.pool, stream, tables, d_add, slots, done, d_release)
         return slots, done
 

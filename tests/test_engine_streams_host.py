@@ -46,7 +46,8 @@ def engine(monkeypatch):
         eng = Engine.__new__(Engine)
         eng.pool = None
         eng.__dict__.update(Hkv=2, d=64, device="cuda", _plans=[], _prompt_plans=[])
-        eng.torch = SimpleNamespace(cuda=cuda, empty=empty, bfloat16=torch.bfloat16, int64=torch.int64)
+        eng.torch = SimpleNamespace(cuda=cuda, empty=empty, empty_like=lambda x: empty(x.shape, dtype=x.dtype), bfloat16=torch.bfloat16,
+                                    int64=torch.int64)
         return eng, owners, calls
     return make
 
@@ -78,3 +79,13 @@ def test_rows_of_no_stream_while_another_is_current(engine):
     assert not owners and not calls
     eng.read_kv(0, slots, torch.empty(5, 2, 64), torch.empty(5, 2, 64))
     assert calls == [("gk_read_kv", None)]
+
+
+@pytest.mark.parametrize("current,stream,owner", [(0, None, 0), (0, SIDE, SIDE), (SIDE, SIDE, SIDE), (SIDE, OTHER, OTHER), (SIDE, 0, 0),
+                                                  (SIDE, None, 0)])
+def test_slots_belong_to_the_stream_that_writes_them(engine, current, stream, owner):
+    eng, owners, calls = engine(current)
+    tables = SimpleNamespace(length=torch.zeros(3, dtype=torch.int32))
+    slots, done = eng.tables_step(tables, None, 7, stream=stream)
+    assert owners == [owner, owner] and calls == [("gk_tables_step", stream)] and eng.torch.cuda.current == current
+    assert slots.shape == (7,) and slots.dtype is torch.int64 and done.shape == (3,) and done.dtype is torch.int32

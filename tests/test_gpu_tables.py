@@ -267,3 +267,23 @@ def test_from_lengths_to_decode():
     assert (l1 - lse).abs().max() < 1e-3 and (o - out.float()).abs().max() < 2e-2
     eng.seq_release(held)
     eng.close()
+
+
+def test_a_step_on_a_side_stream():
+    """What a step on a side stream allocates is not memory that the current stream still uses."""
+    eng = _engine(1 << 18, 1, 0)
+    tables, _ = eng.device_tables(1, 1 << 18, 1 << 18)
+    n = 200000
+    used = torch.empty(n, dtype=torch.int64, device="cuda")
+    side, a = torch.cuda.Stream(), torch.randn(8192, 8192, device="cuda").to(torch.bfloat16)
+    add = ints([n])
+    torch.cuda.synchronize()
+    for _ in range(40):
+        a = a @ a
+    used.fill_(7)
+    del used                                            # free for the current stream, whose fill is still to come
+    slots, done = eng.tables_step(tables, add, n, stream=side)
+    torch.cuda.synchronize()
+    assert eng.device_error() == gk.GK_OK and done.tolist() == [n]
+    assert torch.equal(slots, tables.table[0, :n].long())
+    eng.close()
