@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 import sys
+import threading
 
 import numpy as np
 
@@ -449,9 +450,19 @@ def _gpu_row(x, n, dtype, what):
     return _row_of(x, n, dtype, what)
 
 
+class _Call(threading.local):
+    """The gk_qkv that a thread's calls fill in, a copy of c: the library reads it while other threads may run."""
+
+    def __init__(self, c):
+        self.c = gk_qkv.from_buffer_copy(c)
+        self.ref = ctypes.byref(self.c)
+        self.seen = None
+
+
 class Rope:
     """How the queries and keys of a layer are normed and rotated: cos_sin fp32 [positions, rot_dim] (cosines, then sines),
-    bf16 weights [head_dim] or None (no norm).  Kept by the caller; the tensors stay alive with it."""
+    bf16 weights [head_dim] or None (no norm).  Kept by the caller; the tensors stay alive with it.  Pools of several threads
+    may share one."""
 
     def __init__(self, cos_sin=None, rot_dim=None, interleaved=False, q_weight=None, k_weight=None, eps=1e-6):
         import torch
@@ -473,27 +484,30 @@ class Rope:
             self.dims.add(w.shape[0])
         self.tensors = cos_sin, q_weight, k_weight
         self.rotates = bool(rot_dim)
-        self.c = gk_qkv(0, rot_dim or 0, int(bool(interleaved)), eps, 0 if cos_sin is None else cos_sin.shape[0], _ptr(cos_sin), None,
-                        _ptr(q_weight), _ptr(k_weight))
-        self.ref = ctypes.byref(self.c)
-        self.seen = None
+        self.call = _Call(gk_qkv(0, rot_dim or 0, int(bool(interleaved)), eps, 0 if cos_sin is None else cos_sin.shape[0],
+                                 _ptr(cos_sin), None, _ptr(q_weight), _ptr(k_weight)))
+
+    @property
+    def c(self):
+        return self.call.c
 
     def set(self, pool, positions, q, k, v, q_out, k_out, n):
         """Fill the call's rows in: bf16 [n, heads, d] tensors (tokens may be strided) or addresses of packed rows."""
-        c = self.c
+        call = self.call
+        c = call.c
         # what a layout was found to be when it came last (strides, heads and types: not what the tensors hold or where)
         seen = (_geometry.get(pool), n, _layout(q), _layout(q_out), _layout(k), _layout(k_out), _layout(v), _layout(positions))
-        if seen != self.seen:
-            self.seen = None
-            self._check(pool, positions, q, k, v, q_out, k_out, n)
-            self.seen = seen
+        if seen != call.seen:
+            call.seen = None
+            self._check(c, pool, positions, q, k, v, q_out, k_out, n)
+            call.seen = seen
         c.d_q, c.d_q_out, c.d_k, c.d_k_out, c.d_v = _ptr(q), _ptr(q_out), _ptr(k), _ptr(k_out), _ptr(v)
         if self.rotates:
             c.d_positions = _ptr(positions)
-        return self.ref
+        return call.ref
 
-    def _check(self, pool, positions, q, k, v, q_out, k_out, n):
-        c, torch = self.c, self.torch
+    def _check(self, c, pool, positions, q, k, v, q_out, k_out, n):
+        torch = self.torch
         hq, hkv, dim = _geometry.get(pool, (None, None, None))
         if dim is not None and any(d != dim for d in self.dims):
             raise ValueError(f"the norms' weights are of {self.dims} channels, the pool's heads of {dim}")

@@ -1,6 +1,7 @@
 """4-bit pools and the calls on q, k, v rows without a GPU: sizes, plans and refusals."""
 import ctypes
 import random
+import threading
 
 import numpy as np
 import pytest
@@ -298,3 +299,71 @@ def test_slots_of_tensors(gk, pool):
     with pytest.raises(ValueError, match="copy-on-write"):
         gk.gk_append_qkv(pool, None, 0, rope, None, OnGpu(torch.zeros(7, dtype=torch.int64)), t["q"], t["k"], t["v"],
                          d_cow_pairs=OnGpu(torch.zeros(4, dtype=torch.int64)))
+
+
+class Library:
+    """Stands in for libgk: a call on rows says what it was given once the other thread's call is under way too."""
+
+    def __init__(self, calls):
+        self.together, self.got = threading.Barrier(calls), {}
+
+    def gk_qk_norm_rope(self, pool, stream, ref):
+        self.together.wait(20)
+        c = ref._obj
+        self.got[stream] = {f: getattr(c, f) for f, _ in c._fields_}
+        return 0
+
+    def gk_append_qkv(self, pool, stream, layer, ref, slots, n_cow, cow):
+        return self.gk_qk_norm_rope(pool, stream, ref)
+
+
+@pytest.mark.parametrize("append", [False, True])
+def test_threads_that_share_a_rope(gk, monkeypatch, append):
+    """Two threads, each with a pool and rows of its own, in a call at once: either's rows are its own."""
+    monkeypatch.setattr(gk, "_lib", Library(2))
+    monkeypatch.setattr(gk, "_geometry", {1: (8, 2, 128), 2: (4, 4, 64)})
+    rope = gk.Rope(OnGpu(torch.zeros(100, 64)), None, True)
+    failed = []
+
+    def run(pool, n):
+        try:
+            for _ in range(20):
+                at = [pool * 1000000 + 4096 * i for i in range(7)]
+                if append:
+                    gk.gk_append_qkv(pool, pool, 0, rope, at[0], at[1], at[2], at[3], at[4], at[5], at[6], n=n)
+                else:
+                    gk.gk_qk_norm_rope(pool, pool, rope, at[0], at[2], at[3], at[5], at[6], n=n)
+                got = gk._lib.got[pool]
+                want = dict(num_tokens=n, rot_dim=64, interleaved=1, num_positions=100, d_cos_sin=4096, d_positions=at[0], d_q=at[2],
+                            d_k=at[3], d_v=at[4] if append else None, d_q_out=at[5], d_k_out=at[6])
+                assert {f: got[f] for f in want} == want
+        except Exception as e:
+            failed.append(e)
+    threads = [threading.Thread(target=run, args=x) for x in ((1, 7), (2, 300))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
+
+
+def test_layouts_are_checked_by_each_thread(gk, pool, monkeypatch):
+    """A layout that one thread has seen is another's to check, strides and all."""
+    rope = gk.Rope(OnGpu(torch.zeros(100, 64)))
+    fused = torch.zeros(7, 12 * 128, dtype=torch.bfloat16)
+    q, k, v = (OnGpu(fused[:, a:b].view(7, -1, 128)) for a, b in ((0, 1024), (1024, 1280), (1280, 1536)))
+    rope.set(pool, n=7, **rows(gk, q=q, k=k, v=v))
+    seen = []
+
+    def other():
+        rope.set(pool, n=7, **rows(gk))
+        seen.append((rope.c.num_tokens, rope.c.q_stride))
+        try:
+            rope.set(pool, n=7, **rows(gk, q=bf16(7, 4, 128)))
+        except ValueError:
+            rope.set(pool, n=7, **rows(gk, q=q, k=k, v=v))
+            seen.append((rope.c.num_tokens, rope.c.q_stride, rope.c.rot_dim))
+    t = threading.Thread(target=other)
+    t.start()
+    t.join()
+    assert seen == [(7, 1024), (7, 1536, 64)] and rope.c.q_stride == 1536
