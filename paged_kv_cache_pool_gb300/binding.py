@@ -578,30 +578,47 @@ def gk_read_kv(pool, stream, layer, d_slot_mapping, d_k, d_v, n=None):
         _check(st, pool)
 
 
+def _packed(x, what, hint=""):
+    """Address of x, a contiguous tensor or an address, and what a call that knows its size checks of it (None of an address)."""
+    if x is None or isinstance(x, int):
+        return x, None
+    if not x.is_contiguous():
+        raise ValueError(f"{what} must be contiguous{hint}")
+    return x.data_ptr(), (x.numel(), x.dtype, x.is_cuda)
+
+
+_FUSED = ": queries in the rows of a fused projection need an output of their own (q_out)"
+
+
 class Batch:
-    """Keeps the host arrays of a gk_batch alive; .set_layer() swaps the per-layer device pointers."""
+    """Keeps the host arrays of a gk_batch alive; .set_device() swaps the per-layer device pointers."""
 
     def __init__(self, prefix_hot_base, prefix_len, suffix_len, d_block_table=None, max_blocks=0, d_q=None,
                  d_out=None, d_lse=None):
         self.prefix_hot_base = np.ascontiguousarray(prefix_hot_base, dtype=np.int64)
         self.prefix_len = np.ascontiguousarray(prefix_len, dtype=np.int32)
         self.suffix_len = np.ascontiguousarray(suffix_len, dtype=np.int32)
+        q, self.q = _packed(d_q, "q", _FUSED)
+        lse, self.lse = _packed(d_lse, "lse")
         self.c = gk_batch(len(self.prefix_len), max_blocks, _i64p(self.prefix_hot_base), _i32p(self.prefix_len),
-                          _i32p(self.suffix_len), _ptr(d_block_table), _ptr(d_q), _ptr(d_out), _ptr(d_lse), None, None)
+                          _i32p(self.suffix_len), _ptr(d_block_table), q, _ptr(d_out), lse, None, None)
+        self.ref = ctypes.byref(self.c)
 
     def set_device(self, d_block_table=None, max_blocks=None, d_q=None, d_out=None, d_lse=None, d_new_k=None,
                    d_new_v=None):
         """d_lse, d_new_k and d_new_v are set on every call (None clears them: no LSE
-        output, no fused append); the others keep their value when None."""
+        output, no fused append); the others keep their value when None.  ValueError, with the
+        batch as it was, for a q or lse that is not contiguous."""
+        lse, lse_seen = _packed(d_lse, "lse")
+        if d_q is not None:
+            self.c.d_q, self.q = _packed(d_q, "q", _FUSED)
         if d_block_table is not None:
             self.c.d_block_table = _ptr(d_block_table)
         if max_blocks is not None:
             self.c.max_blocks = max_blocks
-        if d_q is not None:
-            self.c.d_q = _ptr(d_q)
         if d_out is not None:
             self.c.d_out = _ptr(d_out)
-        self.c.d_lse = _ptr(d_lse)
+        self.c.d_lse, self.lse = lse, lse_seen
         self.c.d_new_k = _ptr(d_new_k)
         self.c.d_new_v = _ptr(d_new_v)
         return self
@@ -647,14 +664,21 @@ def gk_decode_cascade(pool, stream, layer, batch, plan):
 
 
 def gk_decode_kv4(pool, stream, layer, batch, plan, d_out):
-    """bf16 out [B, Hq, d] of a decode step over a 4-bit pool (the batch's q, lse and block table; its d_out is not used)."""
+    """bf16 out [B, Hq, d] of a decode step over a 4-bit pool (the batch's q [B, Hq, d], lse and block table; its d_out is not used).
+    All are packed: append_qkv's queries in place, in a fused projection's rows, are not."""
+    n, torch = batch.c.num_requests, sys.modules.get("torch")
+    hq, _, d = _geometry.get(pool, (None, None, None))
     if not isinstance(d_out, int):
-        hq, _, d = _geometry.get(pool, (None, None, None))
-        shape = (batch.c.num_requests, d_out.shape[1] if hq is None else hq, d_out.shape[2] if d is None else d)
-        if d_out.shape != shape or d_out.dtype is not sys.modules["torch"].bfloat16 or not d_out.is_contiguous() or not d_out.is_cuda:
+        shape = (n, d_out.shape[1] if hq is None else hq, d_out.shape[2] if d is None else d)
+        if d_out.shape != shape or d_out.dtype is not torch.bfloat16 or not d_out.is_contiguous() or not d_out.is_cuda:
             raise ValueError("out must be contiguous bf16 [%d, %d, %d] on the GPU" % shape)
         d_out = d_out.data_ptr()
-    st = lib().gk_decode_kv4(pool, _stream(stream), layer, ctypes.byref(batch.c), plan, d_out)
+    if hq is not None:
+        if batch.q is not None and (batch.q[0] < n * hq * d or batch.q[1] is not torch.bfloat16 or not batch.q[2]):
+            raise ValueError(f"q must be bf16 [{n}, {hq}, {d}] on the GPU")
+        if batch.lse is not None and (batch.lse[0] < n * hq or batch.lse[1] is not torch.float32 or not batch.lse[2]):
+            raise ValueError(f"lse must be fp32 [{n}, {hq}] on the GPU")
+    st = (_lib or lib()).gk_decode_kv4(pool, _stream(stream), layer, batch.ref, plan, d_out)
     if st:
         _check(st, pool)
 

@@ -20,6 +20,8 @@ append_qkv stands in append_kv's place where the layer's queries and keys are no
 normed and rotated yet.  With kv_bits=4 the COLD cache holds 4-bit rows; the decode
 step is then append_slots -> append_qkv (or append_kv) -> plan -> decode_kv4, and
 read_kv gives tokens back as bf16, for a HOT prefix or the prompt step behind them.
+Decode reads packed queries: where q is a view of a fused projection, append_qkv is
+given a q_out of its own (in place it serves the prompt step, which takes strides).
 
 Every method is one library call; the work is in libgk.
 """

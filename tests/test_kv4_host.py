@@ -367,3 +367,40 @@ def test_layouts_are_checked_by_each_thread(gk, pool, monkeypatch):
     t.start()
     t.join()
     assert seen == [(7, 1024), (7, 1536, 64)] and rope.c.q_stride == 1536
+
+
+def test_queries_of_a_decode_are_packed(gk, pool, monkeypatch):
+    """Views of a fused projection, which append_qkv rotates in place, are refused where the rows are read as packed ones; so are
+    queries and an lse of too few rows, of another type, or on the host."""
+    fused = OnGpu(torch.zeros(3, 12 * 128, dtype=torch.bfloat16)[:, :1024].view(3, 8, 128))
+    batch = gk.Batch([-1] * 3, [0] * 3, [40] * 3, 4096, 64, 8192, None, 12288)
+    plan = gk.gk_plan_build(pool, batch)
+    with pytest.raises(ValueError, match="q must be contiguous"):
+        batch.set_device(d_q=fused, d_lse=16384)
+    with pytest.raises(ValueError, match="lse must be contiguous"):
+        batch.set_device(d_q=bf16(3, 8, 128), d_lse=OnGpu(torch.zeros(3, 16)[:, ::2]))
+    assert (batch.c.d_q, batch.c.d_lse) == (8192, 12288)
+    with pytest.raises(ValueError, match="q must be contiguous"):
+        gk.Batch([-1] * 3, [0] * 3, [40] * 3, 4096, 64, fused)
+    called = []
+    monkeypatch.setattr(gk, "_lib", type("Lib", (), {"gk_decode_kv4": lambda self, *a: called.append(a) or 0})())
+    out = bf16(3, 8, 128)
+    good = [8192, bf16(3, 8, 128), bf16(4, 8, 128), bf16(3, 1024), OnGpu(fused.x[:, :, :].contiguous()),
+            OnGpu(torch.zeros(1, 12 * 128, dtype=torch.bfloat16)[:, :1024].view(1, 8, 128).expand(1, 8, 128))]
+    for q in good[:-1]:
+        gk.gk_decode_kv4(pool, None, 0, batch.set_device(d_q=q, d_lse=OnGpu(torch.zeros(3, 8))), plan, out)
+    assert len(called) == 5
+    # one request's row is packed however its projection strides
+    one = gk.Batch([-1], [0], [40], 4096, 64).set_device(d_q=good[-1])
+    gk.gk_decode_kv4(pool, None, 0, one, plan, bf16(1, 8, 128))
+    for q in (bf16(2, 8, 128), bf16(3, 8, 64), OnGpu(torch.zeros(3, 8, 128)), torch.zeros(3, 8, 128, dtype=torch.bfloat16)):
+        with pytest.raises(ValueError, match="q must be bf16"):
+            gk.gk_decode_kv4(pool, None, 0, batch.set_device(d_q=q), plan, out)
+    batch.set_device(d_q=8192)
+    for lse in (OnGpu(torch.zeros(2, 8)), OnGpu(torch.zeros(3, 8, dtype=torch.bfloat16)), torch.zeros(3, 8)):
+        with pytest.raises(ValueError, match="lse must be fp32"):
+            gk.gk_decode_kv4(pool, None, 0, batch.set_device(d_lse=lse), plan, out)
+    gk.gk_decode_kv4(pool, None, 0, batch.set_device(), plan, out)
+    assert len(called) == 7
+    monkeypatch.undo()
+    gk.gk_plan_destroy(plan)
