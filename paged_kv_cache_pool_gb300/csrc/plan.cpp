@@ -242,10 +242,12 @@ void partition_kv4(const std::vector<int64_t>& n, int64_t slots, std::vector<int
     total += x;
     most = std::max(most, x);
   }
-  // the least budget that the slots suffice for, to half a stage or 0.4 %, with at most kMostPieces of a request (where a
-  // CTA is one warp an SM has 15 of them, and the join of 2048 states took longer than the gather)
+  // The least budget that the slots suffice for, to half a stage or 0.4 %, with at most kMostPieces of a request: one in what a
+  // CTA has left, the others whole CTAs (where a CTA is one warp an SM has 16 of them, and the join of 2048 states took longer
+  // than the gather).
   int64_t lo = std::max<int64_t>(kMinGatherQuota + kPieceTokens, total / slots);
-  lo = std::max(lo, (most / kMostPieces + kKv4Tokens - 1) / kKv4Tokens * kKv4Tokens + kPieceTokens);
+  const int64_t least = (most + kMostPieces - 2) / (kMostPieces - 1);
+  lo = std::max(lo, (least + kKv4Tokens - 1) / kKv4Tokens * kKv4Tokens + kPieceTokens);
   int64_t hi = lo;
   while (fill_kv4(n, slots, hi, nullptr, nullptr) > slots) hi += std::max<int64_t>(hi / 2, kKv4Tokens);
   while (hi - lo > std::max<int64_t>(kKv4Tokens / 2, hi / 256)) {

@@ -404,3 +404,24 @@ def test_queries_of_a_decode_are_packed(gk, pool, monkeypatch):
     assert len(called) == 7
     monkeypatch.undo()
     gk.gk_plan_destroy(plan)
+
+
+@pytest.mark.parametrize("d,hkv", [(64, 1), (128, 1), (64, 2)])
+def test_pieces_of_a_request_are_at_most_512(gk, d, hkv):
+    """Lengths that leave a remainder, alone and behind requests that fill a part of a CTA."""
+    rnd = random.Random(hkv)
+    p = gk.gk_pool_create_kv4(1, hkv, hkv, d, 64, 1 << 24, 1, 0)
+    try:
+        for n in [33279, 131583, 512 * 64 + 511, 512 * 64 + 1, 511 * 64 + 65, 511 * 96 + 1, 1 << 20, (1 << 22) - 1] + [
+                rnd.randint(20000, 300000) for _ in range(40)]:
+            for ahead in ([], [70], [5] * 31, [rnd.randint(1, 500) for _ in range(rnd.randint(1, 40))]):
+                lens = ahead + [n] + ahead
+                plan = gk.gk_plan_build(p, gk.Batch([-1] * len(lens), [0] * len(lens), lens, None, n))
+                begin, segs = gk.gk_plan_segments(plan)
+                gk.gk_plan_destroy(plan)
+                pieces = np.bincount(segs[:, 0], minlength=len(lens))
+                assert pieces.max() <= 512, (lens, pieces.max())
+                at = segs[segs[:, 0] == len(ahead)]
+                assert at[0, 1] == 0 and at[-1, 2] == n and (at[1:, 1] == at[:-1, 2]).all() and len(begin) - 1 <= 152 * 16
+    finally:
+        gk.gk_pool_destroy(p)
