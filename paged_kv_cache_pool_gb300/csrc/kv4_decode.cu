@@ -91,6 +91,12 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// of two fp16 each, NaN where either is
+__device__ __forceinline__ uint32_t max_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -290,7 +296,9 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
   const uint32_t v_at = kTok * (D / 2) +
                         (D == 128 ? tq * 64 + ((gq >> 1) ^ ((tq >> 1) << 1)) * 16 + (gq & 1) * 8 : tq * 32 + gq * 4);
   const uint32_t first = gq < 4 ? ~0u : 0u;                // paired: of weights, whose column is the first tile's
-  const int head = PAIR ? gq & 3 : gq;                     // of the query's fragments
+  // of the query's fragments; columns without a head repeat another's, so that what a warp finds over all of them (the largest
+  // product of weight and span) is of rows that count
+  const int head = (PAIR ? gq & 3 : gq) % G;
   const int half = PAIR ? tq >> 1 : 0;                     // this thread's tile
   const uint32_t s_at = kTok * D + (ta + 16 * half) * (D / 8);
   int cslot = 0;
@@ -310,8 +318,7 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
 #pragma unroll
       for (int i = 0; i < KW; ++i) {
         const int w = KW * tq + i, ch = D == 128 ? 8 * (w >> 1) + 64 * (w & 1) : 8 * w;   // channels ch .. ch + 7
-        raw[i] = make_uint4(0, 0, 0, 0);
-        if (head < G) raw[i] = *reinterpret_cast<const uint4*>(p.q + ((int64_t)seg.x * p.Hq + h * G + head) * D + ch);
+        raw[i] = *reinterpret_cast<const uint4*>(p.q + ((int64_t)seg.x * p.Hq + h * G + head) * D + ch);
       }
 #pragma unroll
       for (int i = 0; i < KW; ++i) {
@@ -353,10 +360,13 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
     float o[MT][4], R[NG][2] = {}, m[2] = {-INFINITY, -INFINITY}, l[2] = {};
 #pragma unroll
     for (int i = 0; i < MT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    // V's spans, up to the word `most`, are scaled by the power of two vs, to below 2^11: with kSlack the weights that
-    // fp16 holds stay below 2^15, and one below its normal range is off by 2^-35 of the largest span at most
-    float vs = 1.f;
-    int32_t most = -1;                 // not chosen yet
+    // fp16 holds a token's weight times its group's span, scaled by the group's power of two vs: the largest product of the stage that
+    // chose vs is below 2^11, those of later stages below 2^15, or vs is chosen again.  One below fp16's normal range is off by
+    // 2^-35 of that largest product at most.  (The product, not the span: a token of wide values and no weight must not take the
+    // others' bits.)
+    float vs[NG];                      // 0: not chosen yet
+#pragma unroll
+    for (int g = 0; g < NG; ++g) vs[g] = 0.f;
 
     for (int left = seg.z - seg.y; left > 0; left -= kTok) {
       const int n = min(kTok, left);
@@ -454,22 +464,17 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
             }
       }
       // The exponents' reference m is raised only where a score passes it by kSlack (a vote in place of a
-      // maximum over the warp), the scale vs of V's spans lowered only where one passes `most`.
+      // maximum over the warp).
       float d[NS][4];
 #pragma unroll
       for (int u = 0; u < NS; ++u)
 #pragma unroll
         for (int i = 0; i < 4; i += 2)
           f2unpack(fadd2(f2pack(sc[u][i], sc[u][i + 1]), f2pack(-m[0], -m[1])), d[u][i], d[u][i + 1]);
-      // (the span is a word's high half and not negative: words order as their spans)
-      int32_t top = 0;
-#pragma unroll
-      for (int u = 0; u < NS; ++u)
-#pragma unroll
-        for (int g = 0; g < NG; ++g) top = __vimax3_s32(top, (int32_t)vscale[u][0][g], (int32_t)vscale[u][1][g]);
       float past = fmaxf(fmax3(d[0][0], d[0][1], d[0][2]), d[0][3]);
       if (!PAIR) past = fmax3(fmax3(past, d[NS - 1][0], d[NS - 1][1]), d[NS - 1][2], d[NS - 1][3]);
-      if (__any_sync(0xffffffffu, past > kSlack || top > most)) {
+      bool again = false;              // choose vs: weights of before are smaller now, and so may be all that is to come
+      if (__any_sync(0xffffffffu, past > kSlack)) {
         float x0 = fmaxf(fmaxf(sc[0][0], sc[0][2]), fmaxf(sc[NS - 1][0], sc[NS - 1][2]));
         float x1 = fmaxf(fmaxf(sc[0][1], sc[0][3]), fmaxf(sc[NS - 1][1], sc[NS - 1][3]));
 #pragma unroll
@@ -489,20 +494,11 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
           R[g][0] *= a0;
           R[g][1] *= a1;
         }
-        if (__any_sync(0xffffffffu, top > most)) {
-          top = __reduce_max_sync(0xffffffffu, top);
-          const int e = exponent(__uint_as_float((uint32_t)top & 0xffff0000u));
-          const float to = pow2(min(113, 10 - e));
-          if (most >= 0) {
-            a0 *= to / vs;
-            a1 *= to / vs;
-          }
-          vs = to;
-          most = (e + 127) << 23 | 0x007fffff;   // the largest word of a span below 2^(e + 1)
-        }
+        if (vs[0] != 0.f) {
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-          o[i][0] *= a0; o[i][1] *= a1; o[i][2] *= a0; o[i][3] *= a1;
+          for (int i = 0; i < MT; ++i) {
+            o[i][0] *= a0; o[i][1] *= a1; o[i][2] *= a0; o[i][3] *= a1;
+          }
         }
         m[0] = x0;
         m[1] = x1;
@@ -510,41 +506,92 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
         for (int u = 0; u < NS; ++u)
 #pragma unroll
           for (int i = 0; i < 4; ++i) d[u][i] = sc[u][i] - m[i & 1];
+        again = true;
+      }
+      float e[NS][4];                  // rows a and b of the first head, then of the second
+#pragma unroll
+      for (int u = 0; u < NS; ++u) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) e[u][i] = ex2(d[u][i]);
+        l[0] += e[u][0];
+        l[0] += e[u][2];
+        l[1] += e[u][1];
+        l[1] += e[u][3];
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          const float la = bf_lo(vscale[u][0][g]), lb = bf_lo(vscale[u][1][g]);
+          R[g][0] = fmaf(e[u][0], la, R[g][0]);
+          R[g][1] = fmaf(e[u][1], la, R[g][1]);
+          R[g][0] = fmaf(e[u][2], lb, R[g][0]);
+          R[g][1] = fmaf(e[u][3], lb, R[g][1]);
+        }
+      }
+      // products of weight and span, scaled, of rows a and b, both heads a word
+      uint32_t ws[NS][NG][2], high = 0;
+      auto weigh = [&](bool wide) {
+#pragma unroll
+        for (int u = 0; u < NS; ++u)
+#pragma unroll
+          for (int g = 0; g < NG; ++g) {
+            const uint64_t span = f2pack(bf_hi(vscale[u][0][g]), bf_hi(vscale[u][1][g])), by = f2pack(vs[g], vs[g]);
+            const uint64_t e0 = f2pack(e[u][0], e[u][2]), e1 = f2pack(e[u][1], e[u][3]);
+            float a0, b0, a1, b1;
+            f2unpack(wide ? mul2(mul2(e0, span), by) : mul2(e0, mul2(span, by)), a0, b0);
+            f2unpack(wide ? mul2(mul2(e1, span), by) : mul2(e1, mul2(span, by)), a1, b1);
+            ws[u][g][0] = pack_f16x2(a0, a1);
+            ws[u][g][1] = pack_f16x2(b0, b1);
+            high = max_f16x2(max_f16x2(ws[u][g][0], ws[u][g][1]), high);
+          }
+      };
+      if (!again) {
+        weigh(false);
+        // 2^15 (0x7800) and more, infinity and NaN (a span that overflows times its scale, on a weight of 0); not one is negative
+        again = __any_sync(0xffffffffu, ((high + 0x08000800u) & 0x80008000u) != 0);
+      }
+      if (again) {
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          float top = 0.f, held = 0.f;
+#pragma unroll
+          for (int u = 0; u < NS; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top = fmaxf(top, e[u][i] * bf_hi(vscale[u][i >> 1][g]));
+          top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+          int to = min(113, 10 - exponent(top));
+          if (vs[g] != 0.f) {
+            // what O holds, in a new scale too
+            int by = to - exponent(vs[g]);
+            if (by > 0) {
+#pragma unroll
+              for (int i = 4 * g; i < 4 * g + 4; ++i) held = fmaxf(fmaxf(fmaxf(fabsf(o[i][0]), fabsf(o[i][1])), fmaxf(fabsf(o[i][2]), fabsf(o[i][3]))), held);
+              held = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(held)));
+              by = min(by, 96 - exponent(held));
+              to = exponent(vs[g]) + by;
+            }
+            const int half = by / 2;
+            const float f = pow2(half), f2 = pow2(by - half);
+#pragma unroll
+            for (int i = 4 * g; i < 4 * g + 4; ++i)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) o[i][k] = o[i][k] * f * f2;
+          }
+          vs[g] = pow2(to);
+        }
+        weigh(true);
       }
       uint32_t b[2][NG][2];            // P^T times the spans, of either tile
 #pragma unroll
-      for (int u = 0; u < NS; ++u) {
-        float e[4];                    // rows a and b of the first head, then of the second
+      for (int u = 0; u < NS; ++u)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) e[i] = ex2(d[u][i]);
-        l[0] += e[0];
-        l[0] += e[2];
-        l[1] += e[1];
-        l[1] += e[3];
-        const uint64_t vv = f2pack(vs, vs), e0 = f2pack(e[0], e[2]), e1 = f2pack(e[1], e[3]);
+        for (int g = 0; g < NG; ++g)
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          const uint32_t wa = vscale[u][0][g], wb = vscale[u][1][g];
-          const float la = bf_lo(wa), lb = bf_lo(wb);
-          R[g][0] = fmaf(e[0], la, R[g][0]);
-          R[g][1] = fmaf(e[1], la, R[g][1]);
-          R[g][0] = fmaf(e[2], lb, R[g][0]);
-          R[g][1] = fmaf(e[3], lb, R[g][1]);
-          const uint64_t span = mul2(f2pack(bf_hi(wa), bf_hi(wb)), vv);
-          float a0, b0, a1, b1;
-          f2unpack(mul2(e0, span), a0, b0);
-          f2unpack(mul2(e1, span), a1, b1);
-          b[u][g][0] = transpose8x8(pack_f16x2(a0, a1));
-          b[u][g][1] = transpose8x8(pack_f16x2(b0, b1));
-          if (PAIR) {
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
+          for (int k = 0; k < 2; ++k) {
+            b[u][g][k] = transpose8x8(ws[u][g][k]);
+            if (PAIR) {
               b[1][g][k] = b[0][g][k] & ~first;
               b[0][g][k] &= first;
             }
           }
-        }
-      }
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         // tokens tq, tq + 4, tq + 8, tq + 12 of the tile
@@ -590,7 +637,9 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
 #pragma unroll
         for (int k = 0; k < 4; ++k) o[i][k] += __shfl_xor_sync(0xffffffffu, o[i][k], 2);
     }
-    const float back = 1.f / vs;
+    float back[NG];
+#pragma unroll
+    for (int g = 0; g < NG; ++g) back[g] = 1.f / vs[g];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int hh = 2 * tq + k;       // (paired: lanes from tq = 2 on hold what the others do)
@@ -602,8 +651,8 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
         float y[8];                    // channels 64 g + 8 gq .. + 7
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          y[2 * i] = fmaf(o[4 * g + i][k] * f, back, R[g][k] * inv);
-          y[2 * i + 1] = fmaf((o[4 * g + i][2 + k] - o[4 * g + i][k]) * (f * 0.0625f), back, R[g][k] * inv);
+          y[2 * i] = fmaf(o[4 * g + i][k] * f, back[g], R[g][k] * inv);
+          y[2 * i + 1] = fmaf((o[4 * g + i][2 + k] - o[4 * g + i][k]) * (f * 0.0625f), back[g], R[g][k] * inv);
         }
         const int64_t at = row * D + 64 * g + 8 * gq;
         if (dest >= 0) {

@@ -547,3 +547,56 @@ def test_bad_last_block_of_a_request(d, g, page, length):
         K[bad], V[bad], size[bad] = 0, 0, 0
         check_attention(np64(s.out[r]), np64(s.lse[r]), attend(np64(s.q[r]), (none, none), (K[i], V[i], size[i])), f"request {r}")
     s.close()
+
+
+def check_weighted(s, what=""):
+    """Outputs against 64 bits, in the values that carry weight.  As attend() counts them, but for the products of weight and span:
+    those are scaled so that a largest one, over the queries of a KV head, lies between 2^10 and 2^11, and one below fp16's normal
+    range is off by half a step of 2^-24, 2^-35 of it.  Weights are relative to a score that the largest passes by 2^4 at most and
+    that was a row's largest once, so that they add up to 1 or more.  With W = max e^(s_j - max s) (|lo| + span) of a KV head:
+      |O - O*| <= 2^-8 |O*| + (2^-11 + 2^-12) C + n 2^-31 W."""
+    torch.cuda.synchronize()
+    assert s.eng.device_error() == gk.GK_OK
+    K, V, size = values(s.eng.cold[s.layer, s.slots].cpu().numpy(), s.hkv, s.d)
+    at, g = np.cumsum([0] + s.cold), s.hq // s.hkv
+    for r, n in enumerate(s.cold):
+        i = slice(at[r], at[r + 1])
+        for h in range(s.hkv):
+            q, out, lse = (np64(x)[r, h * g:(h + 1) * g] for x in (s.q, s.out, s.lse))
+            z = q @ K[i, h].T / np.sqrt(s.d)
+            m = z.max(1, keepdims=True)
+            p = np.exp(z - m)
+            total = p.sum(1, keepdims=True)
+            assert np.abs(lse - (m + np.log(total))[:, 0]).max() <= 2e-4, f"{what}: lse of request {r}"
+            O, C = p @ V[i, h] / total, p @ size[i, h] / total
+            W = (p[:, :, None] * size[i, h][None]).max()
+            over = np.abs(out - O) - (2.0 ** -8 * np.abs(O) + (2.0 ** -11 + 2.0 ** -12) * C + n * 2.0 ** -31 * W)
+            assert over.max() <= 0, f"{what}: request {r}, KV head {h} off by {over.max():.3g} over its bound"
+
+
+@pytest.mark.parametrize("d,g", [(64, 1), (64, 4), (128, 2), (128, 4), (128, 5), (128, 8)])
+@pytest.mark.parametrize("power,others,query", [(40, 0, 64), (90, 0, 64), (110, -25, 128)])
+def test_wide_values_of_little_weight(d, g, power, others, query):
+    """A token whose values are far larger than the others' and whose weight is far smaller (or 0) takes nothing from the tokens that
+    carry the weight: at the first place, at a stage's ends, at the last, and where it had the weight until larger scores came."""
+    n, places = 200, [0, 31, 32, 100, 199]
+    rng = torch.Generator(device="cuda").manual_seed(power)
+    requests = len(places) + 2
+    k, v = (torch.randn(requests, n, 2, d, generator=rng, device="cuda") for _ in range(2))
+    k *= 0.25
+    k[..., 0] = 0
+    wide = 2.0 ** power                   # times the values' own scale, so that it is a number of fp32
+    for r, t in enumerate(places):
+        k[r, t, :, 0] = -12
+        v[r, t] *= wide
+    k[-2, :32, :, 0] = -12                # a stage of small scores, the wide token among them
+    v[-2, 3] *= wide
+    k[-1, :, :, 0] = torch.linspace(-12, 0, n, device="cuda")[:, None]     # scores that rise all the way
+    v[-1, 3] *= wide
+    v[-1, 70, 1] *= wide
+    v[v.abs() < 2.0 ** 20] *= 2.0 ** others
+    s = Step(d, g, 2, [n] * requests, k=k.flatten(0, 1).to(BF), v=v.flatten(0, 1).to(BF), scale=0.25)
+    s.q[..., 0] = query
+    s.run()
+    check_weighted(s)
+    s.close()
