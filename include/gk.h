@@ -459,8 +459,10 @@ gk_status gk_cascade_merge(gk_pool* pool, void* stream, int32_t layer, const gk_
  * may be NULL, d_new_k and d_new_v must be (GK_ERR_UNSUPPORTED: append first, gk_append_qkv).  Products and sums
  * are held in fp32; the weights are rounded to bf16 over the prefix and to fp16, times the group's span, over COLD,
  * the output to bf16 at the end.  (fp16 holds the products of weight and span scaled by a power of two: one below 2^-24 of the
- * largest in its 64 channels, over the queries that share the KV head, is off by up to 2^-35 of that largest.)  Queries of magnitude up to 2^100 are in
- * range; a row that has a query of infinity or NaN, or attends a key that is held as NaN, comes out NaN, lse
+ * largest in its 64 channels, over the queries that share the KV head, is off by up to 2^-35 of that largest.)
+ * A score over COLD is a part from lo and a part from codes, each in fp32, which may cancel: it is off by up to 2^-18 of
+ * sum_c |q_c| (|lo| + span) / sqrt(d), and lse by as much as the key whose sum is largest.
+ * Queries of magnitude up to 2^100 are in range; a row that has a query of infinity or NaN, or attends a key that is held as NaN, comes out NaN, lse
  * too; channels whose attended values include NaN come out NaN.  A request without a token gives 0 and
  * minus infinity.  An out-of-range block id counts as zero K and V and is reported as GK_ERR_DEVICE_BOUNDS
  * by gk_device_error().  The batch's lengths and HOT bases are the plan's; only its device pointers and

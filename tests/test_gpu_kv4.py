@@ -6,7 +6,7 @@ import random
 import numpy as np
 import pytest
 
-from kv4_ref import attend, check_attention, values
+from kv4_ref import attend, bf16_value, check_attention, fields, values
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -599,4 +599,31 @@ def test_wide_values_of_little_weight(d, g, power, others, query):
     s.q[..., 0] = query
     s.run()
     check_weighted(s)
+    s.close()
+
+
+@pytest.mark.parametrize("d,g", [(64, 4), (128, 2), (128, 4), (128, 5)])
+@pytest.mark.parametrize("scale", [40, 400])
+def test_lse_of_large_scores(d, g, scale):
+    """Scores of hundreds and thousands, whose parts from lo and from codes cancel.  Of the sum S = sum |q| (|lo| + span) / sqrt(d):
+    sum(q) in at most 11 fp32 sums and a product, 12 roundings of 2^-24, three bf16 terms to 2^-27; each tensor-core product adds 8 or 16
+    exact terms and what was there, counted as 2^-21 of their absolute sum, once for the part of lo and at most four times for that
+    of codes; four roundings of 2^-24 scale and add the parts: below 2^-18 S.  lse by as much as the worst key, and 2e-4 as ever."""
+    s = Step(d, g, 2, [300, 70, 1000, 1], scale=scale, seed=scale)
+    s.run()
+    torch.cuda.synchronize()
+    rows = s.eng.cold[1, s.slots].cpu().numpy()
+    K = values(rows, 2, d)[0]
+    lo, span = (np.repeat(np.abs(bf16_value(x).astype(np.float64)), 64, -1)[:, :, 0] for x in fields(rows, 2, d)[1:])
+    at = np.cumsum([0] + s.cold)
+    for r in range(4):
+        i = slice(at[r], at[r + 1])
+        for h in range(2):
+            q = np64(s.q[r, h * g:(h + 1) * g])
+            z = q @ K[i, h].T / np.sqrt(d)
+            m = z.max(1)
+            want = m + np.log(np.exp(z - m[:, None]).sum(1))
+            S = (np.abs(q) @ (lo + span)[i, h].T / np.sqrt(d)).max(1)
+            off = np.abs(np64(s.lse[r, h * g:(h + 1) * g]) - want)
+            assert (off <= 2.0 ** -18 * S + 2e-4).all(), (r, h, off.max(), S.max())
     s.close()
