@@ -17,7 +17,7 @@
 // 2048 tokens took 450 us so and 265 with fp16.)
 //
 // GB300, 4 requests of 262144 tokens, 32/8 heads of 128, pages of 16 (1.2 GB of rows): 210 us, 5.8 TB/s, 85 % of the
-// measured copy rate; the same work on rows that stay in L2 takes 171, so instructions bind it next to HBM, half
+// measured copy rate; the same work on rows that stay in L2 takes 177, so instructions bind it next to HBM, half
 // of the issue slots and of the ALU pipe's (masks, byte permutes, integer tests) busy.
 #include <cmath>
 
@@ -306,7 +306,8 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
     const int4 seg = seg_at(sg);
     const int32_t dest = seg.w >= 0 ? seg.w : ~seg.x;
     // Q as B fragments: the channels of a thread's word i of K, paired (c, c + 4); scaled by a power of two to
-    // between 2^13 and 2^14, so that fp16 holds a head's bf16 values to 2^-38 of the largest
+    // between 2^13 and 2^14, and the odd channels, whose codes come 16 times as large, by 2^-4 of it: fp16 holds a head's bf16
+    // values to half a step of 2^-24, 2^-38 of the largest in the even channels and 2^-34 in the odd ones
     uint32_t qf[KW][4];
     float F[2];
     // sum(q) of each group (times scale) as the B fragment that meets lo: column gq, rows 2 tq and 2 tq + 1 the groups' tq-th
@@ -363,7 +364,7 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
     // fp16 holds a token's weight times its group's span, scaled by the group's power of two vs: the largest product of the stage that
     // chose vs is below 2^11, those of later stages below 2^15, or vs is chosen again.  One below fp16's normal range is off by
     // 2^-35 of that largest product at most.  (The product, not the span: a token of wide values and no weight must not take the
-    // others' bits.)
+    // others' bits.  4 requests of 262144 tokens take 209 us by either, on rows in L2 171 by spans and 177 by products.)
     float vs[NG];                      // 0: not chosen yet
 #pragma unroll
     for (int g = 0; g < NG; ++g) vs[g] = 0.f;
@@ -678,7 +679,7 @@ __global__ void __launch_bounds__(32 * kMaxKvHeads, kSmWarps / kMaxKvHeads) kv4_
 // O = sum_e 2^(l_e - m) O_e / sum_e 2^(l_e - m), LSE = (m + log2 sum_e 2^(l_e - m)) ln 2 over the partial
 // states of a request, m the largest l_e, for each query head.  WARPS warps share a row: each joins the states
 // e = its index + WARPS i, then the first one theirs.  A state of LSE -inf (weight 0) may hold anything.
-// SPLIT blocks share a row's channels (one request of 131072 tokens, 32 rows of 304 states: the step 36.7 us, 35.7 by four).
+// SPLIT blocks share a row's channels (one request of 131072 tokens, 32 rows of 293 states: the step 36.7 us, 35.7 by four).
 // Bound by latency: a warp asks for eight states' rows before it uses any.
 template <int D, int WARPS, int SPLIT = 1>
 __global__ void __launch_bounds__(WARPS > 8 ? 32 * WARPS : 256) kv4_join_kernel(const float* part_o, const float* part_l, const RequestDev* __restrict__ reqs,
@@ -841,7 +842,9 @@ int launch_kv4_join(const LaunchCommon& lc, void* stream, const gk_batch* b, con
   const gk_pool_config& c = *lc.cfg;
   const int64_t rows = (int64_t)pl->B * c.num_q_heads;
   const int most = pl->kv4_most_states;
-  // a warp a row while two rounds hold its states, or while the rows alone fill the SMs
+  // A warp a row while two rounds hold its states, or while the rows alone fill the SMs.  Steps of one request, 32 rows, by 1, 8
+  // and 32 warps a row: 16 states 7.9, 8.0, 7.5 us, 32 10.3, 8.0, 10.1, 64 15.3, 8.6, 10.4, 128 (not by 1) 8.6, 10.2; 16 requests
+  // of 19 61.1, 59.7, 67.3, 8 of 38 40.5, 35.3, 40.1, 4 of 73 23.7 by 8 and 23.3 by 32.
   const int warps = most <= 16 || rows >= 32 * (int64_t)lc.num_sms ? 1 : most <= 64 ? 8 : 32;
   // as many blocks a row as one wave holds (of 32 warps; 128 rows by four, in four waves, cost the step 10 %)
   const int most_split = c.head_dim / 32, sms = lc.num_sms;

@@ -23,7 +23,10 @@ namespace {
 
 constexpr int kWarps = 4;  // warps of a block
 constexpr int kChunk = 7;  // most passes of a warp (5, 12 or 14 a warp: 3 - 10 % slower)
-constexpr int kBlocks = 7;  // of an SM, as registers allow (4-bit rows, 16384 tokens of 32/8 heads of 128: six 66 us, seven 63)
+// Blocks of an SM, as registers allow (72 a thread).  16384 tokens of 32/8 heads of 128, normed, that rotate in halves, in pairs, in
+// halves of 64 channels: into bf16 rows 64, 68, 68 us (by six blocks 68, 71, 70), into 4-bit rows 66, 71, 78 (69, 71, 72: the
+// last form spills 24 bytes a thread under this bound).
+constexpr int kBlocks = 7;
 constexpr int kFewWarps = 64;  // warps of an SM at most
 
 // how channels rotate: not at all, whole heads in halves, neighbouring pairs, a part of the head in halves
@@ -301,7 +304,7 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks) qkv_kernel(const QkvPara
   for (int i = first; i < end; ++i) {
     const int kind = kind_of(i), h = head_of(i, kind);
     const bool mine = h < (kind == 0 ? p.Hq : p.Hkv);
-    // a group a pass, and one more for each pass done: all but the last kChunk - 1 have landed
+    // a group a pass, and one more ahead of each pass: all but the last kChunk - 1 have landed, this pass's rows and the next one's
     asm volatile("cp.async.commit_group;" ::: "memory");
     asm volatile("cp.async.wait_group %0;" ::"n"(kChunk - 1) : "memory");
     uint4 y0 = buf[(i - first) * 64], y1 = buf[(i - first) * 64 + 32];
